@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libflashgmm.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["gmm_kernels.hip", "gmm_assign.hip", "gmm_lists.hip", "gmm_api.hip"]
+SOURCES = ["gmm_kernels.hip", "gmm_assign.hip", "gmm_lists.hip", "gmm_api.hip", "gmm_mx.hip", "gmm_draw.hip",
+           "gmm_rows_api.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -38,7 +39,8 @@ def hipcc() -> str:
 
 
 HEADERS = [os.path.join(CSRC, "gmm_device.h"), os.path.join(CSRC, "gmm_internal.h"),
-           os.path.join(ROOT, "include", "flashgmm.h")]
+           os.path.join(CSRC, "gmm_rows.h"), os.path.join(ROOT, "include", "flashgmm.h"),
+           os.path.join(ROOT, "include", "flashgmm_rows.h")]
 
 
 def _stale(src: str, obj: str) -> bool:

@@ -13,6 +13,7 @@
 
 #include "flashgmm.h"
 #include "gmm_internal.h"
+#include "gmm_rows.h"
 
 // default limit of the soft assignment's own buffers (the selections of all
 // rows and the radix-sort buffer that builds the lists from them)
@@ -173,6 +174,14 @@ gmm_status soft_assign_run(gmm_ctx* ctx, const float* X, int64_t N, int64_t ldx,
                            int64_t* list_offsets, int32_t* list_ids, int64_t ids_capacity, int64_t* nnz);
 
 }  // namespace
+
+void gmm::set_free_error(const char* msg) noexcept {
+  try {
+    g_create_err = msg;
+  } catch (...) {  // no memory for the message: the status alone is returned
+    g_create_err.clear();
+  }
+}
 
 extern "C" {
 

@@ -1,0 +1,187 @@
+"""The row operators without a GPU: the header and the binding agree, every
+refusal comes before the device is touched, and the references that the GPU
+tests use agree with hand-made cases."""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import soft_clustering_amd as sc
+from tests import rows_reference as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, CAPACITY = 1, 6
+P = ctypes.c_void_p(4096)     # aligned, never dereferenced: the call is refused first
+ODD = ctypes.c_void_p(4097)
+
+
+def test_header_binding_and_library_agree():
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "flashgmm_rows.h")).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(gmm_[a-z_]+)\s*\(", src)))
+    assert names == sorted(sc.ROW_EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", sc.LIB_PATH], capture_output=True, text=True).stdout
+    assert set(names) <= set(re.findall(r"\bT (gmm_[a-z_]+)$", out, flags=re.M))
+
+
+def refused(status, text, want=INVALID):
+    assert status == want, status
+    assert text in sc.raw_library().gmm_last_error(None).decode()
+
+
+def test_quantize_refusals():
+    lib = sc.raw_library()
+    good = dict(X=P, type=0, N=4, D=128, ldx=128, codes=P, ldc=64, scales=P, lds=4)
+
+    def q(**kw):
+        a = {**good, **kw}
+        return lib.gmm_mx_quantize(a["X"], a["type"], a["N"], a["D"], a["ldx"], a["codes"], a["ldc"], a["scales"],
+                                   a["lds"], None)
+
+    refused(q(N=-1), "N must be")
+    refused(q(N=(1 << 30) + 1), "N must be")
+    refused(q(D=0), "D must be")
+    refused(q(D=(1 << 20) + 1), "D must be")
+    refused(q(type=3), "element type")
+    refused(q(X=None), "X is NULL")
+    refused(q(X=ODD), "aligned")
+    refused(q(ldx=127), "row stride")
+    refused(q(codes=None), "non-NULL")
+    refused(q(scales=None), "non-NULL")
+    refused(q(codes=ODD), "aligned")
+    refused(q(scales=ODD), "aligned")
+    refused(q(ldc=48), "code stride")
+    refused(q(ldc=72), "code stride")
+    refused(q(D=129, ldx=129), "code stride")
+    refused(q(lds=6), "scale stride")
+    assert q(N=0) == 0
+    refused(lib.gmm_mx_dequantize(None, 64, P, 4, 4, 128, P, 0, 128, None), "non-NULL")
+    refused(lib.gmm_mx_dequantize(P, 64, P, 4, 4, 128, P, 0, 127, None), "row stride")
+    refused(lib.gmm_mx_dequantize(P, 64, P, 4, 4, 128, P, 5, 128, None), "element type")
+    assert lib.gmm_mx_dequantize(P, 64, P, 4, 0, 128, P, 0, 128, None) == 0
+
+
+def test_product_refusals():
+    lib = sc.raw_library()
+    good = dict(A=P, at=3, lda=64, as_=P, ldas=4, M=100, B=P, ldb=64, bs=P, ldbs=4, N=5, D=100, bias=None, C=P, ct=0,
+                ldc=5, ws=None, wb=0)
+
+    def q(**kw):
+        a = {**good, **kw}
+        return lib.gmm_mx_product(a["A"], a["at"], a["lda"], a["as_"], a["ldas"], a["M"], a["B"], a["ldb"], a["bs"],
+                                  a["ldbs"], a["N"], a["D"], a["bias"], a["C"], a["ct"], a["ldc"], a["ws"], a["wb"],
+                                  None)
+
+    refused(q(M=-1), "M must be")
+    refused(q(N=-1), "N must be")
+    refused(q(D=0), "D must be")
+    refused(q(at=4, lda=100), "element type")
+    refused(q(A=None), "non-NULL")
+    refused(q(as_=None), "non-NULL")
+    refused(q(at=0, lda=99), "row stride")
+    refused(q(bs=None), "B: codes")
+    refused(q(ldb=60), "code stride")
+    refused(q(ldbs=5), "scale stride")
+    refused(q(ct=3), "C: unknown")
+    refused(q(C=None), "C is NULL")
+    refused(q(C=ODD), "aligned")
+    refused(q(ldc=4), "row stride")
+    refused(q(bias=ODD), "bias")
+    assert q(M=0) == 0 and q(N=0) == 0
+    need = lib.gmm_mx_product_workspace(0, 100, 5, 100)
+    assert need > 0
+    refused(q(at=0, lda=100), "workspace", CAPACITY)
+    refused(q(at=0, lda=100, ws=P, wb=need - 1), "workspace", CAPACITY)
+    refused(q(at=0, lda=100, ws=ctypes.c_void_p(4100), wb=need), "16-byte aligned")
+    for bad in ((4, 1, 1, 1), (-1, 1, 1, 1), (0, -1, 1, 1), (0, 1, 1, 0)):
+        assert lib.gmm_mx_product_workspace(*bad) == 0
+
+
+def test_draw_refusals():
+    lib = sc.raw_library()
+    good = dict(z=P, type=0, N=4, V=10, ld=10, u=P, ts=None, t=1.0, ks=None, k=0, ps=None, p=1.0, ms=None, m=0.0,
+                ids=P)
+
+    def q(**kw):
+        a = {**good, **kw}
+        return lib.gmm_draw(a["z"], a["type"], a["N"], a["V"], a["ld"], a["u"], a["ts"], a["t"], a["ks"], a["k"],
+                            a["ps"], a["p"], a["ms"], a["m"], a["ids"], None, 0, None)
+
+    refused(q(N=-1), "N must be")
+    refused(q(V=0), "V must be")
+    refused(q(V=(1 << 20) + 1, ld=1 << 21), "V must be")
+    refused(q(type=3), "element type")
+    refused(q(z=None), "logits is NULL")
+    refused(q(ld=9), "row stride")
+    refused(q(t=-0.5), "temperature")
+    refused(q(t=float("nan")), "temperature")
+    refused(q(p=float("nan")), "top_p")
+    refused(q(m=float("nan")), "min_p")
+    refused(q(u=None), "non-NULL")
+    refused(q(ids=None), "non-NULL")
+    refused(q(ids=ODD), "aligned")
+    refused(q(ts=ODD), "aligned")
+    assert q(N=0) == 0
+
+
+def test_binding_refusals_on_cpu_tensors():
+    x = torch.zeros(4, 128)
+    with pytest.raises(ValueError, match="GPU"):
+        sc.mx_quantize(x)
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        sc.mx_quantize(x.double())
+    with pytest.raises(ValueError, match="2-D"):
+        sc.mx_quantize(x[0])
+    with pytest.raises(ValueError, match="GPU"):
+        sc.draw(x, torch.zeros(4))
+    c, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8)
+    rows = sc.MXRows(c, s, 100)
+    assert len(rows) == 4 and len(rows[1:3]) == 2 and rows.nbytes == 4 * 68
+    with pytest.raises(TypeError, match="slice"):
+        rows[0]
+    with pytest.raises(TypeError, match="slice"):
+        rows[::2]
+    with pytest.raises(ValueError, match="4 x 128|N x 128"):
+        sc.MXRows(c, s, 129)
+    with pytest.raises(TypeError, match="uint8"):
+        sc.MXRows(c.int(), s, 128)
+    with pytest.raises(ValueError, match="same rows"):
+        sc.MXRows(c, s[:3], 128)
+    with pytest.raises(ValueError, match="GPU"):
+        sc.mx_product(rows, rows)
+    with pytest.raises(ValueError, match="GPU"):
+        sc.mx_dequantize(rows)
+    with pytest.raises(TypeError, match="MXRows"):
+        sc.mx_product(x, x)
+
+
+def test_reference_quantize_by_hand():
+    x = np.zeros((1, 64))
+    # largest 7: e = 0; each midpoint goes to the even code; 7 saturates at 6
+    x[0, :10] = [7, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -5.5]
+    x[0, 32] = 2.0 ** -140
+    x[0, 33] = -0.0
+    codes, scales = R.quantize(x)
+    v = R.values(codes, scales, 64)[0]
+    assert v[:10].tolist() == [6, 0, 1, 1, 2, 2, 4, 4, 0, -6]
+    assert scales[0].tolist() == [127, 0, 0, 0]
+    assert v[32] == 0 and np.signbit(v[33])
+    x[0, 40] = np.inf
+    codes, scales = R.quantize(x)
+    assert scales[0, 1] == 255 and np.isnan(R.values(codes, scales, 64)[0, 32:]).all()
+
+
+def test_reference_draw_by_hand():
+    z = np.log([4.0, 1.0, 3.0, 2.0])  # weights 1, 1/4, 3/4, 1/2
+    assert [R.draw(z, u) for u in (0.0, 0.39, 0.41, 0.49, 0.51, 0.79, 0.81, 0.999)] == [0, 0, 1, 1, 2, 2, 3, 3]
+    assert np.flatnonzero(R.kept(z, top_k=2)).tolist() == [0, 2]
+    assert np.flatnonzero(R.kept(z, top_p=0.41)).tolist() == [0, 2]
+    assert np.flatnonzero(R.kept(z, top_p=0.0)).tolist() == [0]
+    assert np.flatnonzero(R.kept(z, top_k=3, top_p=0.8)).tolist() == [0, 2, 3]
+    assert np.flatnonzero(R.kept(z, min_p=0.4)).tolist() == [0, 2, 3]
+    assert np.flatnonzero(R.kept(np.zeros(6), top_k=4, top_p=0.5)).tolist() == [0, 1]
+    assert R.draw([0.0, 5.0, 5.0], 0.9, temperature=0.0) == 1
+    assert R.draw([-np.inf] * 3, 0.5) == -1 and R.draw([0.0, np.nan], 0.5) == -1 and R.draw([np.inf, 0], 0.5) == -1
