@@ -10,15 +10,14 @@
 // the borders of the cumulative weights by 1e-7 of the sum, enough to change
 // draws); 2^42 V stays below 2^63 for V <= 2^20.
 //
-// Nothing is sorted.  Rank order is the order of the pairs (logit descending,
-// index ascending), so what top-k and top-p keep is everything up to one such
-// pair, the cut.  It is found by histograms: first over (M - z) / T, 30 wide
-// (weights below exp(-30) round to zero), whose bins give the counts and the
-// weights ranked above; then, inside the bin that holds the cut, over the
-// ordered integer keys of the logits, until a bin is a single key; ties are
-// cut at an index.  The draw itself is in index order: sums of the weights
-// that stay for each wave's part of each tile, a search over those sums, and
-// one wave's search of its part.
+// Rank order is the order of the pairs (logit descending, index ascending),
+// held as one integer, the place: inverted order key of the logit above the
+// index.  What top-k and top-p keep is every element up to one place, the
+// cut.  A histogram over (M - z) / T, 30 wide (weights below exp(-30) round to
+// zero), gives the bin that the cut lies in; only that bin's members, or the
+// few elements up to it, are put in order.  The draw itself is in index
+// order: sums of the weights that stay over parts of the row, a search over
+// those sums, and a search of one part.
 #include "gmm_rows.h"
 
 #include <limits.h>
@@ -30,33 +29,49 @@ typedef unsigned long long u64;
 namespace {
 
 constexpr int kFix = 42;
+constexpr int kIdxBits = 20;  // V <= 2^20
+constexpr u64 kNoCut = ~0ull;  // a place behind every element's
 
 template <int TYPE>
 struct Logit;
 template <>
 struct Logit<kFloat> {
   using T = float;
+  static constexpr int VEC = 4;  // elements of one 16-byte load
 };
 template <>
 struct Logit<kBfloat> {
   using T = __bf16;
+  static constexpr int VEC = 8;
 };
 template <>
 struct Logit<kHalf> {
   using T = _Float16;
+  static constexpr int VEC = 8;
 };
 
-// Integer key whose order is the order of the floats (no NaN; -0 has become
-// +0 when the logits were read).
+// Order key: an integer whose order is the order of the floats (no NaN; -0
+// has become +0 when the logits were read), and back.
 __device__ __forceinline__ unsigned order_key(float z) {
   const unsigned b = __float_as_uint(z);
   return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(unsigned k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ u64 place_of(float z, int idx) { return ((u64)~order_key(z) << kIdxBits) | (unsigned)idx; }
+// place_of(z, idx) > cut, in 32-bit steps
+__device__ __forceinline__ bool behind(float z, int idx, u64 cut) {
+  const unsigned k = order_key(z), ck = ~(unsigned)(cut >> kIdxBits);
+  return k < ck || (k == ck && idx > (int)(cut & ((1u << kIdxBits) - 1)));
+}
+__device__ __forceinline__ float place_value(u64 p) { return key_value(~(unsigned)(p >> kIdxBits)); }
+__device__ __forceinline__ int place_index(u64 p) { return (int)(p & ((1u << kIdxBits) - 1)); }
 
-// round(2^42 2^t) for t <= 0; 0 below -43.  t = n + f with n whole and |f| <=
+// round(2^42 2^t) for t <= 0 (0 below -43, NaN included).  t = n + f with n whole and |f| <=
 // 1/2; 2^f = sum (f ln 2)^i / i! up to i = 11 (the rest is below 2^-46).
 __device__ __forceinline__ u64 fixed_exp2(double t) {
-  if (!(t > -43.0)) return 0;
+  t = fmax(t, -100.0);
   const double n = rint(t);
   const double x = (t - n) * 0.693147180559945309417;
   double p = 1.0 / 39916800.0;
@@ -76,209 +91,486 @@ __device__ __forceinline__ u64 fixed_exp2(double t) {
   return (u64)__double_as_longlong(y) & 0xFFFFFFFFFFFFFull;
 }
 
-__device__ __forceinline__ u64 shfl_up64(u64 v, int d) {
-  const unsigned lo = __shfl_up((unsigned)v, d), hi = __shfl_up((unsigned)(v >> 32), d);
+// Sums over the lanes of a wave on the data-parallel primitives (shifts
+// within rows of 16, then two broadcasts across rows).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 dpp64(u64 v) {  // 0 where there is no source lane
+  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)v, CTRL, ROWS, 0xF, false);
+  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(v >> 32), CTRL, ROWS, 0xF, false);
   return ((u64)hi << 32) | lo;
 }
-__device__ __forceinline__ u64 shfl_xor64(u64 v, int d) {
-  const unsigned lo = __shfl_xor((unsigned)v, d), hi = __shfl_xor((unsigned)(v >> 32), d);
-  return ((u64)hi << 32) | lo;
-}
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += shfl_xor64(v, d);
+__device__ __forceinline__ u64 wave_scan(u64 v) {  // inclusive
+  v += dpp64<0x111, 0xF>(v);
+  v += dpp64<0x112, 0xF>(v);
+  v += dpp64<0x114, 0xF>(v);
+  v += dpp64<0x118, 0xF>(v);
+  v += dpp64<0x142, 0xA>(v);
+  v += dpp64<0x143, 0xC>(v);
   return v;
 }
-__device__ __forceinline__ u64 wave_scan(u64 v, int lane) {  // inclusive
+__device__ __forceinline__ u64 lane_value(u64 v, int lane) {
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, lane);
+  const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), lane);
+  return ((u64)hi << 32) | lo;
+}
+__device__ __forceinline__ u64 wave_sum(u64 v) { return lane_value(wave_scan(v), 63); }
+__device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const u64 o = shfl_up64(v, d);
-    if (lane >= d) v += o;
+  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ u64 wave_min(u64 v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const unsigned lo = __shfl_xor((unsigned)v, d), hi = __shfl_xor((unsigned)(v >> 32), d);
+    const u64 o = ((u64)hi << 32) | lo;
+    v = o < v ? o : v;
   }
   return v;
 }
+// Orders a wave's LDS accesses before its later ones (other lanes' included).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+  __builtin_amdgcn_wave_barrier();
+}
 
-constexpr int NF = 256;  // key ranges in one step of the refinement
-
-// What a row keeps: everything ranked up to (key, idx), with weight >= wmin.
-struct Cut {
-  unsigned key;
-  int idx;
+// What a row's settings amount to once its largest logit is known.
+struct Scale {
+  double M, c;   // largest logit; log2(e) / T
+  float half, bs;  // M / 2; bins per unit of (M - z) / 2, which does not overflow
+  u64 wmin;      // weights below it are cut by min-p
 };
+__device__ __forceinline__ Scale scale_for(float M, float temp, float min_p, int nb) {
+  Scale s;
+  s.M = M;
+  s.c = 1.44269504088896340736 / (double)temp;
+  s.half = 0.5f * M;
+  s.bs = (float)(nb - 1) / (15.f * temp);
+  s.wmin = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1;
+  return s;
+}
+__device__ __forceinline__ u64 weight(const Scale& s, float x) { return fixed_exp2(((double)x - s.M) * s.c); }
+// bins are ordered as the logits are, and the last one has no weight
+template <int NB>
+__device__ __forceinline__ int bin_of(const Scale& s, float x) {
+  return (int)fminf((s.half - 0.5f * x) * s.bs, (float)(NB - 1));
+}
+// The running sum, in units of weight, that the draw has to reach: the first
+// one above u * total, and no more than the total.
+__device__ __forceinline__ u64 draw_target(float u, u64 total) {
+  if (!(u < 1.f)) return total;
+  const u64 t = (u64)floor(fmax((double)u, 0.0) * (double)total);
+  return (t < total - 1 ? t : total - 1) + 1;
+}
+__device__ __forceinline__ u64 mass_target(float top_p, u64 total) {
+  return (u64)fmax(1.0, ceil((double)top_p * (double)total));
+}
 
-template <int NB, int PARTS, int NW, int HELD>
-struct Shared {
-  float4 row[HELD];    // the row's logits
-  u64 hist[NB];        // weights in each bin of (M - z) / T
-  unsigned count[NB];  // elements in each
-  u64 fine[NF];        // weights or elements in each range of keys
-  u64 part[PARTS];
-  u64 wave[NW];
-  unsigned lo, hi;
-  int found;       // bin or slot that a search ended in
-  u64 before;      // sum in front of it
-  u64 inside;      // its own sum
-  int id;
-  unsigned bad[NW];
-  float top[NW];
-};
-
-// One workgroup of THREADS lanes to a row.  TILES > 0: the row (at most
-// TILES * THREADS * 4 logits) is held in LDS as floats, each lane reading
-// back what it wrote; 0: it is read again in every pass.  Element order:
-// idx = (tile * THREADS + tid) * 4 + v.
-template <int TYPE, int THREADS, int TILES, int NB, int PARTS>
-struct Row {
+// ---------------------------------------------------------------------------
+// Short rows, V <= 256 TILES: one wave to a row, 4 TILES logits in each lane's
+// registers (element idx = tile * 256 + 4 lane + v).  Weights are evaluated
+// where they are used, once for the draw and once more for top-p: kept, they
+// would take half of the registers that let 5 waves run on a SIMD.
+template <int TYPE, int TILES>
+struct WaveRow {
   using T = typename Logit<TYPE>::T;
-  static constexpr int NW = THREADS / 64;
-  using SH = Shared<NB, PARTS, NW, TILES ? TILES * THREADS : 1>;
+  static constexpr int PER = 4 * TILES, NB = 256, CAP = 64;
+  struct SH {
+    u64 hist[NB];  // sums of bins, or f of the list's entries
+    u64 list[CAP];
+  };
+
+  SH& sh;
+  const int lane;
+  float x[PER];
+  Scale s;
+
+  __device__ __forceinline__ WaveRow(SH& sh_, const T* z, int V) : sh(sh_), lane(threadIdx.x & 63) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int idx = t * 256 + 4 * lane;
+      if (idx + 4 <= V) {
+        T q[4];
+        __builtin_memcpy(q, z + idx, sizeof q);  // rows may start at any element
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[4 * t + v] = (float)q[v] + 0.f;
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[4 * t + v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
+      }
+    }
+  }
+  // Makes the logits new values to the compiler, which would otherwise compute
+  // all bins, places and weights once, ahead, and spill them.
+  __device__ __forceinline__ void fresh() {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) asm volatile("" : "+v"(x[i]));
+  }
+  __device__ __forceinline__ int index(int i) const { return (i >> 2) * 256 + 4 * lane + (i & 3); }
+
+  // First of the NB sums in hist whose running sum reaches need(total), -1 if
+  // none does; left: what is still missing in front of it.
+  template <class F>
+  __device__ __forceinline__ int search(F&& need, u64& left) {
+    u64 q[NB / 64], own = 0;
+#pragma unroll
+    for (int i = 0; i < NB / 64; ++i) own += q[i] = sh.hist[lane * (NB / 64) + i];
+    const u64 scan = wave_scan(own);
+    const u64 want = need(lane_value(scan, 63));
+    u64 run = scan - own, mine = 0;
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < NB / 64; ++i) {
+      if (run < want && want <= run + q[i]) {
+        at = lane * (NB / 64) + i;
+        mine = want - run;
+      }
+      run += q[i];
+    }
+    const u64 who = __ballot(at >= 0);
+    wave_sync();
+    if (!who) return -1;
+    const int l = __ffsll(who) - 1;
+    left = lane_value(mine, l);
+    return __builtin_amdgcn_readlane(at, l);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < NB / 64; ++i) sh.hist[i * 64 + lane] = 0;
+    wave_sync();
+  }
+
+  // The place, among the members (a bit of mask for each of this lane's
+  // elements), at which the sum of f in rank order reaches need.
+  __device__ __forceinline__ u64 cut_among(unsigned mask, u64 need, bool by_weight) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const u64 who = __ballot((mask >> i) & 1);
+      if ((mask >> i) & 1) {
+        const int at = n + __popcll(who & ((1ull << lane) - 1));
+        if (at < CAP) {
+          sh.list[at] = place_of(x[i], index(i));
+          sh.hist[at] = by_weight ? weight(s, x[i]) : 1;
+        }
+      }
+      n += __popcll(who);
+    }
+    wave_sync();
+    if (n <= CAP) {  // what ranks in front of each member, by comparing all
+      const u64 own = lane < n ? sh.list[lane] : kNoCut;
+      const u64 f = lane < n ? sh.hist[lane] : 0;
+      u64 before = 0;
+      for (int j = 0; j < n; ++j) before += sh.list[j] < own ? sh.hist[j] : 0;
+      const u64 who = __ballot(lane < n && before < need && need <= before + f);
+      wave_sync();
+      return lane_value(own, __ffsll(who) - 1);
+    }
+    // many members: ranges of places, NB at a step
+    u64 lo = kNoCut, hi = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if ((mask >> i) & 1) {
+        const u64 p = place_of(x[i], index(i));
+        lo = p < lo ? p : lo;
+        hi = p > hi ? p : hi;
+      }
+    lo = wave_min(lo);
+    hi = ~wave_min(~hi);
+    for (;;) {
+      int sft = 0;
+      while (((hi - lo) >> sft) >= NB) ++sft;
+      fresh();
+      clear();
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if ((mask >> i) & 1) {
+          const u64 p = place_of(x[i], index(i));
+          if (p >= lo && p <= hi) atomicAdd(&sh.hist[(p - lo) >> sft], by_weight ? weight(s, x[i]) : 1ull);
+        }
+      wave_sync();
+      const u64 want = need;
+      const int b = search([&](u64) { return want; }, need);
+      lo += (u64)(b > 0 ? b : 0) << sft;
+      if (sft == 0) return lo;
+      const u64 end = lo + ((1ull << sft) - 1);
+      hi = end < hi ? end : hi;
+    }
+  }
+
+  __device__ __forceinline__ int draw(float u, float temp, int top_k, float top_p, float min_p, int V) {
+    float top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      bad |= !(x[i] < INFINITY);  // +inf or NaN
+      top = fmaxf(top, x[i]);
+    }
+    const float M = wave_max(top);
+    if (__ballot(bad) || !(M > -INFINITY)) return -1;
+    if (!(temp > 0.f)) {  // the largest logit, lowest index first
+      u64 first = kNoCut;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (x[i] == M) first = (unsigned)index(i);
+      return (int)wave_min(first);
+    }
+    s = scale_for(M, temp, min_p, NB);
+    unsigned in = (1u << (PER - 1) << 1) - 1u;  // the elements that stay
+#pragma unroll 1
+    for (int mass = 0; mass < 2; ++mass) {  // first the cut by rank, then by mass
+      if (mass ? !(top_p < 1.f) : !(top_k >= 1 && top_k < V)) continue;
+      fresh();
+      clear();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int b = bin_of<NB>(s, x[i]);
+        if (((in >> i) & 1) && b < NB - 1) atomicAdd(&sh.hist[b], mass ? weight(s, x[i]) : 1ull);
+      }
+      wave_sync();
+      u64 need = 0;
+      const int b = search([&](u64 total) { return mass ? mass_target(top_p, total) : (u64)top_k; }, need);
+      if (b < 0) continue;  // all that has weight stays
+      fresh();
+      unsigned members = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) members |= (unsigned)(bin_of<NB>(s, x[i]) == b) << i;
+      const u64 cut = cut_among(members & in, need, mass);
+      fresh();
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (behind(x[i], index(i), cut)) in &= ~(1u << i);
+    }
+    fresh();
+    // running sums in index order: tile by tile, lane by lane
+    u64 before[TILES + 1];
+    u64 run[TILES];
+    before[0] = 0;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      u64 own = 0;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) own += stays(4 * t + v, in);
+      const u64 scan = wave_scan(own);
+      run[t] = before[t] + scan - own;
+      before[t + 1] = before[t] + lane_value(scan, 63);
+    }
+    const u64 want = draw_target(u, before[TILES]);
+    // the tile that reaches it, and its four weights again
+    int tile = 0;
+#pragma unroll
+    for (int t = 1; t < TILES; ++t) tile += before[t] < want;
+    u64 r = run[0];
+    float y[4] = {x[0], x[1], x[2], x[3]};
+    unsigned stay = in;
+#pragma unroll
+    for (int t = 1; t < TILES; ++t)
+      if (tile == t) {
+        r = run[t];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] = x[4 * t + v];
+        stay = in >> (4 * t);
+      }
+    int id = INT_MAX;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u64 q = (stay >> v) & 1 ? weight(s, y[v]) : 0;
+      q = q >= s.wmin ? q : 0;
+      if (r < want && want <= r + q) id = tile * 256 + 4 * lane + v;
+      r += q;
+    }
+    const u64 who = __ballot(id != INT_MAX);
+    return __builtin_amdgcn_readlane(id, __ffsll(who) - 1);
+  }
+  __device__ __forceinline__ u64 stays(int i, unsigned in) const {
+    const u64 q = (in >> i) & 1 ? weight(s, x[i]) : 0;
+    return q >= s.wmin ? q : 0;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Longer rows: one workgroup of THREADS lanes to a row.  HELD > 0: the row (at
+// most HELD tiles) is kept in LDS as floats, each lane reading back what it
+// wrote; 0: it is read again in every pass.  A tile is VEC elements a lane,
+// idx = (tile * THREADS + tid) * VEC + v; the 64 VEC elements of a wave in a
+// tile are a part.
+//
+// Passes over the row: the largest logit; a histogram (of counts for top-k, of
+// weights for top-p alone); then either the elements up to the bin of the cut
+// are collected in LDS, put in rank order and cut there (at most CAP of them:
+// nothing else is evaluated), or the parts are summed and the members of the
+// cut's bin collected in the same pass.
+template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+struct BlockRow {
+  using T = typename Logit<TYPE>::T;
+  static constexpr int VEC = Logit<TYPE>::VEC, NW = THREADS / 64, CAP = NB, AHEAD = 16 / VEC;
+  struct SH {
+    float held[HELD ? HELD * THREADS * VEC : 4];
+    u64 hist[NB];  // sums of bins, or the weights of the list's entries
+    u64 list[CAP];
+    u64 part[PARTS];
+    u64 wave[NW];
+    u64 before, lo, hi;
+    int found, count, id;
+    unsigned bad[NW];
+    float top[NW];
+  };
 
   SH& sh;
   const T* z;
-  const int V, ntiles, tid, lane, w;
-  float M;
-  double c;      // log2(e) / T
-  float bscale;  // bins per unit of (M - z) / 2, which does not overflow
+  const int V, ntiles, tid, lane, wv;
+  Scale s;
 
-  __device__ __forceinline__ Row(SH& s, const T* row, int v, int nt)
-      : sh(s), z(row), V(v), ntiles(nt), tid(threadIdx.x), lane(threadIdx.x & 63), w(threadIdx.x >> 6) {}
+  __device__ __forceinline__ BlockRow(SH& sh_, const T* row, int v, int nt)
+      : sh(sh_), z(row), V(v), ntiles(nt), tid(threadIdx.x), lane(threadIdx.x & 63), wv(threadIdx.x >> 6) {}
 
-  // the 4 logits at idx; those past V are -inf
-  __device__ __forceinline__ void load(int idx, float (&x)[4]) const {
-    if (idx + 4 <= V) {
-      T t[4];
-      __builtin_memcpy(t, z + idx, sizeof t);  // rows may start at any element
+  // the logits of this lane in tile t; those past V are -inf
+  __device__ __forceinline__ void load(int t, float (&x)[VEC]) const {
+    const int idx = (t * THREADS + tid) * VEC;
+    if (idx + VEC <= V) {
+      T q[VEC];
+      __builtin_memcpy(q, z + idx, sizeof q);  // rows may start at any element
 #pragma unroll
-      for (int v = 0; v < 4; ++v) x[v] = (float)t[v] + 0.f;
+      for (int v = 0; v < VEC; ++v) x[v] = (float)q[v] + 0.f;
     } else {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) x[v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
+      for (int v = 0; v < VEC; ++v) x[v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
     }
   }
-
-  // this lane's 4 logits of tile t
-  __device__ __forceinline__ void fetch(int t, float (&x)[4]) const {
-    const int i = t * THREADS + tid;
-    if constexpr (TILES > 0) {
-      const float4 q = sh.row[i];
-      x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+  __device__ __forceinline__ void fetch(int t, float (&x)[VEC]) const {
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int v = 0; v < VEC; v += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&sh.held[(t * VEC + v) * THREADS + tid * 4]);
+        x[v] = q.x, x[v + 1] = q.y, x[v + 2] = q.z, x[v + 3] = q.w;
+      }
     } else {
-      load(4 * i, x);
+      load(t, x);
     }
   }
-
-  // f(tile, idx, logit) for this lane's elements, in index order
+  // f(tile, first index, logits) for this lane's tiles, several loads ahead
+  template <class F>
+  __device__ __forceinline__ void tiles(F&& f) const {
+    constexpr int A = HELD > 0 ? 1 : AHEAD;
+    int t = 0;
+    for (; t + A <= ntiles; t += A) {
+      float x[A][VEC];
+#pragma unroll
+      for (int a = 0; a < A; ++a) fetch(t + a, x[a]);
+#pragma unroll
+      for (int a = 0; a < A; ++a) f(t + a, ((t + a) * THREADS + tid) * VEC, x[a]);
+    }
+    for (; t < ntiles; ++t) {
+      float x[VEC];
+      fetch(t, x);
+      f(t, (t * THREADS + tid) * VEC, x);
+    }
+  }
+  // f(idx, logit) for this lane's elements
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
-    for (int t = 0; t < ntiles; ++t) {
-      float x[4];
-      fetch(t, x);
+    tiles([&](int, int idx, float (&x)[VEC]) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) f(t, (t * THREADS + tid) * 4 + v, x[v]);
-    }
+      for (int v = 0; v < VEC; ++v) f(idx + v, x[v]);
+    });
   }
 
-  __device__ __forceinline__ u64 weight(float x) const { return fixed_exp2(((double)x - (double)M) * c); }
-  __device__ __forceinline__ int bin(float x) const { return (int)fminf((0.5f * M - 0.5f * x) * bscale, (float)(NB - 1)); }
-  static __device__ __forceinline__ bool stays(Cut k, unsigned key, int idx) {
-    return key > k.key || (key == k.key && idx <= k.idx);
-  }
-
-  // First of n sums, in order, whose running sum reaches need: sets found,
-  // before and inside for everyone (found = -1 if the total is smaller).
-  // need(total) is asked once the total is known; at(i) is the i-th sum.
+  // First of n sums, in order, whose running sum reaches need(total): sets
+  // found (-1 if the total is smaller) and before for everyone.
   template <class G, class F>
   __device__ __forceinline__ u64 search(int n, G&& at, F&& need) {
     const int per = (n + THREADS - 1) / THREADS;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
     u64 own = 0;
     for (int i = i0; i < i1; ++i) own += at(i);
-    const u64 incl = wave_scan(own, lane);
-    if (lane == 63) sh.wave[w] = incl;
+    const u64 incl = wave_scan(own);
+    if (lane == 63) sh.wave[wv] = incl;
     if (tid == 0) sh.found = -1;
     __syncthreads();
     u64 base = 0, total = 0;
 #pragma unroll
     for (int q = 0; q < NW; ++q) {
-      if (q < w) base += sh.wave[q];
+      if (q < wv) base += sh.wave[q];
       total += sh.wave[q];
     }
     const u64 want = need(total);
-    u64 sum = base + incl - own;
-    if (sum < want && want <= sum + own) {
+    u64 run = base + incl - own;
+    if (run < want && want <= run + own) {
       for (int i = i0; i < i1; ++i) {
-        const u64 x = at(i);
-        if (want <= sum + x) {
+        const u64 q = at(i);
+        if (want <= run + q) {
           sh.found = i;
-          sh.before = sum;
-          sh.inside = x;
+          sh.before = run;
           break;
         }
-        sum += x;
+        run += q;
       }
     }
     __syncthreads();
     return want;
   }
-
-  // The index, in index order, at which the running sum of f(idx, logit)
-  // reaches need(total).
-  template <class F, class G>
-  __device__ __forceinline__ int locate(F&& f, G&& need) {
-    u64 sum = 0;
-    int last = 0;
-    auto flush = [&](int t) {
-      const u64 s = wave_sum(sum);
-      if (lane == 0) sh.part[t * NW + w] = s;
-      sum = 0;
-    };
-    each([&](int t, int idx, float x) {
-      if (t != last) {
-        flush(last);
-        last = t;
-      }
-      sum += f(idx, x);
-    });
-    flush(last);
+  __device__ __forceinline__ u64 block_sum(u64 v) {
+    v = wave_sum(v);
+    if (lane == 0) sh.wave[wv] = v;
     __syncthreads();
-    const u64 want = search(ntiles * NW, [&](int i) { return sh.part[i]; }, need);
-    const int slot = sh.found;
-    if (slot >= 0 && slot % NW == w) {
-      const int t0 = slot / NW;
-      float x[4];
-      fetch(t0, x);
-      const int idx = (t0 * THREADS + tid) * 4;
-      u64 q[4], own = 0;
+    u64 t = 0;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) own += q[v] = f(idx + v, x[v]);
-      u64 run = sh.before + wave_scan(own, lane) - own;
-      if (run < want && want <= run + own) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (run < want && want <= run + q[v]) sh.id = idx + v;
-          run += q[v];
-        }
-      }
-    }
+    for (int q = 0; q < NW; ++q) t += sh.wave[q];
     __syncthreads();
-    return sh.id;
+    return t;
+  }
+  __device__ __forceinline__ void clear() {
+    for (int i = tid; i < NB; i += THREADS) sh.hist[i] = 0;
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+  }
+  // Appends an element to the list (in any order; entries past CAP are only
+  // counted).
+  __device__ __forceinline__ void append(float x, int idx) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < CAP) sh.list[at] = place_of(x, idx);
   }
 
-  // The cut inside bin b of the first histogram, among the elements that the
-  // cut so far keeps: the element at which the sum over the bin's members, in
-  // rank order, of their weights (or of 1 each) reaches need.
-  __device__ __forceinline__ Cut refine(int b, Cut k, u64 need, bool by_weight) {
+  // Sorts the first n <= CAP entries of the list, ascending (bitonic).  Pairs
+  // closer than 128 entries stay within one wave, which needs no barrier.
+  __device__ __forceinline__ void sort_list(int n) {
+    int p = 64;
+    while (p < n) p <<= 1;
+    for (int i = n + tid; i < p; i += THREADS) sh.list[i] = kNoCut;
+    __syncthreads();
+    for (int k = 2; k <= p; k <<= 1)
+      for (int j = k >> 1; j; j >>= 1) {
+        for (int t = tid; t < p / 2; t += THREADS) {
+          const int a = 2 * (t & ~(j - 1)) + (t & (j - 1)), b = a + j;
+          const u64 qa = sh.list[a], qb = sh.list[b];
+          if ((qa > qb) == ((a & k) == 0)) {
+            sh.list[a] = qb;
+            sh.list[b] = qa;
+          }
+        }
+        if (j > 64 || (j == 1 && k >= 128))
+          __syncthreads();
+        else
+          wave_sync();
+      }
+    __syncthreads();
+  }
+
+  // The cut among the members (which(idx, logit)), more than a list holds:
+  // ranges of places, NB at a step.
+  template <class W>
+  __device__ __forceinline__ u64 cut_by_ranges(W&& which, u64 need, bool by_weight) {
     if (tid == 0) {
-      sh.lo = 0xffffffffu;
+      sh.lo = kNoCut;
       sh.hi = 0;
     }
     __syncthreads();
-    unsigned lo = 0xffffffffu, hi = 0;
-    each([&](int, int idx, float x) {
-      const unsigned key = order_key(x);
-      if (x > -INFINITY && bin(x) == b && stays(k, key, idx)) {
-        lo = min(lo, key);
-        hi = max(hi, key);
+    u64 lo = kNoCut, hi = 0;
+    each([&](int idx, float x) {
+      if (which(idx, x)) {
+        const u64 p = place_of(x, idx);
+        lo = p < lo ? p : lo;
+        hi = p > hi ? p : hi;
       }
     });
     if (lo <= hi) {
@@ -289,59 +581,88 @@ struct Row {
     lo = sh.lo;
     hi = sh.hi;
     for (;;) {
-      // the smallest shift that leaves fewer than NF bins
-      const unsigned range = hi - lo;
-      int s = 0;
-      while ((range >> s) >= (unsigned)NF) ++s;
-      for (int i = tid; i < NF; i += THREADS) sh.fine[i] = 0;
-      __syncthreads();
-      each([&](int, int idx, float x) {
-        const unsigned key = order_key(x);
-        if (key >= lo && key <= hi && stays(k, key, idx))
-          atomicAdd(&sh.fine[(hi - key) >> s], by_weight ? weight(x) : 1ull);
+      int sft = 0;
+      while (((hi - lo) >> sft) >= (u64)NB) ++sft;
+      clear();
+      each([&](int idx, float x) {
+        const u64 p = place_of(x, idx);
+        if (p >= lo && p <= hi && which(idx, x)) atomicAdd(&sh.hist[(p - lo) >> sft], by_weight ? weight(s, x) : 1ull);
       });
       __syncthreads();
-      search(NF, [&](int i) { return sh.fine[i]; }, [&](u64) { return need; });
-      const int sb = max(sh.found, 0);
+      search(NB, [&](int i) { return sh.hist[i]; }, [&](u64) { return need; });
       need -= sh.before;
-      hi -= (unsigned)sb << s;
-      if (s == 0) break;
-      lo = max(lo, hi - min(hi, (1u << s) - 1u));
+      lo += (u64)max(sh.found, 0) << sft;
+      __syncthreads();
+      if (sft == 0) return lo;
+      const u64 end = lo + ((1ull << sft) - 1);
+      hi = end < hi ? end : hi;
+    }
+  }
+
+  // Weights of the first n entries of the (sorted) list, into hist.
+  __device__ __forceinline__ void list_weights(int n) {
+    for (int i = tid; i < n; i += THREADS) sh.hist[i] = weight(s, place_value(sh.list[i]));
+    __syncthreads();
+  }
+
+  // The draw from the n <= CAP collected elements, which hold all that can
+  // stay: in rank order for the cuts, then in index order.
+  __device__ __forceinline__ int draw_from_list(int n, float u, int top_k, float top_p) {
+    sort_list(n);
+    list_weights(n);
+    int r = min(n, top_k);
+    if (top_p < 1.f) {
+      u64 sum = 0;
+      for (int i = tid; i < r; i += THREADS) sum += sh.hist[i];
+      sum = block_sum(sum);
+      search(r, [&](int i) { return sh.hist[i]; }, [&](u64) { return mass_target(top_p, sum); });
+      r = sh.found + 1;
       __syncthreads();
     }
-    // ties at key hi: as many as it takes, the first ones by index
-    const u64 one = by_weight ? weight(__uint_as_float(hi & 0x80000000u ? hi ^ 0x80000000u : ~hi)) : 1;
-    const u64 all = sh.inside;
-    __syncthreads();
-    Cut out{hi, hi == k.key ? k.idx : INT_MAX};
-    if (need + one <= all) {  // not all of them
-      const u64 take = (need + one - 1) / one;
-      out.idx = locate([&](int idx, float x) -> u64 { return order_key(x) == hi && stays(k, hi, idx); },
-                       [&](u64) { return take; });
+    // by index; what min-p cuts has no weight
+    for (int i = tid; i < r; i += THREADS) {
+      const u64 p = sh.list[i];
+      sh.list[i] = ((u64)place_index(p) << 32) | order_key(place_value(p));
     }
-    return out;
+    __syncthreads();
+    sort_list(r);
+    for (int i = tid; i < r; i += THREADS) {
+      const u64 q = weight(s, key_value((unsigned)sh.list[i]));
+      sh.hist[i] = q >= s.wmin ? q : 0;
+    }
+    __syncthreads();
+    search(r, [&](int i) { return sh.hist[i]; }, [&](u64 total) { return draw_target(u, total); });
+    const int id = (int)(sh.list[max(sh.found, 0)] >> 32);
+    __syncthreads();
+    return id;
   }
 
   __device__ __forceinline__ int draw(float u, float temp, int top_k, float top_p, float min_p) {
-    if constexpr (TILES > 0) {
-      for (int t = 0; t < ntiles; ++t) {
-        float x[4];
-        load((t * THREADS + tid) * 4, x);
-        sh.row[t * THREADS + tid] = make_float4(x[0], x[1], x[2], x[3]);
-      }
-    }
     float top = -INFINITY;
     bool bad = false;
-    each([&](int, int, float x) {
+    auto look = [&](float x) {
       bad |= !(x < INFINITY);  // +inf or NaN
       top = fmaxf(top, x);
-    });
+    };
+    if constexpr (HELD > 0) {
+      for (int t = 0; t < ntiles; ++t) {
+        float x[VEC];
+        load(t, x);
 #pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+        for (int v = 0; v < VEC; v += 4)
+          *reinterpret_cast<float4*>(&sh.held[(t * VEC + v) * THREADS + tid * 4]) =
+              make_float4(x[v], x[v + 1], x[v + 2], x[v + 3]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) look(x[v]);
+      }
+    } else {
+      each([&](int, float x) { look(x); });
+    }
+    top = wave_max(top);
     const unsigned any = __ballot(bad) != 0;
     if (lane == 0) {
-      sh.top[w] = top;
-      sh.bad[w] = any;
+      sh.top[wv] = top;
+      sh.bad[wv] = any;
     }
     __syncthreads();
     unsigned fault = 0;
@@ -350,100 +671,196 @@ struct Row {
       top = fmaxf(top, sh.top[q]);
       fault |= sh.bad[q];
     }
-    M = top;
+    const float M = top;
     if (fault || !(M > -INFINITY)) return -1;
-    if (!(temp > 0.f))  // the largest logit
-      return locate([&](int, float x) -> u64 { return x == M; }, [](u64) -> u64 { return 1; });
-    c = 1.44269504088896340736 / (double)temp;
-    bscale = (float)(NB - 1) / (15.f * temp);
-    const u64 wmin = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1;
-    Cut cut{0, INT_MAX};  // keeps everything
-    const bool by_rank = top_k >= 1 && top_k < V, by_mass = top_p < 1.f;
-    if (by_rank || by_mass) {
-      for (int i = tid; i < NB; i += THREADS) {
-        sh.hist[i] = 0;
-        sh.count[i] = 0;
-      }
+    if (!(temp > 0.f)) {  // the largest logit, lowest index first
+      if (tid == 0) sh.id = INT_MAX;
       __syncthreads();
-      each([&](int, int, float x) {
-        const int b = bin(x);
-        if (b < NB - 1) {  // the last bin has no weight
-          if (by_rank) atomicAdd(&sh.count[b], 1u);
-          if (by_mass) atomicAdd(&sh.hist[b], weight(x));
-        }
+      int first = INT_MAX;
+      each([&](int idx, float x) {
+        if (x == M) first = min(first, idx);
+      });
+      if (first != INT_MAX) atomicMin(&sh.id, first);
+      __syncthreads();
+      return sh.id;
+    }
+    s = scale_for(M, temp, min_p, NB);
+    u64 cut = kNoCut;  // what ranks behind it is out
+    int b = NB;        // a bin whose members up to need stay: the cut is there
+    u64 need = 0;
+    bool by_weight = false;
+    if (top_k >= 1 && top_k < V) {
+      clear();
+      each([&](int, float x) {
+        const int q = bin_of<NB>(s, x);
+        if (q < NB - 1) atomicAdd(&sh.hist[q], 1ull);
       });
       __syncthreads();
-      int kbin = -1;  // bin of the cut by rank; none if all that has weight stays
-      for (int mass = 0; mass < 2; ++mass) {
-        int b;
-        u64 need;
-        if (!mass) {
-          if (!by_rank) continue;
-          search(NB, [&](int i) { return (u64)sh.count[i]; }, [&](u64) { return (u64)top_k; });
-          b = kbin = sh.found;
-          need = (u64)top_k - sh.before;
+      search(NB, [&](int i) { return sh.hist[i]; }, [&](u64) { return (u64)top_k; });
+      const int kbin = sh.found;
+      if (kbin >= 0) {  // otherwise all that has weight stays
+        need = (u64)top_k - sh.before;
+        const u64 n = sh.before + sh.hist[kbin];
+        const u64 own = sh.hist[kbin];
+        __syncthreads();
+        if (n <= CAP) {
+          clear();
+          each([&](int idx, float x) {
+            if (bin_of<NB>(s, x) <= kbin) append(x, idx);
+          });
           __syncthreads();
-          if (kbin < 0) continue;
+          return draw_from_list((int)n, u, top_k, top_p);
+        }
+        if (top_p < 1.f) {  // the cut by rank has to be known before the sum
+          auto member = [&](int, float x) { return bin_of<NB>(s, x) == kbin; };
+          cut = members_cut(member, need, false, own <= CAP);
         } else {
-          if (!by_mass) break;
-          // the sum over what the cut by rank keeps: the bins in front of its
-          // own, and the members of that bin up to the cut
-          u64 above = 0, inside = 0;
-          for (int i = tid; i < NB; i += THREADS)
-            if (kbin < 0 || i < kbin) above += sh.hist[i];
-          above = block_sum(above);
-          if (kbin >= 0) {
-            each([&](int, int idx, float x) {
-              if (bin(x) == kbin && stays(cut, order_key(x), idx)) inside += weight(x);
-            });
-            inside = block_sum(inside);
-          }
-          const u64 want = (u64)fmax(1.0, ceil((double)top_p * (double)(above + inside)));
-          if (want > above) {
-            b = kbin;
-            need = want - above;
-          } else {
-            search(NB, [&](int i) { return sh.hist[i]; }, [&](u64) { return want; });
-            b = sh.found;
-            need = want - sh.before;
-            __syncthreads();
+          b = kbin;
+        }
+      }
+      __syncthreads();
+    }
+    if (top_p < 1.f) {
+      clear();
+      each([&](int idx, float x) {
+        const int q = bin_of<NB>(s, x);
+        if (q < NB - 1 && (cut == kNoCut || place_of(x, idx) <= cut)) atomicAdd(&sh.hist[q], weight(s, x));
+      });
+      __syncthreads();
+      const u64 want = search(NB, [&](int i) { return sh.hist[i]; }, [&](u64 total) { return mass_target(top_p, total); });
+      b = sh.found;
+      need = want - sh.before;
+      by_weight = true;
+      __syncthreads();
+    }
+    // sums of the parts; members of bin b are collected instead of summed
+    const u64 kcut = cut;
+    auto inside = [&](int idx, float x) {  // stays, apart from the members of b
+      return kcut == kNoCut || place_of(x, idx) <= kcut;
+    };
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    tiles([&](int t, int idx, float (&x)[VEC]) {
+      u64 sum = 0;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (!(x[v] > -INFINITY)) continue;
+        if (b < NB || kcut != kNoCut) {
+          const int q = bin_of<NB>(s, x[v]);
+          if (q > b || !inside(idx + v, x[v])) continue;
+          if (q == b) {
+            append(x[v], idx + v);
+            continue;
           }
         }
-        cut = refine(b, cut, need, mass);
+        const u64 q = weight(s, x[v]);
+        sum += q >= s.wmin ? q : 0;
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) sh.part[t * NW + wv] = sum;
+    });
+    __syncthreads();
+    if (b < NB) {
+      const int n = sh.count;
+      __syncthreads();
+      if (n <= CAP) {
+        cut = list_cut(n, need, by_weight);
+        for (int i = tid; i < n; i += THREADS) {
+          const u64 p = sh.list[i];
+          if (p > cut) continue;
+          const u64 q = weight(s, place_value(p));
+          if (q < s.wmin) continue;
+          const int vec = place_index(p) / VEC;
+          atomicAdd(&sh.part[vec / 64], q);  // lanes are numbered through the row
+        }
+      } else {
+        cut = cut_by_ranges([&](int idx, float x) { return bin_of<NB>(s, x) == b && inside(idx, x); }, need, by_weight);
+        const u64 c = cut;
+        tiles([&](int t, int idx, float (&x)[VEC]) {
+          u64 sum = 0;
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (bin_of<NB>(s, x[v]) == b && place_of(x[v], idx + v) <= c) {
+              const u64 q = weight(s, x[v]);
+              sum += q >= s.wmin ? q : 0;
+            }
+          sum = wave_sum(sum);
+          if (lane == 0) sh.part[t * NW + wv] += sum;
+        });
+      }
+      __syncthreads();
+    }
+    const u64 want = search(ntiles * NW, [&](int i) { return sh.part[i]; },
+                            [&](u64 total) { return draw_target(u, total); });
+    const int slot = sh.found;
+    if (slot >= 0 && slot % NW == wv) {
+      float x[VEC];
+      fetch(slot / NW, x);
+      const int idx = (slot / NW * THREADS + tid) * VEC;
+      u64 q[VEC], own = 0;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        q[v] = 0;
+        if (x[v] > -INFINITY && place_of(x[v], idx + v) <= cut) q[v] = weight(s, x[v]);
+        if (q[v] < s.wmin) q[v] = 0;
+        own += q[v];
+      }
+      u64 run = sh.before + wave_scan(own) - own;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (run < want && want <= run + q[v]) sh.id = idx + v;
+        run += q[v];
       }
     }
-    return locate(
-        [&](int idx, float x) -> u64 {
-          if (!(x > -INFINITY) || !stays(cut, order_key(x), idx)) return 0;
-          const u64 q = weight(x);
-          return q >= wmin ? q : 0;
-        },
-        [&](u64 total) -> u64 {
-          // the first running sum above u * total; the last one at the most
-          if (!(u < 1.f)) return total;
-          const double t = floor(fmax((double)u, 0.0) * (double)total);
-          return min((u64)t, total - 1) + 1;
-        });
+    __syncthreads();
+    return sh.id;
   }
 
-  __device__ __forceinline__ u64 block_sum(u64 v) {
-    v = wave_sum(v);
+  // The place, in the list of n <= CAP members, at which the sum in rank order
+  // reaches need; leaves the list sorted.
+  __device__ __forceinline__ u64 list_cut(int n, u64 need, bool by_weight) {
+    sort_list(n);
+    if (!by_weight) return sh.list[need - 1];
+    list_weights(n);
+    search(n, [&](int i) { return sh.hist[i]; }, [&](u64) { return need; });
+    const u64 c = sh.list[max(sh.found, 0)];
     __syncthreads();
-    if (lane == 0) sh.wave[w] = v;
+    return c;
+  }
+  template <class W>
+  __device__ __forceinline__ u64 members_cut(W&& which, u64 need, bool by_weight, bool fits) {
+    if (!fits) return cut_by_ranges(which, need, by_weight);
+    if (tid == 0) sh.count = 0;
     __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int q = 0; q < NW; ++q) t += sh.wave[q];
+    each([&](int idx, float x) {
+      if (which(idx, x)) append(x, idx);
+    });
     __syncthreads();
-    return t;
+    const int n = sh.count;
+    __syncthreads();
+    return list_cut(n, need, by_weight);
   }
 };
 
 }  // namespace
 
-template <int TYPE, int THREADS, int TILES, int NB, int PARTS>
-__global__ void __launch_bounds__(THREADS) k_draw(DrawArgs a, int ntiles) {
-  using R = Row<TYPE, THREADS, TILES, NB, PARTS>;
+template <int TYPE, int TILES>
+__global__ void __launch_bounds__(64, 4) k_draw_wave(DrawArgs a) {
+  using R = WaveRow<TYPE, TILES>;
+  __shared__ typename R::SH sh;
+  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+    R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+    const int id = row.draw(a.u[n], a.temperatures ? a.temperatures[n] : a.temperature,
+                            a.top_ks ? a.top_ks[n] : a.top_k, a.top_ps ? a.top_ps[n] : a.top_p,
+                            a.min_ps ? a.min_ps[n] : a.min_p, a.V);
+    if (threadIdx.x == 0) a.ids[n] = id;
+    wave_sync();
+  }
+}
+
+template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+__global__ void __launch_bounds__(THREADS) k_draw_block(DrawArgs a, int ntiles) {
+  using R = BlockRow<TYPE, THREADS, HELD, NB, PARTS>;
   __shared__ typename R::SH sh;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
     R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V, ntiles);
@@ -457,20 +874,27 @@ __global__ void __launch_bounds__(THREADS) k_draw(DrawArgs a, int ntiles) {
 
 size_t draw_workspace(int64_t, int) { return 0; }
 
-template <int TYPE, int THREADS, int TILES, int NB, int PARTS>
-static void rows(const DrawArgs& a, hipStream_t s) {
-  const int ntiles = (a.V + THREADS * 4 - 1) / (THREADS * 4);
+template <int TYPE, int TILES>
+static void wave_rows(const DrawArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)(a.N < (1 << 20) ? a.N : (1 << 20));
-  hipLaunchKernelGGL((k_draw<TYPE, THREADS, TILES, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a, ntiles);
+  hipLaunchKernelGGL((k_draw_wave<TYPE, TILES>), dim3(grid), dim3(64), 0, s, a);
+}
+template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+static void block_rows(const DrawArgs& a, hipStream_t s) {
+  constexpr int tile = THREADS * Logit<TYPE>::VEC;
+  const unsigned grid = (unsigned)(a.N < (1 << 20) ? a.N : (1 << 20));
+  hipLaunchKernelGGL((k_draw_block<TYPE, THREADS, HELD, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a,
+                     (a.V + tile - 1) / tile);
 }
 
 template <int TYPE>
 static void draw_type(const DrawArgs& a, hipStream_t s) {
-  if (a.V <= 256) return rows<TYPE, 64, 1, 256, 1>(a, s);
-  if (a.V <= 1024) return rows<TYPE, 64, 4, 256, 4>(a, s);
-  if (a.V <= 4096) return rows<TYPE, 256, 4, 1024, 16>(a, s);
-  if (a.V <= 16384) return rows<TYPE, 1024, 4, 2048, 64>(a, s);
-  return rows<TYPE, 1024, 0, 2048, 4096>(a, s);
+  constexpr int VEC = Logit<TYPE>::VEC;
+  if (a.V <= 256) return wave_rows<TYPE, 1>(a, s);
+  if (a.V <= 1024) return wave_rows<TYPE, 4>(a, s);
+  if (a.V <= 4096) return block_rows<TYPE, 256, 16 / VEC, 1024, 16>(a, s);
+  if (a.V <= 16384) return block_rows<TYPE, 1024, 16 / VEC, 2048, 64>(a, s);
+  return block_rows<TYPE, 1024, 0, 2048, 16384 / VEC>(a, s);
 }
 
 hipError_t launch_draw(const DrawArgs& a, void*, hipStream_t s) {

@@ -41,33 +41,42 @@ def _declare():
 _declare()
 
 
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the hipStream_t of a device's current stream
+
+
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream; raises on a status."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream)
+    index = device.index
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream)
+            st = fn(*args, _raw_stream(index))
     if st != GMM_OK:
         raise GMMError(st, _lib.gmm_last_error(None).decode())
 
 
 def _rows(t, name):
-    """(N, width, row stride) of a 2-D tensor of a supported type."""
+    """(type, N, width, row stride) of a 2-D tensor of a supported type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    N, D = t.shape
+    ld, one = t.stride()
+    if one != 1 and D > 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride(1) == 1)")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows must not overlap (stride(0) >= {t.shape[1]})")
-    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+    if ld < D:
+        if N > 1:
+            raise ValueError(f"{name}'s rows must not overlap (stride(0) >= {D})")
+        ld = D
+    return code, N, D, ld
 
 
 def _out(out, shape, dtype, device, name="out"):
@@ -75,8 +84,8 @@ def _out(out, shape, dtype, device, name="out"):
         return torch.empty(shape, dtype=dtype, device=device)
     if out.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {out.dtype}")
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    if out.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(out.shape)}")
     if out.device != device:
         raise ValueError(f"{name} must be on {device}, got {out.device}")
     return out
@@ -120,30 +129,41 @@ class MXRows:
     def nbytes(self):
         return self.codes.numel() + self.scales.numel()
 
+    @staticmethod
+    def _empty(N, D, device):
+        """Rows to be written (nothing to check)."""
+        G = -(-D // 128)
+        rows = object.__new__(MXRows)
+        rows.codes = torch.empty((N, 64 * G), dtype=torch.uint8, device=device)
+        rows.scales = torch.empty((N, 4 * G), dtype=torch.uint8, device=device)
+        rows.dim = D
+        return rows
+
     def _args(self):
         c, s = self.codes, self.scales
-        return (c.data_ptr(), max(c.stride(0), c.shape[1]) if c.shape[0] > 1 else c.shape[1], s.data_ptr(),
-                max(s.stride(0), s.shape[1]) if s.shape[0] > 1 else s.shape[1])
+        N, wc = c.shape
+        if N > 1:
+            return c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0)
+        return c.data_ptr(), wc, s.data_ptr(), wc // 16
 
 
 def _mx(t, name):
     if not isinstance(t, MXRows):
         raise TypeError(f"{name} must be MXRows")
-    if t.device.type != "cuda":
+    if not t.codes.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
     return t
 
 
 def mx_quantize(X: torch.Tensor, out: MXRows | None = None) -> MXRows:
     """The rows of X (float32, bfloat16 or float16) in 4 bits."""
-    N, D, ld = _rows(X, "X")
+    code, N, D, ld = _rows(X, "X")
+    device = X.device
     if out is None:
-        G = -(-D // 128)
-        out = MXRows(torch.empty(N, 64 * G, dtype=torch.uint8, device=X.device),
-                     torch.empty(N, 4 * G, dtype=torch.uint8, device=X.device), D)
-    elif len(_mx(out, "out")) != N or out.dim != D or out.device != X.device:
-        raise ValueError(f"out must hold {N} rows of {D} values on {X.device}")
-    _call(X.device, _lib.gmm_mx_quantize, X.data_ptr(), _TYPES[X.dtype], N, D, ld, *out._args())
+        out = MXRows._empty(N, D, device)
+    elif len(_mx(out, "out")) != N or out.dim != D or out.device != device:
+        raise ValueError(f"out must hold {N} rows of {D} values on {device}")
+    _call(device, _lib.gmm_mx_quantize, X.data_ptr(), code, N, D, ld, *out._args())
     return out
 
 
@@ -153,9 +173,10 @@ def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.T
     _mx(rows, "rows")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    X = _out(out, (len(rows), rows.dim), dtype, rows.device)
-    N, D, ld = _rows(X, "out")
-    _call(rows.device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), _TYPES[dtype], ld)
+    device = rows.device
+    X = _out(out, (len(rows), rows.dim), dtype, device)
+    code, N, D, ld = _rows(X, "out")
+    _call(device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), code, ld)
     return X
 
 
@@ -166,29 +187,30 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
     _mx(B, "B")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    device = B.device
     if isinstance(A, MXRows):
         M, D = len(A), A.dim
         a_type, (a, lda, a_scales, ldas) = TYPE_MX, A._args()
     else:
-        M, D, lda = _rows(A, "A")
-        a_type, a, a_scales, ldas = _TYPES[A.dtype], A.data_ptr(), None, 0
+        a_type, M, D, lda = _rows(A, "A")
+        a, a_scales, ldas = A.data_ptr(), None, 0
     if D != B.dim:
         raise ValueError(f"A has rows of {D} values, B of {B.dim}")
-    if A.device != B.device:
-        raise ValueError(f"A is on {A.device}, B on {B.device}")
+    if A.device != device:
+        raise ValueError(f"A is on {A.device}, B on {device}")
     N = len(B)
     if bias is not None:
         if not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32:
             raise TypeError("bias must be a float32 tensor")
-        if tuple(bias.shape) != (N,) or bias.device != B.device or not bias.is_contiguous():
-            raise ValueError(f"bias must be {N} contiguous values on {B.device}")
-    C = _out(out, (M, N), dtype, B.device)
-    _, _, ldc = _rows(C, "out")
+        if bias.shape != (N,) or bias.device != device or not bias.is_contiguous():
+            raise ValueError(f"bias must be {N} contiguous values on {device}")
+    C = _out(out, (M, N), dtype, device)
+    c_type, _, _, ldc = _rows(C, "out")
     need = _lib.gmm_mx_product_workspace(a_type, M, N, D)
     # the workspace belongs to this call: torch's allocator hands it on in stream order
-    ws = torch.empty(need, dtype=torch.uint8, device=B.device) if need else None
-    _call(B.device, _lib.gmm_mx_product, a, a_type, lda, a_scales, ldas, M, *B._args(), N, D,
-          None if bias is None else bias.data_ptr(), C.data_ptr(), _TYPES[dtype], ldc,
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _call(device, _lib.gmm_mx_product, a, a_type, lda, a_scales, ldas, M, *B._args(), N, D,
+          None if bias is None else bias.data_ptr(), C.data_ptr(), c_type, ldc,
           None if ws is None else ws.data_ptr(), need)
     return C
 
@@ -199,7 +221,7 @@ def _setting(value, dtype, N, device, name):
         return None, value
     if value.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {value.dtype}")
-    if tuple(value.shape) != (N,) or value.device != device or not value.is_contiguous():
+    if value.shape != (N,) or value.device != device or not value.is_contiguous():
         raise ValueError(f"{name} must be one value or {N} contiguous values on {device}")
     return value.data_ptr(), 0
 
@@ -212,11 +234,11 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     (float32, top_k int32).  Temperature 0 takes the largest logit; top_k < 1,
     top_p >= 1 and min_p <= 0 are off; -1 marks a row without a distribution
     (a NaN, a +inf, or nothing above -inf)."""
-    N, V, ld = _rows(logits, "logits")
+    code, N, V, ld = _rows(logits, "logits")
     dev = logits.device
     if not isinstance(u, torch.Tensor) or u.dtype != torch.float32:
         raise TypeError("u must be a float32 tensor")
-    if tuple(u.shape) != (N,) or u.device != dev or not u.is_contiguous():
+    if u.shape != (N,) or u.device != dev or not u.is_contiguous():
         raise ValueError(f"u must be {N} contiguous values on {dev}")
     ids = _out(out, (N,), torch.int32, dev)
     if not ids.is_contiguous():
@@ -227,7 +249,7 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     m_ptr, m = _setting(min_p, torch.float32, N, dev, "min_p")
     need = _lib.gmm_draw_workspace(N, V)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call(dev, _lib.gmm_draw, logits.data_ptr(), _TYPES[logits.dtype], N, V, ld, u.data_ptr(), t_ptr, float(t), k_ptr,
+    _call(dev, _lib.gmm_draw, logits.data_ptr(), code, N, V, ld, u.data_ptr(), t_ptr, float(t), k_ptr,
           min(max(int(k), 0), 2**31 - 1), p_ptr, float(p), m_ptr, float(m), ids.data_ptr(),
           None if ws is None else ws.data_ptr(), need)
     return ids
