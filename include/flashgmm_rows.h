@@ -44,8 +44,8 @@ typedef enum {
  * codes: 64 G bytes a row, element d in byte d / 2, the even one in the low
  * half; scales: 4 G bytes a row, one for each 32 values; padding has code 0
  * and scale 0.  Row strides are in bytes: ld_codes >= 64 G and a multiple of
- * 16, ld_scales >= 4 G and a multiple of 4; codes 16-byte and scales 4-byte
- * aligned.  1 <= D <= 2^20, at most 2^30 rows. */
+ * 16, ld_scales >= 4 G and a multiple of 4, both at most 2^23; codes 16-byte
+ * and scales 4-byte aligned.  1 <= D <= 2^20, at most 2^30 rows. */
 
 /* Quantisation: for each block of 32 values, with m their largest magnitude,
  *   e = max(floor(log2 m) - 2, -127), scale = e + 127 (0 for a block of zeros),

@@ -15,6 +15,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i8 __attribute__((ext_vector_type(8)));
+typedef unsigned long long u64;
 
 // Element types: conversion from and to float (one rounding, to nearest even).
 template <int TYPE>
@@ -193,105 +194,247 @@ __device__ __forceinline__ i8 operand(i4 v) { return i8{v.x, v.y, v.z, v.w, 0, 0
 template <int CT>
 __device__ __forceinline__ void put_c(typename Elem<CT>::T* p, float x) { *p = Elem<CT>::put(x); }
 
-// Large products: WM x WN waves, each with TM x TN blocks of 32 x 32, one
-// group (128 values) a step through two LDS buffers filled by LDS DMA.
-// LDS rows are 64 bytes: chunk c (block c of the group) of row r sits at slot
-// c ^ swz(r), so 8 consecutive rows' reads of one chunk touch all banks.
-// v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the block
-// 2 g + h in step h: any assignment serves as long as both sides share it,
-// and this one makes the two scale bytes of a lane neighbours.
+// Large products: WM x WN waves, each with TM x TN blocks of 32 x 32.  A step
+// is one group (128 values, 64 bytes of a row); S LDS buffers are filled by LDS
+// DMA S - 1 steps ahead.  Chunk c (block c of the group) of row r sits at slot
+// c ^ swz(r) of its 64 bytes, so 8 consecutive rows' reads of one chunk touch
+// all banks.  v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the
+// block 2 g + h of a group in its step h: any assignment serves as long as both
+// sides share it, and this one makes a lane's two scale bytes neighbours.
+// Scales come for 4 steps at a time, in 16 bytes of each row (the last 4 groups
+// at the end); SHORT rows of fewer groups have them placed by hand.
+// Tiles are numbered so that each XCD has a contiguous range of them, in
+// bands of 8 row tiles: 32 neighbours share 8 + 4 panels in the XCD's L2.
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 2)) & 3; }
 
-template <int WM, int WN, int TM, int TN, int CT>
-__global__ void __launch_bounds__(64 * WM* WN)
+// Orders a wave's LDS accesses before its later ones (other lanes' included).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// LDS DMA: 16 bytes from base + off (a lane's own) to LDS at dst + 16 lane.
+// base and dst are uniform.  In assembly because the compiler, which cannot
+// tell the buffers apart, would otherwise wait for every DMA under way before
+// each LDS read; the waits in front of the barriers order them here.
+__device__ __forceinline__ void lds_dma16(unsigned off, const uint8_t* base, unsigned dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
+               "s"(__builtin_amdgcn_readfirstlane((int)dst))
+               : "m0");
+}
+
+// The same where on is ~0, nothing where it is 0: without a branch, across
+// which the compiler would move matrix instructions.
+__device__ __forceinline__ void lds_dma16_if(u64 on, unsigned off, const uint8_t* base, unsigned dst) {
+  u64 all;
+  asm volatile(
+      "s_mov_b64 %0, exec\n\ts_mov_b64 exec, %4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, %0"
+      : "=&s"(all)
+      : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane((int)dst)), "s"(on)
+      : "m0");
+}
+
+template <int N>
+__device__ __forceinline__ void arrived() {  // all but the last N of this wave's DMA, its LDS accesses, everyone's
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
+  const int T = tm * tn, xcd = t & 7, per = T >> 3, rem = T & 7;
+  const int id = xcd * per + min(xcd, rem) + (t >> 3);
+  const int band = 8 * tn, b = id / band, in = id - b * band;
+  const int rows = min(8, tm - 8 * b);
+  n = in / rows;
+  m = 8 * b + in - n * rows;
+}
+
+template <int WM, int WN, int TM, int TN, int S, bool SHORT, int CT>
+__global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
     k_mx_tile(const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ as, int64_t ldas, int M,
               const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ bs, int64_t ldbs, int N, int G,
               const float* __restrict__ bias, typename Elem<CT>::T* __restrict__ C, int64_t ldc, int tm, int tn) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, NW = WM * WN;
-  constexpr int ROWS = BM + BN;  // A's rows, then B's
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][ROWS * 64];
-  __shared__ __attribute__((aligned(16))) unsigned scales[2][ROWS];
+  constexpr int ROWS = BM + BN;               // A's rows, then B's
+  constexpr int STEP = ROWS * 64;              // code bytes of a step
+  constexpr int OPS = ROWS / 16 / NW;          // DMA instructions of a wave in a step
+  constexpr int SOPS = (ROWS / 64 + NW - 1) / NW;  // and for the scales of 4 steps
+  static_assert(ROWS % (16 * NW) == 0 && S >= 2 && S <= 4 && BM % 64 == 0 && BN % 64 == 0, "tile shape");
+  constexpr int PITCH = 32 * TN + 4;  // floats of a row of results; rows 4 apart start 16 banks apart
+  constexpr int OUT = NW * 32 * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * STEP > OUT ? S * STEP : OUT];
+  __shared__ __attribute__((aligned(16))) uint4 scales[2][ROWS];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w % WM, wn = w / WM;
   const int r32 = lane & 31, g = lane >> 5;
-  const int t = (int)blockIdx.x;
-  const int m0 = (t % tm) * BM, n0 = (t / tm) * BN;
+  const unsigned lds0 = lds_address(lds), scales0 = lds_address(scales);
+  int mt, nt;
+  tile_of((int)blockIdx.x, tm, tn, mt, nt);
+  const int m0 = mt * BM, n0 = nt * BN;
 
-  auto stage = [&](int buf, int k) {
-    // 16 rows an instruction, 4 lanes a row
-    for (int i = w; i < ROWS / 16; i += NW) {
-      const int r = i * 16 + (lane >> 2);
-      const int c = (lane & 3) ^ swz(r);
-      const uint8_t* src;
-      if (i < BM / 16)
-        src = A + (int64_t)min(m0 + r, M - 1) * lda;  // rows past the end repeat the last, and are not stored
-      else
-        src = B + (int64_t)min(n0 + r - BM, N - 1) * ldb;
-      src += (int64_t)k * 64 + c * 16;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)(&codes[buf][i * 1024]), 16, 0, 0);
-    }
-    for (int i = w; i < ROWS / 64; i += NW) {
-      const int r = i * 64 + lane;
-      const uint8_t* src = i < BM / 64 ? as + (int64_t)min(m0 + r, M - 1) * ldas
-                                       : bs + (int64_t)min(n0 + r - BM, N - 1) * ldbs;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + (int64_t)k * 4),
-                                       (__attribute__((address_space(3))) void*)(&scales[buf][i * 64]), 4, 0, 0);
+  // This lane's source of each DMA instruction, relative to its panel's first
+  // row: 16 rows an instruction, 4 lanes a row.  Rows past the end repeat the
+  // last one and are not stored.
+  unsigned voff[OPS], soff[SOPS];
+#pragma unroll
+  for (int i = 0; i < OPS; ++i) {
+    const int r = (w * OPS + i) * 16 + (lane >> 2);
+    voff[i] = (r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)lda : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldb) +
+              ((lane & 3) ^ swz(r)) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < SOPS; ++i) {
+    const int r = min(w + i * NW, ROWS / 64 - 1) * 64 + lane;
+    soff[i] = r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)ldas : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldbs;
+  }
+  const uint8_t* const pa = A + (int64_t)m0 * lda;
+  const uint8_t* const pb = B + (int64_t)n0 * ldb;
+  const uint8_t* const qsa = as + (int64_t)m0 * ldas;
+  const uint8_t* const qsb = bs + (int64_t)n0 * ldbs;
+  // step k into its buffer; past the last one the last again, which nobody
+  // reads (no branch: one straight run of instructions)
+  auto stage = [&](int k) {
+    const int64_t off = 64 * (int64_t)min(k, G - 1);
+    const unsigned dst = lds0 + (unsigned)(k % S) * STEP + w * (OPS * 1024);
+#pragma unroll
+    for (int i = 0; i < OPS; ++i) lds_dma16(voff[i], ((w * OPS + i) * 16 < BM ? pa : pb) + off, dst + i * 1024);
+  };
+  // scales of groups k .. k + 3 (k a multiple of 4), or of a row's last 4
+  auto stage_scales = [&](int k, u64 on) {
+    const int64_t off = 4 * (int64_t)min(k, G - 4);
+#pragma unroll
+    for (int i = 0; i < SOPS; ++i) {
+      const int blk = min(w + i * NW, ROWS / 64 - 1);  // a spare instruction repeats the last block
+      lds_dma16_if(on, soff[i], (blk < BM / 64 ? qsa : qsb) + off,
+                   scales0 + (unsigned)((k >> 2) & 1) * (ROWS * 16) + blk * 1024);
     }
   };
-
-  f16v acc[TM][TN] = {};
-  stage(0, 0);
-  for (int k = 0; k < G; ++k) {
-    const int buf = k & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's DMA has landed
-    __syncthreads();                     // everyone's has, and the other buffer is free
-    if (k + 1 < G) stage(buf ^ 1, k + 1);
-    const uint8_t* cb = codes[buf];
-    const unsigned short* sb = reinterpret_cast<const unsigned short*>(scales[buf]);
-    int sa[TM], sn[TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = sb[2 * ((wm * TM + i) * 32 + r32) + g];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) sn[j] = sb[2 * (BM + (wn * TN + j) * 32 + r32) + g];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i4 a[TM], b[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int r = (wm * TM + i) * 32 + r32;
-        a[i] = *reinterpret_cast<const i4*>(cb + r * 64 + (((2 * g + h) ^ swz(r)) * 16));
-      }
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int r = BM + (wn * TN + j) * 32 + r32;
-        b[j] = *reinterpret_cast<const i4*>(cb + r * 64 + (((2 * g + h) ^ swz(r)) * 16));
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          if (h == 0)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a[i]), operand(b[j]), acc[i][j], 4, 4,
-                                                                        0, sa[i], 0, sn[j]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a[i]), operand(b[j]), acc[i][j], 4, 4,
-                                                                        1, sa[i], 1, sn[j]);
-        }
+  if constexpr (SHORT) {
+    for (int r = tid; r < ROWS; r += 64 * NW) {
+      const uint8_t* p = r < BM ? as + (int64_t)min(m0 + r, M - 1) * ldas : bs + (int64_t)min(n0 + r - BM, N - 1) * ldbs;
+      for (int e = 0; e < G; ++e)  // as the last of 4 groups
+        reinterpret_cast<unsigned*>(&scales[0][r])[4 - G + e] = reinterpret_cast<const unsigned*>(p)[e];
     }
+  } else {
+    stage_scales(0, ~0ull);
   }
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) stage(k);
+
+  // Operands of a half step are read from LDS while the matrix unit works on
+  // the half before; the barrier stands in front of a step's second half,
+  // whose operands this wave has then in registers.
+  f16v acc[TM][TN] = {};
+  i4 fa[2][TM], fb[2][TN];
+  int qa[2][TM], qb[2][TN];  // scales of even and odd steps, this lane's half in the low bits
+  auto read = [&](int k, int h) {
+    const uint8_t* cb = lds + (k % S) * STEP;
+    const int c = ((2 * g + h) ^ swz(r32)) * 16;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[h][i] = *reinterpret_cast<const i4*>(cb + ((wm * TM + i) * 32 + r32) * 64 + c);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[h][j] = *reinterpret_cast<const i4*>(cb + (BM + (wn * TN + j) * 32 + r32) * 64 + c);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_scales = [&](int k, int e) {  // of step k, into set e
+    const int c = k - min(k & ~3, G - 4);
+    const unsigned* sb = reinterpret_cast<const unsigned*>(scales[(k >> 2) & 1]) + min(c, 3);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) qa[e][i] = (int)(sb[4 * ((wm * TM + i) * 32 + r32)] >> (16 * g));
+#pragma unroll
+    for (int j = 0; j < TN; ++j) qb[e][j] = (int)(sb[4 * (BM + (wn * TN + j) * 32 + r32)] >> (16 * g));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Step k is in LDS for everyone, and step k - 1 read by everyone; its buffer
+  // takes step k + S - 1.  The scales of the next 4 steps follow 3 steps ahead
+  // at the latest, which is as far as the wait leaves DMA outstanding.
+  auto arrive = [&](int k) {
+    arrived<(S - 2) * OPS>();
+    if constexpr (!SHORT) stage_scales((k & ~3) + 4, (k & 3) == 0 ? ~0ull : 0ull);
+    stage(k + S - 1);
+  };
+  // one half step's products: block Q of a lane's two, scales of set E
+#define GMM_MX_HALF(Q, E)                                                                                          \
+  do {                                                                                                             \
+    _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =      \
+        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fa[Q][i]), operand(fb[Q][j]), acc[i][j], 4, 4, Q,  \
+                                                        qa[E][i], Q, qb[E][j]);                                    \
+    __builtin_amdgcn_sched_barrier(0);                                                                             \
+  } while (0)
+
+  arrive(0);
+  read_scales(0, 0);
+  read(0, 0);
+  int k = 0;
+  for (; k + 1 < G; k += 2) {
+    read(k, 1);
+    GMM_MX_HALF(0, 0);
+    arrive(k + 1);
+    read_scales(k + 1, 1);
+    read(k + 1, 0);
+    GMM_MX_HALF(1, 0);
+    read(k + 1, 1);
+    GMM_MX_HALF(0, 1);
+    arrive(k + 2);
+    read_scales(k + 2, 0);
+    read(k + 2, 0);
+    GMM_MX_HALF(1, 1);
+  }
+  if (G & 1) {
+    read(k, 1);
+    GMM_MX_HALF(0, 0);
+    GMM_MX_HALF(1, 0);
+  }
+#undef GMM_MX_HALF
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the buffers are reused
+
+  // The result goes through LDS so that it leaves in 16-byte stores along
+  // rows of 32 TN columns (accumulators hold 32 columns of 2 rows): rows that
+  // start anywhere in a 128-byte line are then written nearly whole.
+  using T = typename Elem<CT>::T;
+  constexpr int WN32 = 32 * TN, VEC = 16 / sizeof(T), LPR = WN32 / VEC;  // lanes to a row
+  float bv[TN];
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int n = n0 + (wn * TN + j) * 32 + r32;
-    if (n >= N) continue;
-    const float bv = bias ? bias[n] : 0.f;
+    bv[j] = bias && n < N ? bias[n] : 0.f;
+  }
+  __syncthreads();
+  float* blk = reinterpret_cast<float*>(lds) + w * 32 * PITCH;
+  const int col = (lane % LPR) * VEC, nc = n0 + wn * WN32 + col;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int m = m0 + (wm * TM + i) * 32 + (v & 3) + 8 * (v >> 2) + 4 * g;
-        if (m < M) put_c<CT>(C + (int64_t)m * ldc + n, acc[i][j][v] + bv);
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) blk[((v & 3) + 8 * (v >> 2) + 4 * g) * PITCH + 32 * j + r32] = acc[i][j][v] + bv[j];
+    wave_sync();
+#pragma unroll
+    for (int q = 0; q < 32 / (64 / LPR); ++q) {
+      const int row = q * (64 / LPR) + lane / LPR;
+      const int m = m0 + (wm * TM + i) * 32 + row;
+      T t[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; v += 4) {
+        const f4 x = *reinterpret_cast<const f4*>(blk + row * PITCH + col + v);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) t[v + y] = Elem<CT>::put(x[y]);
       }
+      if (m < M) {
+        T* out = C + (int64_t)m * ldc + nc;
+        if (nc + VEC <= N) {
+          __builtin_memcpy(out, t, sizeof t);
+        } else {
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (nc + v < N) out[v] = t[v];
+        }
+      }
+    }
+    wave_sync();
   }
 }
 
@@ -400,6 +543,23 @@ static void few_rows(const MxProduct& p, int G, hipStream_t s) {
                      (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, p.bias, (typename Elem<CT>::T*)p.C, p.ldc);
 }
 
+template <int WM, int WN, int TM, int TN, int S, int CT>
+static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
+  const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
+  if (tm * tn > (1 << 23)) return hipErrorInvalidValue;  // a result of over 2^37 elements
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, s, (const uint8_t*)p.A, p.lda, p.as,
+                       p.ldas, (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, G, p.bias, (typename Elem<CT>::T*)p.C,
+                       p.ldc, (int)tm, (int)tn);
+  };
+  if (G < 4)
+    launch(k_mx_tile<WM, WN, TM, TN, S, true, CT>);
+  else
+    launch(k_mx_tile<WM, WN, TM, TN, S, false, CT>);
+  return hipGetLastError();
+}
+
 template <int CT>
 static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
   if (p.M <= kFewRows) {
@@ -417,13 +577,15 @@ static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
       few_rows<kMx, 4, CT>(p, G, s);
     return hipGetLastError();
   }
-  constexpr int WM = 2, WN = 2, TM = 2, TN = 2;
-  const int64_t tm = (p.M + 127) / 128, tn = (p.N + 127) / 128;
-  if (tm * tn > (1 << 23)) return hipErrorInvalidValue;  // a result of over 2^37 elements
-  hipLaunchKernelGGL((k_mx_tile<WM, WN, TM, TN, CT>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, s,
-                     (const uint8_t*)p.A, p.lda, p.as, p.ldas, (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, G, p.bias,
-                     (typename Elem<CT>::T*)p.C, p.ldc, (int)tm, (int)tn);
-  return hipGetLastError();
+  // The tile.  Large ones read less from L2 and LDS for each product, small
+  // ones fill the 256 CUs and let a workgroup's stores overlap another's
+  // products.  Measured (us): 8192 x 8192 x 8192 330 with 256 x 256, 368 with
+  // 256 x 128, 439 with 128 x 128; 1024 x 100003 x 128 142, 114 and 131;
+  // 128 x 16384 x 4096 35, 26 and 20.
+  const int64_t cus = 256;
+  if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 3, CT>(p, G, s);
+  if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 2, CT>(p, G, s);
+  return tiles<2, 2, 2, 2, 2, CT>(p, G, s);
 }
 
 hipError_t launch_mx_product(const MxProduct& p0, void* workspace, hipStream_t s) {

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int32_t kMaxWidth = 1 << 20;
+constexpr int64_t kMaxStride = 1 << 23;  // bytes of a row of codes or scales: a tile's rows lie within 4 GiB
 
 gmm_status refuse(gmm_status st, const char* fmt, ...) {
   char buf[256];
@@ -73,11 +74,11 @@ gmm_status check_mx(const uint8_t* codes, int64_t ldc, const uint8_t* scales, in
   if (!aligned(codes, 16) || !aligned(scales, 4))
     return refuse(GMM_ERR_INVALID_ARG, "%s: codes must be 16-byte and scales 4-byte aligned", name);
   const int G = gmm::mx_groups(D);
-  if (ldc < (int64_t)64 * G || (ldc & 15) || ldc > ((int64_t)1 << 40))
-    return refuse(GMM_ERR_INVALID_ARG, "%s: code stride must be >= %d and a multiple of 16 (got %lld)", name, 64 * G,
+  if (ldc < (int64_t)64 * G || (ldc & 15) || ldc > kMaxStride)
+    return refuse(GMM_ERR_INVALID_ARG, "%s: code stride must be in [%d, 2^23] and a multiple of 16 (got %lld)", name, 64 * G,
                   (long long)ldc);
-  if (lds < (int64_t)4 * G || (lds & 3) || lds > ((int64_t)1 << 40))
-    return refuse(GMM_ERR_INVALID_ARG, "%s: scale stride must be >= %d and a multiple of 4 (got %lld)", name, 4 * G,
+  if (lds < (int64_t)4 * G || (lds & 3) || lds > kMaxStride)
+    return refuse(GMM_ERR_INVALID_ARG, "%s: scale stride must be in [%d, 2^23] and a multiple of 4 (got %lld)", name, 4 * G,
                   (long long)lds);
   return GMM_OK;
 }
