@@ -439,22 +439,48 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
 }
 
 // Few rows of A (up to 16 MT): bound by reading B once.  A wave takes NT
-// blocks of 16 B rows and a share of the groups; the waves of a workgroup
-// share the same rows and add their sums through LDS in wave order.  B is the
-// first operand (its rows along the accumulator's registers), A the second.
-// AT = kMx: A's codes as stored.  Otherwise A's rows are quantised in
-// registers: lane (r, g) holds block g of row r, which is the operand layout.
-template <int AT, int MT, int NT, int CT>
-__global__ void __launch_bounds__(512)
+// blocks of 16 B rows and a share of the groups, 4 at a time, all of whose
+// loads go out before the first is used.  The waves of a workgroup share the
+// same rows and add their sums through LDS in wave order.  B is the first
+// operand (its rows along the accumulator's registers), A the second.
+// AT = kMx: A's codes as stored.  Otherwise the workgroup quantises A's rows
+// into LDS while its first codes of B are on their way, one block of 32 values
+// to a thread.
+// SHORT: rows of fewer than 4 groups, whose scales are brought one by one.
+
+// The 4 scale words of groups k .. k + 3 of a row (k a multiple of 4); those
+// that are not there repeat the last.
+template <bool SHORT>
+__device__ __forceinline__ void scales4(const uint8_t* __restrict__ row, int k, int G, unsigned (&s)[4]) {
+  if constexpr (SHORT) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = *reinterpret_cast<const unsigned*>(row + 4 * min(e, G - 1));
+  } else {
+    unsigned q[4];
+    const int from = min(k, G - 4), d = k - from;
+    __builtin_memcpy(q, row + 4 * (int64_t)from, 16);
+    s[0] = d == 0 ? q[0] : d == 1 ? q[1] : d == 2 ? q[2] : q[3];
+    s[1] = d == 0 ? q[1] : d == 1 ? q[2] : q[3];
+    s[2] = d == 0 ? q[2] : q[3];
+    s[3] = q[3];
+  }
+}
+
+constexpr int few_waves(int MT) { return MT == 4 ? 4 : 8; }  // waves of a workgroup at most
+
+template <int AT, int MT, int NT, bool SHORT, int CT>
+__global__ void __launch_bounds__(64 * few_waves(MT))
     k_mx_rows(const void* __restrict__ A, int64_t lda, const uint8_t* __restrict__ as, int64_t ldas, int M,
               const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ bs, int64_t ldbs, int N, int D,
-              int G, const float* __restrict__ bias, typename Elem<CT>::T* __restrict__ C, int64_t ldc) {
-  static_assert(AT == kMx || MT == 1, "rows are quantised on the way for one block of 16");
-  __shared__ __attribute__((aligned(16))) float part[8][NT * MT][64 * 4];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, NWV = blockDim.x >> 6;
+              int G, int share, const float* __restrict__ bias, typename Elem<CT>::T* __restrict__ C, int64_t ldc) {
+  using T = typename Elem<CT>::T;
+  __shared__ __attribute__((aligned(16))) float part[few_waves(MT)][NT * MT][64 * 4];
+  extern __shared__ __attribute__((aligned(16))) uint8_t held[];  // A's codes [G][M][64], scales [G][M][4]
+  const int tid = threadIdx.x, lane = tid & 63, NWV = blockDim.x >> 6;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int share = (G + NWV - 1) / NWV;
-  const int k0 = w * share, k1 = min(G, k0 + share);
+  const int k0 = w * share, k1 = min(G, k0 + share);  // share is a multiple of 4
+  bool first = AT != kMx;
   for (int n0 = (int)blockIdx.x * (16 * NT); n0 < N; n0 += (int)gridDim.x * (16 * NT)) {
     const uint8_t* brow[NT];
     const uint8_t* srow[NT];
@@ -464,46 +490,78 @@ __global__ void __launch_bounds__(512)
       brow[j] = B + n * ldb + g * 16;
       srow[j] = bs + n * ldbs;
     }
-    f4 acc[NT][MT] = {};
-    for (int k = k0; k < k1; ++k) {
-      i4 b[NT];
-      int sb[NT];
+    i4 b[4][NT];
+    unsigned sb[NT][4];
+    auto load_b = [&](int k) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        b[j] = *reinterpret_cast<const i4*>(brow[j] + (int64_t)k * 64);
-        sb[j] = (int)(*reinterpret_cast<const unsigned*>(srow[j] + (int64_t)k * 4) >> (8 * g));
+        scales4<SHORT>(srow[j], k, G, sb[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e][j] = *reinterpret_cast<const i4*>(brow[j] + 64 * (int64_t)min(k + e, G - 1));
       }
-      i4 a[MT];
-      int sa[MT];
+    };
+    f4 acc[NT][MT] = {};
+    auto multiply = [&](int k) {
+      i4 a[4][MT];
+      unsigned sa[MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int64_t m = min(16 * i + r, M - 1);
+        const int m = min(16 * i + r, M - 1);
         if constexpr (AT == kMx) {
-          a[i] = *reinterpret_cast<const i4*>(static_cast<const uint8_t*>(A) + m * lda + (int64_t)k * 64 + g * 16);
-          sa[i] = as[m * ldas + (int64_t)k * 4 + g];
+          scales4<SHORT>(as + m * ldas, k, G, sa[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            a[e][i] = *reinterpret_cast<const i4*>(static_cast<const uint8_t*>(A) + m * lda + 64 * (int64_t)min(k + e, G - 1) +
+                                                   g * 16);
         } else {
-          using T = typename Elem<AT>::T;
-          const T* row = static_cast<const T*>(A) + m * lda;
-          float v[4][8];
-          unsigned top = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            load8<AT>(row, k * 128 + g * 32 + q * 8, D, v[q]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max_mag(top, v[q][e]);
+          for (int e = 0; e < 4; ++e) {
+            const int at = min(k + e, G - 1) * M + m;
+            a[e][i] = *reinterpret_cast<const i4*>(held + at * 64 + g * 16);
+            sa[i][e] = *reinterpret_cast<const unsigned*>(held + G * M * 64 + at * 4);
           }
-          const unsigned s = scale_of(top);
-          sa[i] = (int)s;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) a[i][q] = (int)codes8(v[q], s);
         }
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int e = 0; e < 4; ++e) {
+        const int there = k + e < G ? -1 : 0;  // a group that is not there adds zeros
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b[j]), operand(a[i]), acc[j][i], 4, 4, 0,
-                                                                       sb[j], 0, sa[i]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b[e][j]), operand(a[e][i] & there),
+                                                                         acc[j][i], 4, 4, 0, (int)(sb[j][e] >> (8 * g)), 0,
+                                                                         (int)(sa[i][e] >> (8 * g)));
+      }
+    };
+    load_b(min(k0, (G - 1) & ~3));
+    if (first) {
+      first = false;
+      if constexpr (AT != kMx) {
+        for (int t = tid; t < M * 4 * G; t += blockDim.x) {
+          const int m = t / (4 * G), q = t - m * (4 * G), at = (q >> 2) * M + m;
+          const typename Elem<AT>::T* row = static_cast<const typename Elem<AT>::T*>(A) + m * lda;
+          float v[4][8];
+          unsigned top = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            load8<AT>(row, q * 32 + x * 8, D, v[x]);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) top = max_mag(top, v[x][y]);
+          }
+          const unsigned s = scale_of(top);
+          i4 c;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) c[x] = (int)codes8(v[x], s);
+          *reinterpret_cast<i4*>(held + at * 64 + (q & 3) * 16) = c;
+          held[G * M * 64 + at * 4 + (q & 3)] = (uint8_t)s;
+        }
+        __syncthreads();
+      }
+    }
+    for (int k = k0; k < k1; k += 4) {
+      if (k > k0) load_b(k);
+      multiply(k);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -515,32 +573,77 @@ __global__ void __launch_bounds__(512)
       f4 s = *reinterpret_cast<const f4*>(&part[0][q][lane * 4]);
       for (int x = 1; x < NWV; ++x) s += *reinterpret_cast<const f4*>(&part[x][q][lane * 4]);
       const int m = 16 * (q % MT) + r, n = n0 + 16 * (q / MT) + 4 * g;
-      if (m >= M) continue;
+      if (bias) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (n + v < N) put_c<CT>(C + (int64_t)m * ldc + n + v, s[v] + (bias ? bias[n + v] : 0.f));
+        for (int v = 0; v < 4; ++v) s[v] += bias[min(n + v, N - 1)];
+      }
+      if (m >= M) continue;
+      T* out = C + (int64_t)m * ldc + n;
+      T t[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) t[v] = Elem<CT>::put(s[v]);
+      if (n + 4 <= N) {
+        __builtin_memcpy(out, t, sizeof t);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (n + v < N) out[v] = t[v];
+      }
     }
     __syncthreads();
   }
 }
 
-// Rows of A that one workgroup of the few-rows kernel takes, and up to which
-// rows that are not in 4 bits yet are quantised inside it.
-constexpr int kFewRows = 64, kFewFloatRows = 16;
+constexpr int kFewRows = 64;  // rows of A that the few-rows kernel takes
 
-size_t mx_product_workspace(int a_type, int64_t M, int64_t N, int D) {
-  if (a_type == kMx || M <= kFewFloatRows) return 0;
-  return (size_t)M * 68 * (size_t)mx_groups(D);
+// Waves of a workgroup: each takes at least 4 groups.
+static int waves_for(int G, int most) {
+  const int w = (G + 3) / 4;
+  return w < most ? w : most;
+}
+// Rows that are not in 4 bits are quantised inside the few-rows kernel where
+// that is at most one block for each of its threads.  Above, each of the
+// N / 32 workgroups would repeat more work than a kernel of its own costs:
+// 8 rows of 4096 float32 against 16384 rows take 19 us inside, 9 us and 2.5 us
+// apart; one row 10.4 us inside.
+static bool quantised_inside(int a_type, int64_t M, int G) {
+  return a_type != kMx && M <= 16 && M * 4 * G <= 64 * waves_for(G, few_waves(1));
 }
 
-template <int AT, int MT, int CT>
-static void few_rows(const MxProduct& p, int G, hipStream_t s) {
-  constexpr int NT = 2;
-  const int waves = G >= 32 ? 8 : G >= 8 ? 4 : G >= 2 ? 2 : 1;
+size_t mx_product_workspace(int a_type, int64_t M, int64_t N, int D) {
+  const int G = mx_groups(D);
+  if (a_type == kMx || quantised_inside(a_type, M, G)) return 0;
+  return (size_t)M * 68 * (size_t)G;
+}
+
+template <int AT, int MT, int NT, bool SHORT, int CT>
+static void few_rows_as(const MxProduct& p, int G, hipStream_t s) {
+  const int waves = waves_for(G, few_waves(MT));
+  const int share = ((G + 3) / 4 + waves - 1) / waves * 4;
   const int64_t tiles = (p.N + 16 * NT - 1) / (16 * NT);
   const unsigned grid = (unsigned)(tiles < (1 << 20) ? tiles : (1 << 20));  // the kernel strides over the rest
-  hipLaunchKernelGGL((k_mx_rows<AT, MT, NT, CT>), dim3(grid), dim3(64 * waves), 0, s, p.A, p.lda, p.as, p.ldas,
-                     (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, p.bias, (typename Elem<CT>::T*)p.C, p.ldc);
+  const size_t held = AT == kMx ? 0 : (size_t)p.M * G * 68;
+  hipLaunchKernelGGL((k_mx_rows<AT, MT, NT, SHORT, CT>), dim3(grid), dim3(64 * waves), held, s, p.A, p.lda, p.as,
+                     p.ldas, (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, share, p.bias,
+                     (typename Elem<CT>::T*)p.C, p.ldc);
+}
+template <int AT, int MT, int NT, int CT>
+static void few_rows_nt(const MxProduct& p, int G, hipStream_t s) {
+  if (G < 4)
+    few_rows_as<AT, MT, NT, true, CT>(p, G, s);
+  else
+    few_rows_as<AT, MT, NT, false, CT>(p, G, s);
+}
+// Blocks of 16 B rows to a wave: one where two would leave CUs idle (1 x 1024
+// x 8192: 6.7 us against 9.8), otherwise two (1 x 16384 x 4096: 8.9 us against
+// 10.1 with one), four where A has more rows to bring (64 x 16384 x 4096: 18 us
+// against 21 with two).
+template <int AT, int MT, int CT>
+static void few_rows(const MxProduct& p, int G, hipStream_t s) {
+  if (p.N <= 16 * 512)
+    few_rows_nt<AT, MT, 1, CT>(p, G, s);
+  else
+    few_rows_nt<AT, MT, MT == 4 ? 4 : 2, CT>(p, G, s);
 }
 
 template <int WM, int WN, int TM, int TN, int S, int CT>
@@ -591,7 +694,7 @@ static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
 hipError_t launch_mx_product(const MxProduct& p0, void* workspace, hipStream_t s) {
   MxProduct p = p0;
   const int G = mx_groups(p.D);
-  if (p.a_type != kMx && p.M > kFewFloatRows) {
+  if (p.a_type != kMx && !quantised_inside(p.a_type, p.M, G)) {
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + (size_t)p.M * 64 * G;
     hipError_t e = launch_mx_quantize(p.A, p.a_type, p.M, p.D, p.lda, codes, 64 * (int64_t)G, scales, 4 * (int64_t)G, s);
