@@ -21,6 +21,7 @@
 #include "gmm_rows.h"
 
 #include <limits.h>
+#include <stdlib.h>
 
 namespace gmm {
 
@@ -68,27 +69,34 @@ __device__ __forceinline__ bool behind(float z, int idx, u64 cut) {
 __device__ __forceinline__ float place_value(u64 p) { return key_value(~(unsigned)(p >> kIdxBits)); }
 __device__ __forceinline__ int place_index(u64 p) { return (int)(p & ((1u << kIdxBits) - 1)); }
 
-// round(2^42 2^t) for t <= 0 (0 below -43, NaN included).  t = n + f with n whole and |f| <=
-// 1/2; 2^f = sum (f ln 2)^i / i! up to i = 11 (the rest is below 2^-46).
-__device__ __forceinline__ u64 fixed_exp2(double t) {
+// a * b + c with c in scalar registers (left to itself the compiler copies
+// each constant into the accumulator of a two-address instruction first).
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
+  return r;
+}
+// round(2^42 2^t) for t <= 0 (0 below -43, NaN included).  t = n + f with n
+// whole and |f| <= 1/2; 2^f = 1 + f q(f), q of degree 8 fitted to the least
+// largest error (2^-45.8); n goes into the exponent.  The rounded integer
+// stands in the low bits of the result plus 2^52.
+constexpr double kOnes = 4503599627370496.0;  // 2^52
+__device__ __forceinline__ double fixed_exp2_up(double t) {
+  constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: sums with it are whole, in the low bits
   t = fmax(t, -100.0);
-  const double n = rint(t);
-  const double x = (t - n) * 0.693147180559945309417;
-  double p = 1.0 / 39916800.0;
-  p = fma(p, x, 1.0 / 3628800.0);
-  p = fma(p, x, 1.0 / 362880.0);
-  p = fma(p, x, 1.0 / 40320.0);
-  p = fma(p, x, 1.0 / 5040.0);
-  p = fma(p, x, 1.0 / 720.0);
-  p = fma(p, x, 1.0 / 120.0);
-  p = fma(p, x, 1.0 / 24.0);
-  p = fma(p, x, 1.0 / 6.0);
-  p = fma(p, x, 0.5);
-  p = fma(p, x, 1.0);
-  p = fma(p, x, 1.0);
-  // adding 2^52 leaves the rounded integer in the low bits of the sum
-  const double y = ldexp(p, (int)n + kFix) + 4503599627370496.0;
-  return (u64)__double_as_longlong(y) & 0xFFFFFFFFFFFFFull;
+  const double u = t + kWhole;
+  const double f = t - (u - kWhole);
+  double q = fma_const(0x1.b68e3bcc4f117p-24, f, 0x1.63e7f9e4ad781p-20);
+  q = fma_const(q, f, 0x1.ffcb39c272ef4p-17);
+  q = fma_const(q, f, 0x1.430896a09ff32p-13);
+  q = fma_const(q, f, 0x1.5d87fea692c29p-10);
+  q = fma_const(q, f, 0x1.3b2ab724d3d1cp-7);
+  q = fma_const(q, f, 0x1.c6b08d703894cp-5);
+  q = fma_const(q, f, 0x1.ebfbdff81b63bp-3);
+  q = fma_const(q, f, 0x1.62e42fefa3a26p-1);
+  q = fma(q, f, 1.0);
+  const int n = (int)(unsigned)(u64)__double_as_longlong(u);
+  return __hiloint2double(__double2hiint(q) + ((n + kFix) << 20), __double2loint(q)) + kOnes;
 }
 
 // Sums over the lanes of a wave on the data-parallel primitives (shifts
@@ -108,16 +116,41 @@ __device__ __forceinline__ u64 wave_scan(u64 v) {  // inclusive
   v += dpp64<0x143, 0xC>(v);
   return v;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  return v + __longlong_as_double((long long)dpp64<CTRL, ROWS>((u64)__double_as_longlong(v)));
+}
+__device__ __forceinline__ double wave_scan(double v) {
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  v = dpp_add<0x143, 0xC>(v);
+  return v;
+}
 __device__ __forceinline__ u64 lane_value(u64 v, int lane) {
   const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, lane);
   const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), lane);
   return ((u64)hi << 32) | lo;
 }
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  return __longlong_as_double((long long)lane_value((u64)__double_as_longlong(v), lane));
+}
 __device__ __forceinline__ u64 wave_sum(u64 v) { return lane_value(wave_scan(v), 63); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_max(float v) {  // v itself where there is no source lane
+  const int b = __float_as_int(v);
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, ROWS, 0xF, false)));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+  v = dpp_max<0x111, 0xF>(v);
+  v = dpp_max<0x112, 0xF>(v);
+  v = dpp_max<0x114, 0xF>(v);
+  v = dpp_max<0x118, 0xF>(v);
+  v = dpp_max<0x142, 0xA>(v);
+  v = dpp_max<0x143, 0xC>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 __device__ __forceinline__ u64 wave_min(u64 v) {
 #pragma unroll
@@ -138,22 +171,37 @@ __device__ __forceinline__ void wave_sync() {
 struct Scale {
   double M, c;   // largest logit; log2(e) / T
   float half, bs;  // M / 2; bins per unit of (M - z) / 2, which does not overflow
-  u64 wmin;      // weights below it are cut by min-p
+  double dmin;     // weights below it are cut by min-p
 };
+__device__ __forceinline__ double uniform(double v) {  // the same in all lanes: into scalar registers
+  return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(v)),
+                          __builtin_amdgcn_readfirstlane(__double2loint(v)));
+}
+__device__ __forceinline__ float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
 __device__ __forceinline__ Scale scale_for(float M, float temp, float min_p, int nb) {
   Scale s;
-  s.M = M;
-  s.c = 1.44269504088896340736 / (double)temp;
-  s.half = 0.5f * M;
-  s.bs = (float)(nb - 1) / (15.f * temp);
-  s.wmin = min_p > 0.f ? (u64)ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1;
+  s.M = uniform((double)M);
+  s.c = uniform(1.44269504088896340736 / (double)temp);
+  s.half = uniform(0.5f * M);
+  s.bs = uniform((float)(nb - 1) / (15.f * temp));
+  s.dmin = uniform(min_p > 0.f ? ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1.0);
   return s;
 }
-__device__ __forceinline__ u64 weight(const Scale& s, float x) { return fixed_exp2(((double)x - s.M) * s.c); }
+__device__ __forceinline__ u64 weight(const Scale& s, float x) {
+  return (u64)__double_as_longlong(fixed_exp2_up(((double)x - s.M) * s.c)) & 0xFFFFFFFFFFFFFull;
+}
+// The same as a float64, in which sums of up to 2048 weights are exact; 0 if
+// it is below wmin.
+__device__ __forceinline__ double weight_if(const Scale& s, float x) {
+  const double q = fixed_exp2_up(((double)x - s.M) * s.c) - kOnes;
+  return q >= s.dmin ? q : 0.0;
+}
 // bins are ordered as the logits are, and the last one has no weight
 template <int NB>
 __device__ __forceinline__ int bin_of(const Scale& s, float x) {
-  return (int)fminf((s.half - 0.5f * x) * s.bs, (float)(NB - 1));
+  return (int)fminf(fmaf(x, -0.5f, s.half) * s.bs, (float)(NB - 1));
 }
 // The running sum, in units of weight, that the draw has to reach: the first
 // one above u * total, and no more than the total.
@@ -342,25 +390,25 @@ struct WaveRow {
         if (behind(x[i], index(i), cut)) in &= ~(1u << i);
     }
     fresh();
-    // running sums in index order: tile by tile, lane by lane
-    u64 before[TILES + 1];
-    u64 run[TILES];
+    // running sums in index order: tile by tile, lane by lane (a row's 1024
+    // weights at most sum to 2^52: exact)
+    double before[TILES + 1], run[TILES];
     before[0] = 0;
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      u64 own = 0;
+      double own = 0;
 #pragma unroll
       for (int v = 0; v < 4; ++v) own += stays(4 * t + v, in);
-      const u64 scan = wave_scan(own);
+      const double scan = wave_scan(own);
       run[t] = before[t] + scan - own;
       before[t + 1] = before[t] + lane_value(scan, 63);
     }
-    const u64 want = draw_target(u, before[TILES]);
+    const double want = (double)draw_target(u, (u64)before[TILES]);
     // the tile that reaches it, and its four weights again
     int tile = 0;
 #pragma unroll
     for (int t = 1; t < TILES; ++t) tile += before[t] < want;
-    u64 r = run[0];
+    double r = run[0];
     float y[4] = {x[0], x[1], x[2], x[3]};
     unsigned stay = in;
 #pragma unroll
@@ -374,26 +422,24 @@ struct WaveRow {
     int id = INT_MAX;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      u64 q = (stay >> v) & 1 ? weight(s, y[v]) : 0;
-      q = q >= s.wmin ? q : 0;
+      const double q = (stay >> v) & 1 ? weight_if(s, y[v]) : 0;
       if (r < want && want <= r + q) id = tile * 256 + 4 * lane + v;
       r += q;
     }
     const u64 who = __ballot(id != INT_MAX);
     return __builtin_amdgcn_readlane(id, __ffsll(who) - 1);
   }
-  __device__ __forceinline__ u64 stays(int i, unsigned in) const {
-    const u64 q = (in >> i) & 1 ? weight(s, x[i]) : 0;
-    return q >= s.wmin ? q : 0;
+  __device__ __forceinline__ double stays(int i, unsigned in) const {
+    return (in >> i) & 1 ? weight_if(s, x[i]) : 0;
   }
 };
 
 // ---------------------------------------------------------------------------
 // Longer rows: one workgroup of THREADS lanes to a row.  HELD > 0: the row (at
 // most HELD tiles) is kept in LDS as floats, each lane reading back what it
-// wrote; 0: it is read again in every pass.  A tile is VEC elements a lane,
-// idx = (tile * THREADS + tid) * VEC + v; the 64 VEC elements of a wave in a
-// tile are a part.
+// wrote; 0: it is read again in every pass.  A part is a run of AHEAD * 64 * VEC
+// elements, which a wave takes in AHEAD loads of VEC a lane; parts go to the
+// waves in turn.
 //
 // Passes over the row: the largest logit; a histogram (of counts for top-k, of
 // weights for top-p alone); then either the elements up to the bin of the cut
@@ -404,8 +450,9 @@ template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
 struct BlockRow {
   using T = typename Logit<TYPE>::T;
   static constexpr int VEC = Logit<TYPE>::VEC, NW = THREADS / 64, CAP = NB, AHEAD = 16 / VEC;
+  static constexpr int PART = AHEAD * 64 * VEC;  // 1024 elements
   struct SH {
-    float held[HELD ? HELD * THREADS * VEC : 4];
+    float held[HELD ? PARTS * PART : 4];
     u64 hist[NB];  // sums of bins, or the weights of the list's entries
     u64 list[CAP];
     u64 part[PARTS];
@@ -418,15 +465,18 @@ struct BlockRow {
 
   SH& sh;
   const T* z;
-  const int V, ntiles, tid, lane, wv;
+  const int V, nparts, tid, lane, wv;
   Scale s;
 
-  __device__ __forceinline__ BlockRow(SH& sh_, const T* row, int v, int nt)
-      : sh(sh_), z(row), V(v), ntiles(nt), tid(threadIdx.x), lane(threadIdx.x & 63), wv(threadIdx.x >> 6) {}
+  __device__ __forceinline__ BlockRow(SH& sh_, const T* row, int v)
+      : sh(sh_), z(row), V(v), nparts((v + PART - 1) / PART), tid(threadIdx.x), lane(threadIdx.x & 63),
+        wv(__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)) {}
 
-  // the logits of this lane in tile t; those past V are -inf
-  __device__ __forceinline__ void load(int t, float (&x)[VEC]) const {
-    const int idx = (t * THREADS + tid) * VEC;
+  // first of this lane's elements in load a of part p
+  __device__ __forceinline__ int index(int p, int a) const { return (p * AHEAD + a) * (64 * VEC) + lane * VEC; }
+  // the logits there; those past V are -inf
+  __device__ __forceinline__ void load(int p, int a, float (&x)[VEC]) const {
+    const int idx = index(p, a);
     if (idx + VEC <= V) {
       T q[VEC];
       __builtin_memcpy(q, z + idx, sizeof q);  // rows may start at any element
@@ -437,42 +487,43 @@ struct BlockRow {
       for (int v = 0; v < VEC; ++v) x[v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
     }
   }
-  __device__ __forceinline__ void fetch(int t, float (&x)[VEC]) const {
+  __device__ __forceinline__ float4* held(int p, int a, int v) const {
+    return reinterpret_cast<float4*>(&sh.held[(p * AHEAD + a) * (64 * VEC) + v * 64 + lane * 4]);
+  }
+  __device__ __forceinline__ void fetch(int p, int a, float (&x)[VEC]) const {
     if constexpr (HELD > 0) {
 #pragma unroll
       for (int v = 0; v < VEC; v += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(&sh.held[(t * VEC + v) * THREADS + tid * 4]);
+        const float4 q = *held(p, a, v);
         x[v] = q.x, x[v + 1] = q.y, x[v + 2] = q.z, x[v + 3] = q.w;
       }
     } else {
-      load(t, x);
+      load(p, a, x);
     }
   }
-  // f(tile, first index, logits) for this lane's tiles, several loads ahead
-  template <class F>
-  __device__ __forceinline__ void tiles(F&& f) const {
-    constexpr int A = HELD > 0 ? 1 : AHEAD;
-    int t = 0;
-    for (; t + A <= ntiles; t += A) {
-      float x[A][VEC];
+  // f(part, load, logits) for this wave's parts, a part's loads ahead; end(part)
+  template <class F, class E>
+  __device__ __forceinline__ void parts(F&& f, E&& end) const {
+    for (int p = wv; p < nparts; p += NW) {
+      float x[AHEAD][VEC];
 #pragma unroll
-      for (int a = 0; a < A; ++a) fetch(t + a, x[a]);
+      for (int a = 0; a < AHEAD; ++a) fetch(p, a, x[a]);
 #pragma unroll
-      for (int a = 0; a < A; ++a) f(t + a, ((t + a) * THREADS + tid) * VEC, x[a]);
-    }
-    for (; t < ntiles; ++t) {
-      float x[VEC];
-      fetch(t, x);
-      f(t, (t * THREADS + tid) * VEC, x);
+      for (int a = 0; a < AHEAD; ++a) f(p, a, x[a]);
+      end(p);
     }
   }
-  // f(idx, logit) for this lane's elements
+  // f(idx, logit) for this lane's elements, one load at a time (rare passes)
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
-    tiles([&](int, int idx, float (&x)[VEC]) {
+#pragma unroll 1
+    for (int i = wv * AHEAD; i < nparts * AHEAD; i = i % AHEAD == AHEAD - 1 ? i + 1 + (NW - 1) * AHEAD : i + 1) {
+      float x[VEC];
+      fetch(i / AHEAD, i % AHEAD, x);
+      const int idx = index(i / AHEAD, i % AHEAD);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) f(idx + v, x[v]);
-    });
+    }
   }
 
   // First of n sums, in order, whose running sum reaches need(total): sets
@@ -599,27 +650,27 @@ struct BlockRow {
     }
   }
 
-  // Weights of the first n entries of the (sorted) list, into hist.
-  __device__ __forceinline__ void list_weights(int n) {
-    for (int i = tid; i < n; i += THREADS) sh.hist[i] = weight(s, place_value(sh.list[i]));
-    __syncthreads();
-  }
-
-  // The draw from the n <= CAP collected elements, which hold all that can
-  // stay: in rank order for the cuts, then in index order.
-  __device__ __forceinline__ int draw_from_list(int n, float u, int top_k, float top_p) {
+  // Puts the n <= CAP entries of the list in rank order; the position among
+  // the first r of them at which the sum (of weights, or of 1 each) reaches
+  // need, or top_p of the r weights' sum where need is 0.
+  __device__ __forceinline__ int ranked(int n, int r, u64 need, bool by_weight, float top_p) {
     sort_list(n);
-    list_weights(n);
-    int r = min(n, top_k);
-    if (top_p < 1.f) {
-      u64 sum = 0;
-      for (int i = tid; i < r; i += THREADS) sum += sh.hist[i];
-      sum = block_sum(sum);
-      search(r, [&](int i) { return sh.hist[i]; }, [&](u64) { return mass_target(top_p, sum); });
-      r = sh.found + 1;
-      __syncthreads();
+    if (!by_weight) return (int)need - 1;
+    u64 sum = 0;
+    for (int i = tid; i < r; i += THREADS) {
+      const u64 q = weight(s, place_value(sh.list[i]));
+      sh.hist[i] = q;
+      sum += q;
     }
-    // by index; what min-p cuts has no weight
+    sum = block_sum(sum);
+    if (need == 0) need = mass_target(top_p, sum);
+    search(r, [&](int i) { return sh.hist[i]; }, [&](u64) { return need; });
+    const int at = max(sh.found, 0);
+    __syncthreads();
+    return at;
+  }
+  // The draw from the first r entries, all that stays but for min-p.
+  __device__ __forceinline__ int draw_from_list(int r, float u) {
     for (int i = tid; i < r; i += THREADS) {
       const u64 p = sh.list[i];
       sh.list[i] = ((u64)place_index(p) << 32) | order_key(place_value(p));
@@ -628,7 +679,7 @@ struct BlockRow {
     sort_list(r);
     for (int i = tid; i < r; i += THREADS) {
       const u64 q = weight(s, key_value((unsigned)sh.list[i]));
-      sh.hist[i] = q >= s.wmin ? q : 0;
+      sh.hist[i] = (double)q >= s.dmin ? q : 0;
     }
     __syncthreads();
     search(r, [&](int i) { return sh.hist[i]; }, [&](u64 total) { return draw_target(u, total); });
@@ -645,15 +696,17 @@ struct BlockRow {
       top = fmaxf(top, x);
     };
     if constexpr (HELD > 0) {
-      for (int t = 0; t < ntiles; ++t) {
-        float x[VEC];
-        load(t, x);
+      for (int p = wv; p < nparts; p += NW) {
+        float x[AHEAD][VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; v += 4)
-          *reinterpret_cast<float4*>(&sh.held[(t * VEC + v) * THREADS + tid * 4]) =
-              make_float4(x[v], x[v + 1], x[v + 2], x[v + 3]);
+        for (int a = 0; a < AHEAD; ++a) load(p, a, x[a]);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) look(x[v]);
+        for (int a = 0; a < AHEAD; ++a) {
+#pragma unroll
+          for (int v = 0; v < VEC; v += 4) *held(p, a, v) = make_float4(x[a][v], x[a][v + 1], x[a][v + 2], x[a][v + 3]);
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) look(x[a][v]);
+        }
       }
     } else {
       each([&](int, float x) { look(x); });
@@ -686,184 +739,159 @@ struct BlockRow {
     }
     s = scale_for(M, temp, min_p, NB);
     u64 cut = kNoCut;  // what ranks behind it is out
-    int b = NB;        // a bin whose members up to need stay: the cut is there
-    u64 need = 0;
-    bool by_weight = false;
-    if (top_k >= 1 && top_k < V) {
-      clear();
-      each([&](int, float x) {
-        const int q = bin_of<NB>(s, x);
-        if (q < NB - 1) atomicAdd(&sh.hist[q], 1ull);
-      });
-      __syncthreads();
-      search(NB, [&](int i) { return sh.hist[i]; }, [&](u64) { return (u64)top_k; });
-      const int kbin = sh.found;
-      if (kbin >= 0) {  // otherwise all that has weight stays
-        need = (u64)top_k - sh.before;
-        const u64 n = sh.before + sh.hist[kbin];
-        const u64 own = sh.hist[kbin];
+    bool summed = false;
+    // the cut by rank, the cut by mass among what that keeps, or none
+#pragma unroll 1
+    for (int stage = 0; stage < 3; ++stage) {
+      int b = NB;  // the bin that holds the cut; what lies above stays
+      u64 need = 0;
+      bool whole = false;  // the list shall hold all that can stay
+      if (stage < 2) {
+        if (stage == 0 ? !(top_k >= 1 && top_k < V) : !(top_p < 1.f)) continue;
+        clear();
+        parts(
+            [&](int p, int a, float (&x)[VEC]) {
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) {
+                const int q = bin_of<NB>(s, x[v]);
+                if (q < NB - 1 && (cut == kNoCut || place_of(x[v], index(p, a) + v) <= cut))
+                  atomicAdd(&sh.hist[q], stage ? weight(s, x[v]) : 1ull);
+              }
+            },
+            [](int) {});
         __syncthreads();
-        if (n <= CAP) {
-          clear();
-          each([&](int idx, float x) {
-            if (bin_of<NB>(s, x) <= kbin) append(x, idx);
-          });
+        need = search(NB, [&](int i) { return sh.hist[i]; },
+                      [&](u64 total) { return stage ? mass_target(top_p, total) : (u64)top_k; });
+        if (sh.found < 0) {  // all that has weight stays
           __syncthreads();
-          return draw_from_list((int)n, u, top_k, top_p);
+          continue;
         }
-        if (top_p < 1.f) {  // the cut by rank has to be known before the sum
-          auto member = [&](int, float x) { return bin_of<NB>(s, x) == kbin; };
-          cut = members_cut(member, need, false, own <= CAP);
+        b = sh.found;
+        need -= sh.before;
+        whole = stage == 0 && sh.before + sh.hist[b] <= CAP;
+        __syncthreads();
+      } else if (summed) {
+        break;
+      }
+      const u64 kcut = cut;
+      bool known = b == NB;
+      for (;;) {
+        // sums of the parts (exact: 1024 weights); members of bin b are
+        // collected until the cut is known
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        double sum = 0;
+        if (whole) {
+          parts(
+              [&](int p, int a, float (&x)[VEC]) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                  if (bin_of<NB>(s, x[v]) <= b) append(x[v], index(p, a) + v);
+              },
+              [](int) {});
         } else {
-          b = kbin;
-        }
-      }
-      __syncthreads();
-    }
-    if (top_p < 1.f) {
-      clear();
-      each([&](int idx, float x) {
-        const int q = bin_of<NB>(s, x);
-        if (q < NB - 1 && (cut == kNoCut || place_of(x, idx) <= cut)) atomicAdd(&sh.hist[q], weight(s, x));
-      });
-      __syncthreads();
-      const u64 want = search(NB, [&](int i) { return sh.hist[i]; }, [&](u64 total) { return mass_target(top_p, total); });
-      b = sh.found;
-      need = want - sh.before;
-      by_weight = true;
-      __syncthreads();
-    }
-    // sums of the parts; members of bin b are collected instead of summed
-    const u64 kcut = cut;
-    auto inside = [&](int idx, float x) {  // stays, apart from the members of b
-      return kcut == kNoCut || place_of(x, idx) <= kcut;
-    };
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    tiles([&](int t, int idx, float (&x)[VEC]) {
-      u64 sum = 0;
+          parts(
+              [&](int p, int a, float (&x)[VEC]) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        if (!(x[v] > -INFINITY)) continue;
-        if (b < NB || kcut != kNoCut) {
-          const int q = bin_of<NB>(s, x[v]);
-          if (q > b || !inside(idx + v, x[v])) continue;
-          if (q == b) {
-            append(x[v], idx + v);
-            continue;
-          }
+                for (int v = 0; v < VEC; ++v) {
+                  const int q = b == NB ? -1 : bin_of<NB>(s, x[v]);
+                  const double add = weight_if(s, x[v]);
+                  sum += q < b ? add : 0.0;
+                  if (q == b) {
+                    const u64 place = place_of(x[v], index(p, a) + v);
+                    if (known)
+                      sum += place <= cut ? add : 0.0;
+                    else if (place <= kcut)
+                      append(x[v], index(p, a) + v);
+                  }
+                }
+              },
+              [&](int p) {
+                const double q = lane_value(wave_scan(sum), 63);
+                if (lane == 0) sh.part[p] = (u64)q;
+                sum = 0;
+              });
+          summed = true;
         }
-        const u64 q = weight(s, x[v]);
-        sum += q >= s.wmin ? q : 0;
-      }
-      sum = wave_sum(sum);
-      if (lane == 0) sh.part[t * NW + wv] = sum;
-    });
-    __syncthreads();
-    if (b < NB) {
-      const int n = sh.count;
-      __syncthreads();
-      if (n <= CAP) {
-        cut = list_cut(n, need, by_weight);
-        for (int i = tid; i < n; i += THREADS) {
+        __syncthreads();
+        if (known) break;
+        const int n = sh.count;
+        __syncthreads();
+        if (n > CAP) {
+          cut = cut_by_ranges([&](int idx, float x) { return bin_of<NB>(s, x) == b && place_of(x, idx) <= kcut; }, need,
+                              stage);
+          known = true;
+          continue;
+        }
+        const int r = whole ? min(n, top_k) : n;
+        const bool by_weight = whole ? top_p < 1.f : stage;
+        const int at = ranked(n, r, whole ? (by_weight ? 0 : (u64)r) : need, by_weight, top_p);
+        if (whole) return draw_from_list(at + 1, u);
+        cut = sh.list[at];
+        for (int i = tid; i <= at; i += THREADS) {
           const u64 p = sh.list[i];
-          if (p > cut) continue;
           const u64 q = weight(s, place_value(p));
-          if (q < s.wmin) continue;
-          const int vec = place_index(p) / VEC;
-          atomicAdd(&sh.part[vec / 64], q);  // lanes are numbered through the row
+          if ((double)q >= s.dmin) atomicAdd(&sh.part[place_index(p) / PART], q);
         }
-      } else {
-        cut = cut_by_ranges([&](int idx, float x) { return bin_of<NB>(s, x) == b && inside(idx, x); }, need, by_weight);
-        const u64 c = cut;
-        tiles([&](int t, int idx, float (&x)[VEC]) {
-          u64 sum = 0;
-#pragma unroll
-          for (int v = 0; v < VEC; ++v)
-            if (bin_of<NB>(s, x[v]) == b && place_of(x[v], idx + v) <= c) {
-              const u64 q = weight(s, x[v]);
-              sum += q >= s.wmin ? q : 0;
-            }
-          sum = wave_sum(sum);
-          if (lane == 0) sh.part[t * NW + wv] += sum;
-        });
+        __syncthreads();
+        break;
       }
-      __syncthreads();
     }
-    const u64 want = search(ntiles * NW, [&](int i) { return sh.part[i]; },
-                            [&](u64 total) { return draw_target(u, total); });
-    const int slot = sh.found;
-    if (slot >= 0 && slot % NW == wv) {
-      float x[VEC];
-      fetch(slot / NW, x);
-      const int idx = (slot / NW * THREADS + tid) * VEC;
-      u64 q[VEC], own = 0;
+    const u64 want = search(nparts, [&](int i) { return sh.part[i]; }, [&](u64 total) { return draw_target(u, total); });
+    const int p = sh.found;
+    if (p >= 0 && p % NW == wv) {
+      double run = 0;
+      const double left = (double)(want - sh.before);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        q[v] = 0;
-        if (x[v] > -INFINITY && place_of(x[v], idx + v) <= cut) q[v] = weight(s, x[v]);
-        if (q[v] < s.wmin) q[v] = 0;
-        own += q[v];
-      }
-      u64 run = sh.before + wave_scan(own) - own;
+      for (int a = 0; a < AHEAD; ++a) {
+        float x[VEC];
+        fetch(p, a, x);
+        const int idx = index(p, a);
+        double q[VEC], own = 0;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        if (run < want && want <= run + q[v]) sh.id = idx + v;
-        run += q[v];
+        for (int v = 0; v < VEC; ++v) {
+          q[v] = place_of(x[v], idx + v) <= cut ? weight_if(s, x[v]) : 0.0;
+          own += q[v];
+        }
+        const double scan = wave_scan(own);
+        double r = run + scan - own;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if (r < left && left <= r + q[v]) sh.id = idx + v;
+          r += q[v];
+        }
+        run += lane_value(scan, 63);
       }
     }
     __syncthreads();
     return sh.id;
   }
-
-  // The place, in the list of n <= CAP members, at which the sum in rank order
-  // reaches need; leaves the list sorted.
-  __device__ __forceinline__ u64 list_cut(int n, u64 need, bool by_weight) {
-    sort_list(n);
-    if (!by_weight) return sh.list[need - 1];
-    list_weights(n);
-    search(n, [&](int i) { return sh.hist[i]; }, [&](u64) { return need; });
-    const u64 c = sh.list[max(sh.found, 0)];
-    __syncthreads();
-    return c;
-  }
-  template <class W>
-  __device__ __forceinline__ u64 members_cut(W&& which, u64 need, bool by_weight, bool fits) {
-    if (!fits) return cut_by_ranges(which, need, by_weight);
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    each([&](int idx, float x) {
-      if (which(idx, x)) append(x, idx);
-    });
-    __syncthreads();
-    const int n = sh.count;
-    __syncthreads();
-    return list_cut(n, need, by_weight);
-  }
 };
 
 }  // namespace
 
+// Four rows to a workgroup, each wave its own.
 template <int TYPE, int TILES>
-__global__ void __launch_bounds__(64, 4) k_draw_wave(DrawArgs a) {
+__global__ void __launch_bounds__(256, 4) k_draw_wave(DrawArgs a) {
   using R = WaveRow<TYPE, TILES>;
-  __shared__ typename R::SH sh;
-  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-    R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+  __shared__ typename R::SH sh[4];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  for (int64_t n = (int64_t)blockIdx.x * 4 + wave; n < a.N; n += (int64_t)gridDim.x * 4) {
+    R row(sh[wave], static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
     const int id = row.draw(a.u[n], a.temperatures ? a.temperatures[n] : a.temperature,
                             a.top_ks ? a.top_ks[n] : a.top_k, a.top_ps ? a.top_ps[n] : a.top_p,
                             a.min_ps ? a.min_ps[n] : a.min_p, a.V);
-    if (threadIdx.x == 0) a.ids[n] = id;
+    if (row.lane == 0) a.ids[n] = id;
     wave_sync();
   }
 }
 
 template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
-__global__ void __launch_bounds__(THREADS) k_draw_block(DrawArgs a, int ntiles) {
+__global__ void __launch_bounds__(THREADS, 4) k_draw_block(DrawArgs a) {
   using R = BlockRow<TYPE, THREADS, HELD, NB, PARTS>;
   __shared__ typename R::SH sh;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-    R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V, ntiles);
+    R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
     const int id = row.draw(a.u[n], a.temperatures ? a.temperatures[n] : a.temperature,
                             a.top_ks ? a.top_ks[n] : a.top_k, a.top_ps ? a.top_ps[n] : a.top_p,
                             a.min_ps ? a.min_ps[n] : a.min_p);
@@ -876,25 +904,24 @@ size_t draw_workspace(int64_t, int) { return 0; }
 
 template <int TYPE, int TILES>
 static void wave_rows(const DrawArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.N < (1 << 20) ? a.N : (1 << 20));
-  hipLaunchKernelGGL((k_draw_wave<TYPE, TILES>), dim3(grid), dim3(64), 0, s, a);
+  const int64_t blocks = (a.N + 3) / 4;
+  const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : (1 << 20));
+  hipLaunchKernelGGL((k_draw_wave<TYPE, TILES>), dim3(grid), dim3(256), 0, s, a);
 }
 template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
 static void block_rows(const DrawArgs& a, hipStream_t s) {
-  constexpr int tile = THREADS * Logit<TYPE>::VEC;
   const unsigned grid = (unsigned)(a.N < (1 << 20) ? a.N : (1 << 20));
-  hipLaunchKernelGGL((k_draw_block<TYPE, THREADS, HELD, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a,
-                     (a.V + tile - 1) / tile);
+  hipLaunchKernelGGL((k_draw_block<TYPE, THREADS, HELD, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a);
 }
 
 template <int TYPE>
 static void draw_type(const DrawArgs& a, hipStream_t s) {
-  constexpr int VEC = Logit<TYPE>::VEC;
   if (a.V <= 256) return wave_rows<TYPE, 1>(a, s);
   if (a.V <= 1024) return wave_rows<TYPE, 4>(a, s);
-  if (a.V <= 4096) return block_rows<TYPE, 256, 16 / VEC, 1024, 16>(a, s);
-  if (a.V <= 16384) return block_rows<TYPE, 1024, 16 / VEC, 2048, 64>(a, s);
-  return block_rows<TYPE, 1024, 0, 2048, 16384 / VEC>(a, s);
+  if (a.V <= 4096) return block_rows<TYPE, 256, 1, 1024, 4>(a, s);
+  if (a.V <= 16384) return block_rows<TYPE, 1024, 1, 2048, 16>(a, s);
+  if (a.N >= 256 && !getenv("D1024")) return block_rows<TYPE, 512, 0, 2048, 1024>(a, s);
+  return block_rows<TYPE, 1024, 0, 2048, 1024>(a, s);
 }
 
 hipError_t launch_draw(const DrawArgs& a, void*, hipStream_t s) {
