@@ -21,7 +21,6 @@
 #include "gmm_rows.h"
 
 #include <limits.h>
-#include <stdlib.h>
 
 namespace gmm {
 
@@ -167,6 +166,15 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+struct Settings {
+  float u, temp, top_p, min_p;
+  int top_k;
+};
+__device__ __forceinline__ Settings settings_of(const DrawArgs& a, int64_t n) {
+  return {a.u[n], a.temperatures ? a.temperatures[n] : a.temperature, a.top_ps ? a.top_ps[n] : a.top_p,
+          a.min_ps ? a.min_ps[n] : a.min_p, a.top_ks ? a.top_ks[n] : a.top_k};
+}
+
 // What a row's settings amount to once its largest logit is known.
 struct Scale {
   double M, c;   // largest logit; log2(e) / T
@@ -218,8 +226,10 @@ __device__ __forceinline__ u64 mass_target(float top_p, u64 total) {
 // Short rows, V <= 256 TILES: one wave to a row, 4 TILES logits in each lane's
 // registers (element idx = tile * 256 + 4 lane + v).  Weights are evaluated
 // where they are used, once for the draw and once more for top-p: kept, they
-// would take half of the registers that let 5 waves run on a SIMD.
-template <int TYPE, int TILES>
+// would take half of the registers that let 4 waves run on a SIMD.  Rows with
+// no cut by rank or mass need far fewer registers (CUTS = false), and what
+// bounds them is how many rows are under way.
+template <int TYPE, int TILES, bool CUTS>
 struct WaveRow {
   using T = typename Logit<TYPE>::T;
   static constexpr int PER = 4 * TILES, NB = 256, CAP = 64;
@@ -233,7 +243,8 @@ struct WaveRow {
   float x[PER];
   Scale s;
 
-  __device__ __forceinline__ WaveRow(SH& sh_, const T* z, int V) : sh(sh_), lane(threadIdx.x & 63) {
+  __device__ __forceinline__ WaveRow(SH& sh_, int) : sh(sh_), lane(threadIdx.x & 63) {}
+  __device__ __forceinline__ void load(const T* z, int V) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       const int idx = t * 256 + 4 * lane;
@@ -366,7 +377,7 @@ struct WaveRow {
     s = scale_for(M, temp, min_p, NB);
     unsigned in = (1u << (PER - 1) << 1) - 1u;  // the elements that stay
 #pragma unroll 1
-    for (int mass = 0; mass < 2; ++mass) {  // first the cut by rank, then by mass
+    for (int mass = 0; CUTS && mass < 2; ++mass) {  // first the cut by rank, then by mass
       if (mass ? !(top_p < 1.f) : !(top_k >= 1 && top_k < V)) continue;
       fresh();
       clear();
@@ -466,11 +477,12 @@ struct BlockRow {
   SH& sh;
   const T* z;
   const int V, nparts, tid, lane, wv;
+  int p0, p1;  // the parts that a pass goes over: all of them unless the row is split
   Scale s;
 
   __device__ __forceinline__ BlockRow(SH& sh_, const T* row, int v)
       : sh(sh_), z(row), V(v), nparts((v + PART - 1) / PART), tid(threadIdx.x), lane(threadIdx.x & 63),
-        wv(__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)) {}
+        wv(__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)), p0(0), p1(nparts) {}
 
   // first of this lane's elements in load a of part p
   __device__ __forceinline__ int index(int p, int a) const { return (p * AHEAD + a) * (64 * VEC) + lane * VEC; }
@@ -504,7 +516,7 @@ struct BlockRow {
   // f(part, load, logits) for this wave's parts, a part's loads ahead; end(part)
   template <class F, class E>
   __device__ __forceinline__ void parts(F&& f, E&& end) const {
-    for (int p = wv; p < nparts; p += NW) {
+    for (int p = p0 + wv; p < p1; p += NW) {
       float x[AHEAD][VEC];
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) fetch(p, a, x[a]);
@@ -517,7 +529,7 @@ struct BlockRow {
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
 #pragma unroll 1
-    for (int i = wv * AHEAD; i < nparts * AHEAD; i = i % AHEAD == AHEAD - 1 ? i + 1 + (NW - 1) * AHEAD : i + 1) {
+    for (int i = (p0 + wv) * AHEAD; i < p1 * AHEAD; i = i % AHEAD == AHEAD - 1 ? i + 1 + (NW - 1) * AHEAD : i + 1) {
       float x[VEC];
       fetch(i / AHEAD, i % AHEAD, x);
       const int idx = index(i / AHEAD, i % AHEAD);
@@ -575,11 +587,11 @@ struct BlockRow {
     if (tid == 0) sh.count = 0;
     __syncthreads();
   }
-  // Appends an element to the list (in any order; entries past CAP are only
+  // Appends an element to a list (in any order; entries past CAP are only
   // counted).
-  __device__ __forceinline__ void append(float x, int idx) {
-    const int at = atomicAdd(&sh.count, 1);
-    if (at < CAP) sh.list[at] = place_of(x, idx);
+  static __device__ __forceinline__ void append(int& count, u64* list, float x, int idx) {
+    const int at = atomicAdd(&count, 1);
+    if (at < CAP) list[at] = place_of(x, idx);
   }
 
   // Sorts the first n <= CAP entries of the list, ascending (bitonic).  Pairs
@@ -688,7 +700,8 @@ struct BlockRow {
     return id;
   }
 
-  __device__ __forceinline__ int draw(float u, float temp, int top_k, float top_p, float min_p) {
+  // The largest logit of the parts (on every lane), NaN if one is NaN or +inf.
+  __device__ __forceinline__ float largest() {
     float top = -INFINITY;
     bool bad = false;
     auto look = [&](float x) {
@@ -709,7 +722,12 @@ struct BlockRow {
         }
       }
     } else {
-      each([&](int, float x) { look(x); });
+      parts(
+          [&](int, int, float (&x)[VEC]) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) look(x[v]);
+          },
+          [](int) {});
     }
     top = wave_max(top);
     const unsigned any = __ballot(bad) != 0;
@@ -724,19 +742,224 @@ struct BlockRow {
       top = fmaxf(top, sh.top[q]);
       fault |= sh.bad[q];
     }
-    const float M = top;
-    if (fault || !(M > -INFINITY)) return -1;
-    if (!(temp > 0.f)) {  // the largest logit, lowest index first
-      if (tid == 0) sh.id = INT_MAX;
+    return fault ? __builtin_nanf("") : top;
+  }
+  // The first index of the logit M among the parts, INT_MAX if none.
+  __device__ __forceinline__ int first_of(float M) {
+    if (tid == 0) sh.id = INT_MAX;
+    __syncthreads();
+    int first = INT_MAX;
+    each([&](int idx, float x) {
+      if (x == M) first = min(first, idx);
+    });
+    if (first != INT_MAX) atomicMin(&sh.id, first);
+    __syncthreads();
+    return sh.id;
+  }
+  // The first histogram of the parts: of counts, or of the weights of what the
+  // cut so far keeps.
+  __device__ __forceinline__ void histogram(bool by_weight, u64 cut) {
+    clear();
+    parts(
+        [&](int p, int a, float (&x)[VEC]) {
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const int q = bin_of<NB>(s, x[v]);
+            if (q < NB - 1 && (cut == kNoCut || place_of(x[v], index(p, a) + v) <= cut))
+              atomicAdd(&sh.hist[q], by_weight ? weight(s, x[v]) : 1ull);
+          }
+        },
+        [](int) {});
+    __syncthreads();
+  }
+  // Collects the elements of the parts up to bin b.
+  __device__ __forceinline__ void collect(int b, int& count, u64* list) {
+    parts(
+        [&](int p, int a, float (&x)[VEC]) {
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (bin_of<NB>(s, x[v]) <= b) append(count, list, x[v], index(p, a) + v);
+        },
+        [](int) {});
+  }
+  // The sums of the parts over the bins in front of b, all if b is NB (exact:
+  // 1024 weights).  The members of bin b up to kcut are collected, or, where
+  // the cut is known, added up to it.
+  __device__ __forceinline__ void sum_parts(int b, u64 kcut, bool known, u64 cut, int& count, u64* list, u64* part) {
+    double sum = 0;
+    parts(
+        [&](int p, int a, float (&x)[VEC]) {
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const int q = b == NB ? -1 : bin_of<NB>(s, x[v]);
+            const double add = weight_if(s, x[v]);
+            sum += q < b ? add : 0.0;
+            if (q == b) {
+              const u64 place = place_of(x[v], index(p, a) + v);
+              if (known)
+                sum += place <= cut ? add : 0.0;
+              else if (place <= kcut)
+                append(count, list, x[v], index(p, a) + v);
+            }
+          }
+        },
+        [&](int p) {
+          const double q = lane_value(wave_scan(sum), 63);
+          if (lane == 0) part[p] = (u64)q;
+          sum = 0;
+        });
+  }
+  // From the n <= CAP entries of the list.  whole: they are all that can stay
+  // by rank; the draw from them.  Otherwise the members of the cut's bin: sets
+  // the cut, adds what stays of them to the parts' sums, and returns -2.
+  // Up to 512 entries the lanes count what ranks in front of each (a bitonic
+  // sort of 95 entries takes 12000 cycles, most of them waits between its
+  // steps); more are sorted.
+  __device__ __forceinline__ int from_list(int n, bool whole, u64 need, bool by_weight, float u, int top_k, float top_p,
+                                           u64& cut) {
+    if (n <= 512 && n <= THREADS) {
+      // L lanes for the entries, G groups of them that each look at a share
+      int L = 64;
+      while (L < n) L <<= 1;
+      const int G = THREADS / L, i = tid & (L - 1), group = tid / L;
+      const int share = (n + G - 1) / G, j0 = min(n, group * share), j1 = min(n, j0 + share);
+      struct Entry {
+        u64 place;
+        double w;
+      };
+      Entry* const es = reinterpret_cast<Entry*>(sh.hist);        // L entries (sums of up to 512 weights are exact),
+      double* const sums = reinterpret_cast<double*>(es + L);     // THREADS sums,
+      int* const ranks = reinterpret_cast<int*>(sums + THREADS);  // THREADS counts
+      static_assert(NB * 8 >= (THREADS < 512 ? THREADS : 512) * 16 + THREADS * 12 || NB < 2048 || THREADS > 512, "fit");
+      const bool mine = group == 0 && i < n;
+      const u64 own = i < n ? sh.list[i] : kNoCut;
+      const double w = i < n ? (double)weight(s, place_value(own)) : 0.0;
+      if (group == 0) es[i] = {own, w};
+      if (tid == 0) sh.id = -1;
       __syncthreads();
-      int first = INT_MAX;
-      each([&](int idx, float x) {
-        if (x == M) first = min(first, idx);
-      });
-      if (first != INT_MAX) atomicMin(&sh.id, first);
+      int rank = 0;
+      double before = 0;
+      if ((i & ~63) < n) {  // waves without an entry have nothing to count
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) {
+          const Entry e = es[j];
+          const bool front = e.place < own;
+          rank += front;
+          before += front ? e.w : 0.0;
+        }
+      }
+      sums[tid] = before;
+      ranks[tid] = rank;
+      __syncthreads();
+      if (mine)
+        for (int g = 1; g < G; ++g) {
+          rank += ranks[g * L + i];
+          before += sums[g * L + i];
+        }
+      const int idx = place_index(own);
+      if (!whole) {
+        const bool stay = mine && (by_weight ? before < (double)need : (u64)rank < need);
+        if (stay && (by_weight ? (double)need <= before + w : (u64)rank + 1 == need)) sh.before = own;
+        if (stay && w >= s.dmin) atomicAdd(&sh.part[idx / PART], (u64)w);
+        __syncthreads();
+        cut = sh.before;
+        return -2;
+      }
+      bool stay = mine && rank < top_k;
+      if (top_p < 1.f) {  // an entry that ranks below top_k has only such entries in front of it
+        const u64 sum = block_sum(stay ? (u64)w : 0);
+        stay = stay && before < (double)mass_target(top_p, sum);
+      }
+      // what stays, close together: (index, weight)
+      const double q = stay && w >= s.dmin ? w : 0.0;
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      if (q > 0) es[atomicAdd(&sh.count, 1)] = {(u64)idx, q};
+      __syncthreads();
+      const int m = sh.count;
+      if (tid < m) {
+        const Entry me = es[tid];
+        double total = 0;
+        before = 0;
+#pragma unroll 4
+        for (int j = 0; j < m; ++j) {
+          const Entry e = es[j];
+          total += e.w;
+          before += e.place < me.place ? e.w : 0.0;
+        }
+        const double want = (double)draw_target(u, (u64)total);
+        if (before < want && want <= before + me.w) sh.id = (int)me.place;
+      }
       __syncthreads();
       return sh.id;
     }
+    const int r = whole ? min(n, top_k) : n;
+    if (whole) {
+      by_weight = top_p < 1.f;
+      need = by_weight ? 0 : (u64)r;
+    }
+    const int at = ranked(n, r, need, by_weight, top_p);
+    if (whole) return draw_from_list(at + 1, u);
+    cut = sh.list[at];
+    for (int i = tid; i <= at; i += THREADS) {
+      const u64 p = sh.list[i];
+      const u64 q = weight(s, place_value(p));
+      if ((double)q >= s.dmin) atomicAdd(&sh.part[place_index(p) / PART], q);
+    }
+    __syncthreads();
+    return -2;
+  }
+  // The draw from the parts' sums (each wave looks for the part by itself).
+  __device__ __forceinline__ int from_parts(u64 cut, float u) {
+    const int per = (nparts + 63) / 64, i0 = min(nparts, lane * per), i1 = min(nparts, i0 + per);
+    u64 own = 0;
+    for (int i = i0; i < i1; ++i) own += sh.part[i];
+    const u64 scan = wave_scan(own);
+    const u64 want = draw_target(u, lane_value(scan, 63));
+    u64 run = scan - own;
+    int at = -1;
+    u64 left = 0;
+    for (int i = i0; i < i1; ++i) {
+      const u64 q = sh.part[i];
+      if (run < want && want <= run + q) at = i, left = want - run;
+      run += q;
+    }
+    const u64 who = __ballot(at >= 0);
+    const int l = __ffsll(who) - 1;
+    const int p = __builtin_amdgcn_readlane(at, l);
+    if (wv == p % NW) {
+      const double reach = (double)lane_value(left, l);
+      float x[AHEAD][VEC];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) fetch(p, a, x[a]);
+      double sum = 0;
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int idx = index(p, a);
+        double q[VEC], mine = 0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          q[v] = behind(x[a][v], idx + v, cut) ? 0.0 : weight_if(s, x[a][v]);
+          mine += q[v];
+        }
+        const double up = wave_scan(mine);
+        double r = sum + up - mine;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if (r < reach && reach <= r + q[v]) sh.id = idx + v;
+          r += q[v];
+        }
+        sum += lane_value(up, 63);
+      }
+    }
+    __syncthreads();
+    return sh.id;
+  }
+
+  __device__ __forceinline__ int draw(float u, float temp, int top_k, float top_p, float min_p) {
+    const float M = largest();
+    if (!(M > -INFINITY)) return -1;
+    if (!(temp > 0.f)) return first_of(M);
     s = scale_for(M, temp, min_p, NB);
     u64 cut = kNoCut;  // what ranks behind it is out
     bool summed = false;
@@ -748,18 +971,7 @@ struct BlockRow {
       bool whole = false;  // the list shall hold all that can stay
       if (stage < 2) {
         if (stage == 0 ? !(top_k >= 1 && top_k < V) : !(top_p < 1.f)) continue;
-        clear();
-        parts(
-            [&](int p, int a, float (&x)[VEC]) {
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) {
-                const int q = bin_of<NB>(s, x[v]);
-                if (q < NB - 1 && (cut == kNoCut || place_of(x[v], index(p, a) + v) <= cut))
-                  atomicAdd(&sh.hist[q], stage ? weight(s, x[v]) : 1ull);
-              }
-            },
-            [](int) {});
-        __syncthreads();
+        histogram(stage, cut);
         need = search(NB, [&](int i) { return sh.hist[i]; },
                       [&](u64 total) { return stage ? mass_target(top_p, total) : (u64)top_k; });
         if (sh.found < 0) {  // all that has weight stays
@@ -776,114 +988,89 @@ struct BlockRow {
       const u64 kcut = cut;
       bool known = b == NB;
       for (;;) {
-        // sums of the parts (exact: 1024 weights); members of bin b are
-        // collected until the cut is known
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        double sum = 0;
-        if (whole) {
-          parts(
-              [&](int p, int a, float (&x)[VEC]) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                  if (bin_of<NB>(s, x[v]) <= b) append(x[v], index(p, a) + v);
-              },
-              [](int) {});
-        } else {
-          parts(
-              [&](int p, int a, float (&x)[VEC]) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                  const int q = b == NB ? -1 : bin_of<NB>(s, x[v]);
-                  const double add = weight_if(s, x[v]);
-                  sum += q < b ? add : 0.0;
-                  if (q == b) {
-                    const u64 place = place_of(x[v], index(p, a) + v);
-                    if (known)
-                      sum += place <= cut ? add : 0.0;
-                    else if (place <= kcut)
-                      append(x[v], index(p, a) + v);
-                  }
-                }
-              },
-              [&](int p) {
-                const double q = lane_value(wave_scan(sum), 63);
-                if (lane == 0) sh.part[p] = (u64)q;
-                sum = 0;
-              });
-          summed = true;
-        }
+        if (whole)
+          collect(b, sh.count, sh.list);
+        else
+          sum_parts(b, kcut, known, cut, sh.count, sh.list, sh.part);
+        summed = true;
         __syncthreads();
         if (known) break;
         const int n = sh.count;
         __syncthreads();
-        if (n > CAP) {
-          cut = cut_by_ranges([&](int idx, float x) { return bin_of<NB>(s, x) == b && place_of(x, idx) <= kcut; }, need,
-                              stage);
-          known = true;
-          continue;
+        if (n <= CAP) {
+          const int id = from_list(n, whole, need, stage, u, top_k, top_p, cut);
+          if (whole) return id;
+          break;
         }
-        const int r = whole ? min(n, top_k) : n;
-        const bool by_weight = whole ? top_p < 1.f : stage;
-        const int at = ranked(n, r, whole ? (by_weight ? 0 : (u64)r) : need, by_weight, top_p);
-        if (whole) return draw_from_list(at + 1, u);
-        cut = sh.list[at];
-        for (int i = tid; i <= at; i += THREADS) {
-          const u64 p = sh.list[i];
-          const u64 q = weight(s, place_value(p));
-          if ((double)q >= s.dmin) atomicAdd(&sh.part[place_index(p) / PART], q);
-        }
-        __syncthreads();
-        break;
+        cut = cut_by_ranges([&](int idx, float x) { return bin_of<NB>(s, x) == b && place_of(x, idx) <= kcut; }, need,
+                            stage);
+        known = true;
       }
     }
-    const u64 want = search(nparts, [&](int i) { return sh.part[i]; }, [&](u64 total) { return draw_target(u, total); });
-    const int p = sh.found;
-    if (p >= 0 && p % NW == wv) {
-      double run = 0;
-      const double left = (double)(want - sh.before);
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a) {
-        float x[VEC];
-        fetch(p, a, x);
-        const int idx = index(p, a);
-        double q[VEC], own = 0;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          q[v] = place_of(x[v], idx + v) <= cut ? weight_if(s, x[v]) : 0.0;
-          own += q[v];
-        }
-        const double scan = wave_scan(own);
-        double r = run + scan - own;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          if (r < left && left <= r + q[v]) sh.id = idx + v;
-          r += q[v];
-        }
-        run += lane_value(scan, 63);
-      }
-    }
-    __syncthreads();
-    return sh.id;
+    return from_parts(cut, u);
   }
+};
+
+// ---------------------------------------------------------------------------
+// Few long rows: each is split over several workgroups, in three launches
+// (largest logit; histogram; sums and lists), and a fourth, one workgroup to a
+// row, makes the draw.  What they share lies in the workspace.  (Left to the
+// last workgroup of the third launch to finish, the draw took longer: the
+// device-wide fences that this needs cost 10 to 40 us.)
+constexpr int kSplitThreads = 256, kSplitBins = 2048, kSplitParts = 1024, kMostSplits = 256;
+enum Finish { kNone, kGreedy, kFromParts, kFromList, kWholeList, kAlone };
+struct Split {
+  u64 hist[kSplitBins];
+  u64 list[kSplitBins];
+  u64 part[kSplitParts];
+  float top[kMostSplits];
+  u64 need;                // what the list's sum has to reach
+  int count, first, b, how;  // list entries; index of the largest logit; bin of the cut; Finish
 };
 
 }  // namespace
 
-// Four rows to a workgroup, each wave its own.
-template <int TYPE, int TILES>
-__global__ void __launch_bounds__(256, 4) k_draw_wave(DrawArgs a) {
-  using R = WaveRow<TYPE, TILES>;
-  __shared__ typename R::SH sh[4];
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  for (int64_t n = (int64_t)blockIdx.x * 4 + wave; n < a.N; n += (int64_t)gridDim.x * 4) {
-    R row(sh[wave], static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
-    const int id = row.draw(a.u[n], a.temperatures ? a.temperatures[n] : a.temperature,
-                            a.top_ks ? a.top_ks[n] : a.top_k, a.top_ps ? a.top_ps[n] : a.top_p,
-                            a.min_ps ? a.min_ps[n] : a.min_p, a.V);
-    if (row.lane == 0) a.ids[n] = id;
-    wave_sync();
+// A wave takes `batch` consecutive rows (at most 16), whose settings its lanes
+// read at once.  CUTS = false takes the rows without a cut by rank or mass, the
+// next one's logits on their way meanwhile; true takes the others, or all where
+// it runs alone.
+template <int TYPE, int TILES, bool CUTS>
+__global__ void __launch_bounds__(256, CUTS ? 4 : 5) k_draw_wave(DrawArgs a, int batch, int alone) {
+  using R = WaveRow<TYPE, TILES, CUTS>;
+  __shared__ typename R::SH sh[CUTS ? 4 : 1];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * batch;
+  const int rows = (int)min((int64_t)batch, a.N - n0);
+  if (rows <= 0) return;
+  const Settings set = settings_of(a, n0 + min(lane, rows - 1));
+  const bool cuts = (set.top_k >= 1 && set.top_k < a.V) || set.top_p < 1.f;
+  u64 todo = __ballot(lane < rows && (alone || cuts == CUTS));
+  if (!todo) return;
+  const typename R::T* z = static_cast<const typename R::T*>(a.z) + n0 * a.ld;
+  R row(sh[CUTS ? wave : 0], a.V);
+  row.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
+  int ids = 0;
+  const u64 all = todo;
+  while (todo) {
+    const int r = __ffsll(todo) - 1;
+    todo &= todo - 1;
+    R next(sh[CUTS ? wave : 0], a.V);
+    if (!CUTS && todo) next.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
+    const auto of = [&](float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), r)); };
+    const int id = row.draw(of(set.u), of(set.temp), __builtin_amdgcn_readlane(set.top_k, r), of(set.top_p), of(set.min_p),
+                            a.V);
+    if (lane == r) ids = id;
+    if (CUTS) {
+      wave_sync();
+      if (todo) row.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::PER; ++i) row.x[i] = next.x[i];
+    }
   }
+  if ((all >> lane) & 1) a.ids[n0 + lane] = ids;
 }
 
 template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
@@ -900,13 +1087,195 @@ __global__ void __launch_bounds__(THREADS, 4) k_draw_block(DrawArgs a) {
   }
 }
 
-size_t draw_workspace(int64_t, int) { return 0; }
+template <int TYPE>
+using SplitOf = BlockRow<TYPE, kSplitThreads, 0, kSplitBins, kSplitParts>;
+
+// Workgroup b of the launch: part range b % S of row b / S.
+template <int TYPE>
+__device__ __forceinline__ void take_range(SplitOf<TYPE>& row, int S) {
+  const int per = (row.nparts + S - 1) / S, b = (int)(blockIdx.x % S);
+  row.p0 = min(row.nparts, b * per);
+  row.p1 = min(row.nparts, row.p0 + per);
+}
+// The row's largest logit from its workgroups' (NaN if one is NaN).
+template <class R>
+__device__ __forceinline__ float shared_largest(R& row, const Split& sp, int S) {
+  float top = -INFINITY;
+  bool bad = false;
+  for (int i = row.lane; i < S; i += 64) {
+    const float t = sp.top[i];
+    bad |= t != t;
+    top = fmaxf(top, t);
+  }
+  top = wave_max(top);
+  return __ballot(bad) ? __builtin_nanf("") : top;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kSplitThreads) k_draw_split_top(DrawArgs a, Split* ws, int S) {
+  using R = SplitOf<TYPE>;
+  __shared__ typename R::SH sh;
+  const int n = (int)(blockIdx.x / S), b = (int)(blockIdx.x % S);
+  Split& sp = ws[n];
+  R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+  take_range<TYPE>(row, S);
+  const float top = row.largest();
+  for (int i = b * kSplitThreads + row.tid; i < kSplitBins; i += S * kSplitThreads) sp.hist[i] = 0;
+  if (row.tid == 0) {
+    sp.top[b] = top;
+    if (b == 0) {
+      sp.count = 0;
+      sp.first = INT_MAX;
+    }
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kSplitThreads) k_draw_split_hist(DrawArgs a, Split* ws, int S) {
+  using R = SplitOf<TYPE>;
+  __shared__ typename R::SH sh;
+  const int n = (int)(blockIdx.x / S);
+  Split& sp = ws[n];
+  const Settings set = settings_of(a, n);
+  const bool by_rank = set.top_k >= 1 && set.top_k < a.V;
+  if (!(set.temp > 0.f) || !(by_rank || set.top_p < 1.f)) return;
+  R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+  const float M = shared_largest(row, sp, S);
+  if (!(M > -INFINITY)) return;
+  take_range<TYPE>(row, S);
+  row.s = scale_for(M, set.temp, set.min_p, kSplitBins);
+  row.histogram(!by_rank, kNoCut);
+  for (int i = row.tid; i < kSplitBins; i += kSplitThreads) {
+    const u64 q = sh.hist[i];
+    if (q) atomicAdd(&sp.hist[i], q);
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kSplitThreads) k_draw_split_sum(DrawArgs a, Split* ws, int S) {
+  using R = SplitOf<TYPE>;
+  __shared__ typename R::SH sh;
+  const int n = (int)(blockIdx.x / S);
+  Split& sp = ws[n];
+  const Settings set = settings_of(a, n);
+  R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+  const float M = shared_largest(row, sp, S);
+  const bool by_rank = set.top_k >= 1 && set.top_k < a.V, by_mass = set.top_p < 1.f;
+  int how = kNone, b = kSplitBins;  // the same in each of the row's workgroups
+  u64 need = 0;
+  take_range<TYPE>(row, S);
+  if (M > -INFINITY && !(set.temp > 0.f)) {
+    how = kGreedy;
+    const int first = row.first_of(M);
+    if (row.tid == 0 && first != INT_MAX) atomicMin(&sp.first, first);
+  } else if (M > -INFINITY) {
+    how = kFromParts;
+    row.s = scale_for(M, set.temp, set.min_p, kSplitBins);
+    if (by_rank || by_mass) {
+      need = row.search(kSplitBins, [&](int i) { return sp.hist[i]; },
+                        [&](u64 total) { return by_rank ? (u64)set.top_k : mass_target(set.top_p, total); });
+      if (sh.found >= 0) {
+        b = sh.found;
+        need -= sh.before;
+        // a cut by rank that leaves more than a list holds, and then one by mass: not decided by one histogram
+        how = !by_rank ? kFromList : sh.before + sp.hist[b] <= (u64)R::CAP ? kWholeList : by_mass ? kAlone : kFromList;
+      } else if (by_mass) {
+        how = kAlone;  // by rank all stays, and the histogram was by rank
+      }
+      __syncthreads();
+    }
+    if (row.tid == 0) sh.count = 0;
+    __syncthreads();
+    if (how == kWholeList)
+      row.collect(b, sh.count, sh.list);
+    else if (how != kAlone)
+      row.sum_parts(b, kNoCut, b == kSplitBins, kNoCut, sh.count, sh.list, sp.part);
+    __syncthreads();
+    // this workgroup's entries into the row's list, at a place taken at once
+    const int count = sh.count;
+    if (row.tid == 0) sh.found = count ? atomicAdd(&sp.count, count) : 0;
+    __syncthreads();
+    const int at = sh.found;
+    for (int i = row.tid; i < min(count, R::CAP - at); i += kSplitThreads) sp.list[at + i] = sh.list[i];
+  }
+  if (blockIdx.x % S == 0 && row.tid == 0) {
+    sp.need = need;
+    sp.b = b;
+    sp.how = how;
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Split* ws, int S) {
+  using R = BlockRow<TYPE, 1024, 0, kSplitBins, kSplitParts>;
+  __shared__ typename R::SH sh;
+  const int n = (int)blockIdx.x;
+  const Split& sp = ws[n];
+  const Settings set = settings_of(a, n);
+  R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
+  int how = sp.how, id = -1;
+  const int count = sp.count;
+  if (count > R::CAP) how = kAlone;
+  if (how == kGreedy) {
+    id = sp.first;
+  } else if (how == kAlone) {
+    id = row.draw(set.u, set.temp, set.top_k, set.top_p, set.min_p);
+  } else if (how != kNone) {
+    row.s = scale_for(shared_largest(row, sp, S), set.temp, set.min_p, kSplitBins);
+    for (int i = row.tid; i < count; i += 1024) sh.list[i] = sp.list[i];
+    if (how != kWholeList)
+      for (int i = row.tid; i < row.nparts; i += 1024) sh.part[i] = sp.part[i];
+    __syncthreads();
+    u64 cut = kNoCut;
+    const bool by_rank = set.top_k >= 1 && set.top_k < a.V;
+    if (how != kFromParts) id = row.from_list(count, how == kWholeList, sp.need, !by_rank, set.u, set.top_k, set.top_p, cut);
+    if (how != kWholeList) id = row.from_parts(cut, set.u);
+  }
+  if (row.tid == 0) a.ids[n] = id;
+}
+
+// Workgroups to a row of the split, 0 where rows are not split: at least 4
+// parts (4096 logits) each, and no more in all than two to a CU.
+static int splits_of(int64_t N, int V) {
+  if (V <= 16384 || N > 128) return 0;
+  const int nparts = (V + 1023) / 1024;
+  const int64_t a = (nparts + 3) / 4, b = 512 / N;
+  const int64_t S = a < b ? a : b;
+  return (int)(S < kMostSplits ? S : kMostSplits);
+}
+
+size_t draw_workspace(int64_t N, int V) { return splits_of(N, V) ? (size_t)N * sizeof(Split) : 0; }
+
+template <int TYPE>
+static hipError_t split_rows(const DrawArgs& a, void* workspace, int S, hipStream_t s) {
+  Split* ws = static_cast<Split*>(workspace);
+  const dim3 g((unsigned)(a.N * S)), t(kSplitThreads);
+  hipLaunchKernelGGL(k_draw_split_top<TYPE>, g, t, 0, s, a, ws, S);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_draw_split_hist<TYPE>, g, t, 0, s, a, ws, S);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_draw_split_sum<TYPE>, g, t, 0, s, a, ws, S);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_draw_split_pick<TYPE>, dim3((unsigned)a.N), dim3(1024), 0, s, a, (const Split*)ws, S);
+  return hipGetLastError();
+}
+
 
 template <int TYPE, int TILES>
 static void wave_rows(const DrawArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.N + 3) / 4;
-  const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : (1 << 20));
-  hipLaunchKernelGGL((k_draw_wave<TYPE, TILES>), dim3(grid), dim3(256), 0, s, a);
+  // enough rows to a wave that 4096 waves (4 to a SIMD) take them all, 16 at most
+  const int batch = (int)(a.N / 4096 < 1 ? 1 : a.N / 4096 > 16 ? 16 : a.N / 4096);
+  const int64_t waves = (a.N + batch - 1) / batch;
+  const dim3 g((unsigned)((waves + 3) / 4)), t(256);
+  const bool rank = a.top_ks || (a.top_k >= 1 && a.top_k < a.V), mass = a.top_ps || a.top_p < 1.f;
+  // settings in device memory are known there only: both kernels look at them
+  // (where there are few rows, a second launch costs more than it saves)
+  const bool device = a.top_ks || a.top_ps, both = device && a.N >= 4096;
+  if ((!rank && !mass) || both) hipLaunchKernelGGL((k_draw_wave<TYPE, TILES, false>), g, t, 0, s, a, batch, 0);
+  if (rank || mass) hipLaunchKernelGGL((k_draw_wave<TYPE, TILES, true>), g, t, 0, s, a, batch, !both);
 }
 template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
 static void block_rows(const DrawArgs& a, hipStream_t s) {
@@ -915,23 +1284,25 @@ static void block_rows(const DrawArgs& a, hipStream_t s) {
 }
 
 template <int TYPE>
-static void draw_type(const DrawArgs& a, hipStream_t s) {
-  if (a.V <= 256) return wave_rows<TYPE, 1>(a, s);
-  if (a.V <= 1024) return wave_rows<TYPE, 4>(a, s);
-  if (a.V <= 4096) return block_rows<TYPE, 256, 1, 1024, 4>(a, s);
-  if (a.V <= 16384) return block_rows<TYPE, 1024, 1, 2048, 16>(a, s);
-  if (a.N >= 256 && !getenv("D1024")) return block_rows<TYPE, 512, 0, 2048, 1024>(a, s);
-  return block_rows<TYPE, 1024, 0, 2048, 1024>(a, s);
+static hipError_t draw_type(const DrawArgs& a, void* workspace, hipStream_t s) {
+  if (const int S = splits_of(a.N, a.V)) return split_rows<TYPE>(a, workspace, S, s);
+  if (a.V <= 256)
+    wave_rows<TYPE, 1>(a, s);
+  else if (a.V <= 1024)
+    wave_rows<TYPE, 4>(a, s);
+  else if (a.V <= 4096)
+    block_rows<TYPE, 256, 1, 1024, 4>(a, s);
+  else if (a.V <= 16384)
+    block_rows<TYPE, 1024, 1, 2048, 16>(a, s);
+  else
+    block_rows<TYPE, 512, 0, 2048, 1024>(a, s);
+  return hipGetLastError();
 }
 
-hipError_t launch_draw(const DrawArgs& a, void*, hipStream_t s) {
-  if (a.type == kFloat)
-    draw_type<kFloat>(a, s);
-  else if (a.type == kBfloat)
-    draw_type<kBfloat>(a, s);
-  else
-    draw_type<kHalf>(a, s);
-  return hipGetLastError();
+hipError_t launch_draw(const DrawArgs& a, void* workspace, hipStream_t s) {
+  if (a.type == kFloat) return draw_type<kFloat>(a, workspace, s);
+  if (a.type == kBfloat) return draw_type<kBfloat>(a, workspace, s);
+  return draw_type<kHalf>(a, workspace, s);
 }
 
 }  // namespace gmm
