@@ -193,7 +193,7 @@ __device__ __forceinline__ Scale scale_for(float M, float temp, float min_p, int
   s.M = uniform((double)M);
   s.c = uniform(1.44269504088896340736 / (double)temp);
   s.half = uniform(0.5f * M);
-  s.bs = uniform((float)(nb - 1) / (15.f * temp));
+  s.bs = uniform(fminf((float)(nb - 1) / (15.f * temp), 3e38f));  // finite: 0 stays in bin 0 whatever T is
   s.dmin = uniform(min_p > 0.f ? ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1.0);
   return s;
 }
@@ -201,7 +201,7 @@ __device__ __forceinline__ u64 weight(const Scale& s, float x) {
   return (u64)__double_as_longlong(fixed_exp2_up(((double)x - s.M) * s.c)) & 0xFFFFFFFFFFFFFull;
 }
 // The same as a float64, in which sums of up to 2048 weights are exact; 0 if
-// it is below wmin.
+// it is below dmin.
 __device__ __forceinline__ double weight_if(const Scale& s, float x) {
   const double q = fixed_exp2_up(((double)x - s.M) * s.c) - kOnes;
   return q >= s.dmin ? q : 0.0;
@@ -830,7 +830,8 @@ struct BlockRow {
       Entry* const es = reinterpret_cast<Entry*>(sh.hist);        // L entries (sums of up to 512 weights are exact),
       double* const sums = reinterpret_cast<double*>(es + L);     // THREADS sums,
       int* const ranks = reinterpret_cast<int*>(sums + THREADS);  // THREADS counts
-      static_assert(NB * 8 >= (THREADS < 512 ? THREADS : 512) * 16 + THREADS * 12 || NB < 2048 || THREADS > 512, "fit");
+      static_assert(sizeof sh.hist + sizeof sh.list >= (THREADS < 512 ? THREADS : 512) * 16 + THREADS * 12,
+                    "these lie over hist and, once its entries are read, over list, which follows it");
       const bool mine = group == 0 && i < n;
       const u64 own = i < n ? sh.list[i] : kNoCut;
       const double w = i < n ? (double)weight(s, place_value(own)) : 0.0;
@@ -1032,7 +1033,7 @@ struct Split {
 
 }  // namespace
 
-// A wave takes `batch` consecutive rows (at most 16), whose settings its lanes
+// A wave takes `batch` (at most 32) consecutive rows, whose settings its lanes
 // read at once.  CUTS = false takes the rows without a cut by rank or mass, the
 // next one's logits on their way meanwhile; true takes the others, or all where
 // it runs alone.
@@ -1263,11 +1264,14 @@ static hipError_t split_rows(const DrawArgs& a, void* workspace, int S, hipStrea
   return hipGetLastError();
 }
 
-
 template <int TYPE, int TILES>
 static void wave_rows(const DrawArgs& a, hipStream_t s) {
-  // enough rows to a wave that 4096 waves (4 to a SIMD) take them all, 16 at most
-  const int batch = (int)(a.N / 4096 < 1 ? 1 : a.N / 4096 > 16 ? 16 : a.N / 4096);
+  // enough rows to a wave that 4096 waves (4 to a SIMD) take them all, 4 at most
+  // (65536 x 1024: 123 us at 4 and 8, 128 at 16; one row to a wave, where each
+  // starts by waiting for its settings, then for its logits: 136)
+  int batch = (int)(a.N / 4096 < 1 ? 1 : a.N / 4096 > 4 ? 4 : a.N / 4096);
+  // a launch has less than 2^32 lanes: at most 2^25 waves here
+  if (a.N > (int64_t)batch << 25) batch = (int)((a.N + (1 << 25) - 1) >> 25);
   const int64_t waves = (a.N + batch - 1) / batch;
   const dim3 g((unsigned)((waves + 3) / 4)), t(256);
   const bool rank = a.top_ks || (a.top_k >= 1 && a.top_k < a.V), mass = a.top_ps || a.top_p < 1.f;

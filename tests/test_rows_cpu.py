@@ -185,3 +185,23 @@ def test_reference_draw_by_hand():
     assert np.flatnonzero(R.kept(np.zeros(6), top_k=4, top_p=0.5)).tolist() == [0, 1]
     assert R.draw([0.0, 5.0, 5.0], 0.9, temperature=0.0) == 1
     assert R.draw([-np.inf] * 3, 0.5) == -1 and R.draw([0.0, np.nan], 0.5) == -1 and R.draw([np.inf, 0], 0.5) == -1
+
+
+def test_compressed_scan_refusals():
+    from soft_clustering_amd import ivf_probe
+
+    X = torch.arange(8 * 32, dtype=torch.float32).reshape(8, 32)
+    rows = sc.MXRows(torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4, dtype=torch.uint8), 32)
+    with pytest.raises(TypeError, match="MXRows"):
+        ivf_probe.compressed_topk(X, X, X, 2, 4)
+    with pytest.raises(ValueError, match="integer values"):
+        ivf_probe.compressed_topk(X + 0.5, rows, X, 2, 4)
+    with pytest.raises(ValueError, match="same width"):
+        ivf_probe.compressed_topk(X[:, :31], rows, X, 2, 4)
+    with pytest.raises(ValueError, match="same width"):
+        ivf_probe.compressed_topk(X, rows[:7], X, 2, 4)
+    for k, short in ((0, 4), (5, 4), (2, 9)):
+        with pytest.raises(ValueError, match="shortlist"):
+            ivf_probe.compressed_topk(X, rows, X, k, short)
+    with pytest.raises(ValueError, match="on a GPU"):
+        ivf_probe.compressed_topk(X, rows, X, 2, 4)
