@@ -75,15 +75,13 @@ __device__ __forceinline__ double fma_const(double a, double b, double c) {
   asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
   return r;
 }
-// round(2^42 2^t) for t <= 0 (0 below -43, NaN included).  t = n + f with n
-// whole and |f| <= 1/2; 2^f = 1 + f q(f), q of degree 8 fitted to the least
-// largest error (2^-45.8); n goes into the exponent.  The rounded integer
-// stands in the low bits of the result plus 2^52.
-constexpr double kOnes = 4503599627370496.0;  // 2^52
-__device__ __forceinline__ double fixed_exp2_up(double t) {
-  constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: sums with it are whole, in the low bits
+// 2^42 2^t for t <= 0 (below 1/2 for t < -43 and NaN).  t = n + f with n whole
+// and |f| <= 1/2; 2^f = 1 + f q(f), q of degree 8 fitted to the least largest
+// error (2^-45.8); n goes into the exponent.
+__device__ __forceinline__ double fixed_exp2(double t) {
+  constexpr double kWhole = 6755399441055744.0 + kFix;  // 1.5 * 2^52: sums with it are whole, in the low bits
   t = fmax(t, -100.0);
-  const double u = t + kWhole;
+  const double u = t + kWhole;  // n + 42 in the low bits
   const double f = t - (u - kWhole);
   double q = fma_const(0x1.b68e3bcc4f117p-24, f, 0x1.63e7f9e4ad781p-20);
   q = fma_const(q, f, 0x1.ffcb39c272ef4p-17);
@@ -94,8 +92,8 @@ __device__ __forceinline__ double fixed_exp2_up(double t) {
   q = fma_const(q, f, 0x1.ebfbdff81b63bp-3);
   q = fma_const(q, f, 0x1.62e42fefa3a26p-1);
   q = fma(q, f, 1.0);
-  const int n = (int)(unsigned)(u64)__double_as_longlong(u);
-  return __hiloint2double(__double2hiint(q) + ((n + kFix) << 20), __double2loint(q)) + kOnes;
+  const unsigned n = (unsigned)(u64)__double_as_longlong(u);
+  return __hiloint2double((int)((n << 20) + (unsigned)__double2hiint(q)), __double2loint(q));
 }
 
 // Sums over the lanes of a wave on the data-parallel primitives (shifts
@@ -135,6 +133,23 @@ __device__ __forceinline__ u64 lane_value(u64 v, int lane) {
 }
 __device__ __forceinline__ double lane_value(double v, int lane) {
   return __longlong_as_double((long long)lane_value((u64)__double_as_longlong(v), lane));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double v) {  // permutations: every lane has a source
+  return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_mov_dpp(__double2loint(v), CTRL, 0xF, 0xF, true));
+}
+// v plus v of the lane whose number differs by W (16 or 32)
+template <int W>
+__device__ __forceinline__ double swap_add(double v) {
+  const unsigned hi = (unsigned)__double2hiint(v), lo = (unsigned)__double2loint(v);
+  if constexpr (W == 16) {
+    const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false), l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    return __hiloint2double((int)h[0], (int)l[0]) + __hiloint2double((int)h[1], (int)l[1]);
+  } else {
+    const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false), l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    return __hiloint2double((int)h[0], (int)l[0]) + __hiloint2double((int)h[1], (int)l[1]);
+  }
 }
 __device__ __forceinline__ u64 wave_sum(u64 v) { return lane_value(wave_scan(v), 63); }
 template <int CTRL, int ROWS>
@@ -188,22 +203,25 @@ __device__ __forceinline__ double uniform(double v) {  // the same in all lanes:
 __device__ __forceinline__ float uniform(float v) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
+__device__ __forceinline__ double scale_c(float temp) { return 1.44269504088896340736 / (double)temp; }
+__device__ __forceinline__ float scale_bins(float temp, int nb) {  // finite: 0 stays in bin 0 whatever T is
+  return fminf((float)(nb - 1) / (15.f * temp), 3e38f);
+}
+__device__ __forceinline__ double least_weight(float min_p) {
+  return min_p > 0.f ? ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1.0;
+}
 __device__ __forceinline__ Scale scale_for(float M, float temp, float min_p, int nb) {
-  Scale s;
-  s.M = uniform((double)M);
-  s.c = uniform(1.44269504088896340736 / (double)temp);
-  s.half = uniform(0.5f * M);
-  s.bs = uniform(fminf((float)(nb - 1) / (15.f * temp), 3e38f));  // finite: 0 stays in bin 0 whatever T is
-  s.dmin = uniform(min_p > 0.f ? ceil((double)fminf(min_p, 1.f) * (double)(1ull << kFix)) : 1.0);
-  return s;
+  return {uniform((double)M), uniform(scale_c(temp)), uniform(0.5f * M), uniform(scale_bins(temp, nb)),
+          uniform(least_weight(min_p))};
 }
 __device__ __forceinline__ u64 weight(const Scale& s, float x) {
-  return (u64)__double_as_longlong(fixed_exp2_up(((double)x - s.M) * s.c)) & 0xFFFFFFFFFFFFFull;
+  constexpr double kOnes = 4503599627370496.0;  // 2^52: the rounded integer stands in the sum's low bits
+  return (u64)__double_as_longlong(fixed_exp2(((double)x - s.M) * s.c) + kOnes) & 0xFFFFFFFFFFFFFull;
 }
 // The same as a float64, in which sums of up to 2048 weights are exact; 0 if
 // it is below dmin.
 __device__ __forceinline__ double weight_if(const Scale& s, float x) {
-  const double q = fixed_exp2_up(((double)x - s.M) * s.c) - kOnes;
+  const double q = __builtin_rint(fixed_exp2(((double)x - s.M) * s.c));
   return q >= s.dmin ? q : 0.0;
 }
 // bins are ordered as the logits are, and the last one has no weight
@@ -243,7 +261,9 @@ struct WaveRow {
   float x[PER];
   Scale s;
 
-  __device__ __forceinline__ WaveRow(SH& sh_, int) : sh(sh_), lane(threadIdx.x & 63) {}
+  __device__ __forceinline__ WaveRow(SH& sh_) : sh(sh_), lane(threadIdx.x & 63) {}
+  // places tell -0 from +0, which are equal
+  static __device__ __forceinline__ float plus_zero(float v) { return CUTS ? v + 0.f : v; }
   __device__ __forceinline__ void load(const T* z, int V) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
@@ -252,10 +272,10 @@ struct WaveRow {
         T q[4];
         __builtin_memcpy(q, z + idx, sizeof q);  // rows may start at any element
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x[4 * t + v] = (float)q[v] + 0.f;
+        for (int v = 0; v < 4; ++v) x[4 * t + v] = plus_zero((float)q[v]);
       } else {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x[4 * t + v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
+        for (int v = 0; v < 4; ++v) x[4 * t + v] = idx + v < V ? plus_zero((float)z[idx + v]) : -INFINITY;
       }
     }
   }
@@ -357,7 +377,8 @@ struct WaveRow {
     }
   }
 
-  __device__ __forceinline__ int draw(float u, float temp, int top_k, float top_p, float min_p, int V) {
+  // half and M of the scale are still to be set
+  __device__ __forceinline__ int draw(const Scale& scale, float u, float temp, int top_k, float top_p, int V) {
     float top = -INFINITY;
     bool bad = false;
 #pragma unroll
@@ -374,7 +395,9 @@ struct WaveRow {
         if (x[i] == M) first = (unsigned)index(i);
       return (int)wave_min(first);
     }
-    s = scale_for(M, temp, min_p, NB);
+    s = scale;
+    s.M = uniform((double)M);
+    s.half = uniform(0.5f * M);
     unsigned in = (1u << (PER - 1) << 1) - 1u;  // the elements that stay
 #pragma unroll 1
     for (int mass = 0; CUTS && mass < 2; ++mass) {  // first the cut by rank, then by mass
@@ -401,69 +424,96 @@ struct WaveRow {
         if (behind(x[i], index(i), cut)) in &= ~(1u << i);
     }
     fresh();
-    // running sums in index order: tile by tile, lane by lane (a row's 1024
-    // weights at most sum to 2^52: exact)
-    double before[TILES + 1], run[TILES];
-    before[0] = 0;
+    // Index order is tile by tile, lane by lane: the tiles' sums give the tile,
+    // running sums over the lanes the lane, whose four weights are then
+    // evaluated again (a row's 1024 weights at most sum to 2^52: exact).
+    double own[TILES];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      double own = 0;
+      own[t] = 0;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) own += stays(4 * t + v, in);
-      const double scan = wave_scan(own);
-      run[t] = before[t] + scan - own;
-      before[t + 1] = before[t] + lane_value(scan, 63);
+      for (int v = 0; v < 4; ++v) own[t] += (in >> (4 * t + v)) & 1 ? weight_if(s, x[4 * t + v]) : 0.0;
     }
-    const double want = (double)draw_target(u, (u64)before[TILES]);
-    // the tile that reaches it, and its four weights again
     int tile = 0;
+    double before = 0, scan = 0, mine = own[0], want = 0;
+    if constexpr (TILES == 4) {
+      double sums[4];
+      tile_sums(own, sums);
+      want = target(u, sums[0] + sums[1] + (sums[2] + sums[3]));
 #pragma unroll
-    for (int t = 1; t < TILES; ++t) tile += before[t] < want;
-    double r = run[0];
-    float y[4] = {x[0], x[1], x[2], x[3]};
-    unsigned stay = in;
-#pragma unroll
-    for (int t = 1; t < TILES; ++t)
-      if (tile == t) {
-        r = run[t];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y[v] = x[4 * t + v];
-        stay = in >> (4 * t);
-      }
-    int id = INT_MAX;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const double q = (stay >> v) & 1 ? weight_if(s, y[v]) : 0;
-      if (r < want && want <= r + q) id = tile * 256 + 4 * lane + v;
-      r += q;
+      for (int t = 0; t < 3; ++t)
+        if (before + sums[t] < want && tile == t) before += sums[t], tile = t + 1;
+      tile = __builtin_amdgcn_readfirstlane(tile);
+      if (tile == 1) mine = own[1];
+      if (tile == 2) mine = own[2];
+      if (tile == 3) mine = own[3];
+      scan = wave_scan(mine);
+    } else {
+      static_assert(TILES == 1, "one tile or four");
+      scan = wave_scan(mine);
+      want = target(u, lane_value(scan, 63));
     }
-    const u64 who = __ballot(id != INT_MAX);
-    return __builtin_amdgcn_readlane(id, __ffsll(who) - 1);
+    const double run = before + scan - mine;
+    const int l = __ffsll(__ballot(run < want && want <= run + mine)) - 1;
+    float y = 0;  // lane v: element v of the four
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+      if (tile == t) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float q = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x[4 * t + v]), l));
+          y = lane == v ? q : y;
+        }
+      }
+    const unsigned stay = (unsigned)__builtin_amdgcn_readlane((int)in, l) >> (4 * tile);
+    const double q = (stay >> (lane & 3)) & 1 ? weight_if(s, y) : 0.0;
+    double r = lane_value(run, l);
+    int v = 0;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      r += lane_value(q, e);
+      v += r < want;
+    }
+    return __builtin_amdgcn_readfirstlane(tile * 256 + 4 * l + v);
   }
-  __device__ __forceinline__ double stays(int i, unsigned in) const {
-    return (in >> i) & 1 ? weight_if(s, x[i]) : 0;
+  // draw_target for a total below 2^53
+  static __device__ __forceinline__ double target(float u, double total) {
+    return u < 1.f ? fmin(floor(fmax((double)u, 0.0) * total), total - 1.0) + 1.0 : total;
+  }
+  // The sums of four values over the lanes, on every lane: two exchanges leave
+  // the sum of 4 lanes of value i in the lanes with lane % 4 == i.
+  __device__ __forceinline__ void tile_sums(const double (&own)[TILES], double (&sums)[4]) const {
+    const bool odd = lane & 1, high = lane & 2;
+    const double a = (odd ? own[1] : own[0]) + dpp_move<0xB1>(odd ? own[0] : own[1]);
+    const double b = (odd ? own[3] : own[2]) + dpp_move<0xB1>(odd ? own[2] : own[3]);
+    double c = (high ? b : a) + dpp_move<0x4E>(high ? a : b);
+    c += dpp_move<0x124>(c);
+    c += dpp_move<0x128>(c);
+    c = swap_add<16>(c);
+    c = swap_add<32>(c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[i] = lane_value(c, i);
   }
 };
 
 // ---------------------------------------------------------------------------
-// Longer rows: one workgroup of THREADS lanes to a row.  HELD > 0: the row (at
-// most HELD tiles) is kept in LDS as floats, each lane reading back what it
-// wrote; 0: it is read again in every pass.  A part is a run of AHEAD * 64 * VEC
-// elements, which a wave takes in AHEAD loads of VEC a lane; parts go to the
-// waves in turn.
+// Longer rows: one workgroup of THREADS lanes to a row, which is read again in
+// every pass (kept in LDS, it left one workgroup to a CU, whose barriers nothing
+// covered: 4096 x 16384 324 us against 244, 4096 x 4096 52 against 41).  A part
+// is a run of AHEAD * 64 * VEC elements, which a wave takes in AHEAD loads of
+// VEC a lane; parts go to the waves in turn.
 //
 // Passes over the row: the largest logit; a histogram (of counts for top-k, of
 // weights for top-p alone); then either the elements up to the bin of the cut
 // are collected in LDS, put in rank order and cut there (at most CAP of them:
 // nothing else is evaluated), or the parts are summed and the members of the
 // cut's bin collected in the same pass.
-template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+template <int TYPE, int THREADS, int NB, int PARTS>
 struct BlockRow {
   using T = typename Logit<TYPE>::T;
   static constexpr int VEC = Logit<TYPE>::VEC, NW = THREADS / 64, CAP = NB, AHEAD = 16 / VEC;
   static constexpr int PART = AHEAD * 64 * VEC;  // 1024 elements
   struct SH {
-    float held[HELD ? PARTS * PART : 4];
     u64 hist[NB];  // sums of bins, or the weights of the list's entries
     u64 list[CAP];
     u64 part[PARTS];
@@ -499,27 +549,13 @@ struct BlockRow {
       for (int v = 0; v < VEC; ++v) x[v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
     }
   }
-  __device__ __forceinline__ float4* held(int p, int a, int v) const {
-    return reinterpret_cast<float4*>(&sh.held[(p * AHEAD + a) * (64 * VEC) + v * 64 + lane * 4]);
-  }
-  __device__ __forceinline__ void fetch(int p, int a, float (&x)[VEC]) const {
-    if constexpr (HELD > 0) {
-#pragma unroll
-      for (int v = 0; v < VEC; v += 4) {
-        const float4 q = *held(p, a, v);
-        x[v] = q.x, x[v + 1] = q.y, x[v + 2] = q.z, x[v + 3] = q.w;
-      }
-    } else {
-      load(p, a, x);
-    }
-  }
   // f(part, load, logits) for this wave's parts, a part's loads ahead; end(part)
   template <class F, class E>
   __device__ __forceinline__ void parts(F&& f, E&& end) const {
     for (int p = p0 + wv; p < p1; p += NW) {
       float x[AHEAD][VEC];
 #pragma unroll
-      for (int a = 0; a < AHEAD; ++a) fetch(p, a, x[a]);
+      for (int a = 0; a < AHEAD; ++a) load(p, a, x[a]);
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) f(p, a, x[a]);
       end(p);
@@ -531,7 +567,7 @@ struct BlockRow {
 #pragma unroll 1
     for (int i = (p0 + wv) * AHEAD; i < p1 * AHEAD; i = i % AHEAD == AHEAD - 1 ? i + 1 + (NW - 1) * AHEAD : i + 1) {
       float x[VEC];
-      fetch(i / AHEAD, i % AHEAD, x);
+      load(i / AHEAD, i % AHEAD, x);
       const int idx = index(i / AHEAD, i % AHEAD);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) f(idx + v, x[v]);
@@ -708,27 +744,12 @@ struct BlockRow {
       bad |= !(x < INFINITY);  // +inf or NaN
       top = fmaxf(top, x);
     };
-    if constexpr (HELD > 0) {
-      for (int p = wv; p < nparts; p += NW) {
-        float x[AHEAD][VEC];
+    parts(
+        [&](int, int, float (&x)[VEC]) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) load(p, a, x[a]);
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-#pragma unroll
-          for (int v = 0; v < VEC; v += 4) *held(p, a, v) = make_float4(x[a][v], x[a][v + 1], x[a][v + 2], x[a][v + 3]);
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) look(x[a][v]);
-        }
-      }
-    } else {
-      parts(
-          [&](int, int, float (&x)[VEC]) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) look(x[v]);
-          },
-          [](int) {});
-    }
+          for (int v = 0; v < VEC; ++v) look(x[v]);
+        },
+        [](int) {});
     top = wave_max(top);
     const unsigned any = __ballot(bad) != 0;
     if (lane == 0) {
@@ -932,7 +953,7 @@ struct BlockRow {
       const double reach = (double)lane_value(left, l);
       float x[AHEAD][VEC];
 #pragma unroll
-      for (int a = 0; a < AHEAD; ++a) fetch(p, a, x[a]);
+      for (int a = 0; a < AHEAD; ++a) load(p, a, x[a]);
       double sum = 0;
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) {
@@ -1034,11 +1055,11 @@ struct Split {
 }  // namespace
 
 // A wave takes `batch` (at most 32) consecutive rows, whose settings its lanes
-// read at once.  CUTS = false takes the rows without a cut by rank or mass, the
-// next one's logits on their way meanwhile; true takes the others, or all where
-// it runs alone.
+// read at once.  CUTS = false takes the rows without a cut by rank or mass, true
+// the others, or all where it runs alone.  (The next row's logits fetched during
+// a draw cost registers, and so waves: 91 us against 87 for 65536 x 1024.)
 template <int TYPE, int TILES, bool CUTS>
-__global__ void __launch_bounds__(256, CUTS ? 4 : 5) k_draw_wave(DrawArgs a, int batch, int alone) {
+__global__ void __launch_bounds__(256, CUTS ? 4 : 6) k_draw_wave(DrawArgs a, int batch, int alone) {
   using R = WaveRow<TYPE, TILES, CUTS>;
   __shared__ typename R::SH sh[CUTS ? 4 : 1];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -1050,33 +1071,28 @@ __global__ void __launch_bounds__(256, CUTS ? 4 : 5) k_draw_wave(DrawArgs a, int
   u64 todo = __ballot(lane < rows && (alone || cuts == CUTS));
   if (!todo) return;
   const typename R::T* z = static_cast<const typename R::T*>(a.z) + n0 * a.ld;
-  R row(sh[CUTS ? wave : 0], a.V);
+  const double c = scale_c(set.temp), dmin = least_weight(set.min_p);
+  const float bins = CUTS ? scale_bins(set.temp, R::NB) : 0.f;
+  R row(sh[CUTS ? wave : 0]);
   row.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
   int ids = 0;
   const u64 all = todo;
   while (todo) {
     const int r = __ffsll(todo) - 1;
     todo &= todo - 1;
-    R next(sh[CUTS ? wave : 0], a.V);
-    if (!CUTS && todo) next.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
     const auto of = [&](float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), r)); };
-    const int id = row.draw(of(set.u), of(set.temp), __builtin_amdgcn_readlane(set.top_k, r), of(set.top_p), of(set.min_p),
-                            a.V);
+    const Scale scale = {0, lane_value(c, r), 0, of(bins), lane_value(dmin, r)};
+    const int id = row.draw(scale, of(set.u), of(set.temp), __builtin_amdgcn_readlane(set.top_k, r), of(set.top_p), a.V);
     if (lane == r) ids = id;
-    if (CUTS) {
-      wave_sync();
-      if (todo) row.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
-    } else {
-#pragma unroll
-      for (int i = 0; i < R::PER; ++i) row.x[i] = next.x[i];
-    }
+    wave_sync();
+    if (todo) row.load(z + (int64_t)(__ffsll(todo) - 1) * a.ld, a.V);
   }
   if ((all >> lane) & 1) a.ids[n0 + lane] = ids;
 }
 
-template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+template <int TYPE, int THREADS, int NB, int PARTS>
 __global__ void __launch_bounds__(THREADS, 4) k_draw_block(DrawArgs a) {
-  using R = BlockRow<TYPE, THREADS, HELD, NB, PARTS>;
+  using R = BlockRow<TYPE, THREADS, NB, PARTS>;
   __shared__ typename R::SH sh;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
     R row(sh, static_cast<const typename R::T*>(a.z) + n * a.ld, a.V);
@@ -1089,7 +1105,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_draw_block(DrawArgs a) {
 }
 
 template <int TYPE>
-using SplitOf = BlockRow<TYPE, kSplitThreads, 0, kSplitBins, kSplitParts>;
+using SplitOf = BlockRow<TYPE, kSplitThreads, kSplitBins, kSplitParts>;
 
 // Workgroup b of the launch: part range b % S of row b / S.
 template <int TYPE>
@@ -1208,7 +1224,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_draw_split_sum(DrawArgs a, Sp
 
 template <int TYPE>
 __global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Split* ws, int S) {
-  using R = BlockRow<TYPE, 1024, 0, kSplitBins, kSplitParts>;
+  using R = BlockRow<TYPE, 1024, kSplitBins, kSplitParts>;
   __shared__ typename R::SH sh;
   const int n = (int)blockIdx.x;
   const Split& sp = ws[n];
@@ -1281,10 +1297,10 @@ static void wave_rows(const DrawArgs& a, hipStream_t s) {
   if ((!rank && !mass) || both) hipLaunchKernelGGL((k_draw_wave<TYPE, TILES, false>), g, t, 0, s, a, batch, 0);
   if (rank || mass) hipLaunchKernelGGL((k_draw_wave<TYPE, TILES, true>), g, t, 0, s, a, batch, !both);
 }
-template <int TYPE, int THREADS, int HELD, int NB, int PARTS>
+template <int TYPE, int THREADS, int NB, int PARTS>
 static void block_rows(const DrawArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)(a.N < (1 << 20) ? a.N : (1 << 20));
-  hipLaunchKernelGGL((k_draw_block<TYPE, THREADS, HELD, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a);
+  hipLaunchKernelGGL((k_draw_block<TYPE, THREADS, NB, PARTS>), dim3(grid), dim3(THREADS), 0, s, a);
 }
 
 template <int TYPE>
@@ -1295,11 +1311,9 @@ static hipError_t draw_type(const DrawArgs& a, void* workspace, hipStream_t s) {
   else if (a.V <= 1024)
     wave_rows<TYPE, 4>(a, s);
   else if (a.V <= 4096)
-    block_rows<TYPE, 256, 1, 1024, 4>(a, s);
-  else if (a.V <= 16384)
-    block_rows<TYPE, 1024, 1, 2048, 16>(a, s);
+    block_rows<TYPE, 128, 1024, 4>(a, s);  // 4096 x 2000: 36 us; 256 lanes 51, 512 100
   else
-    block_rows<TYPE, 512, 0, 2048, 1024>(a, s);
+    block_rows<TYPE, 512, 2048, 1024>(a, s);  // 4096 x 16384: 244 us; 256 lanes 262, 1024 334
   return hipGetLastError();
 }
 
