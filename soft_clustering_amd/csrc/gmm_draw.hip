@@ -265,19 +265,19 @@ struct WaveRow {
   // places tell -0 from +0, which are equal
   static __device__ __forceinline__ float plus_zero(float v) { return CUTS ? v + 0.f : v; }
   __device__ __forceinline__ void load(const T* z, int V) {
+    T q[TILES][4];  // converted behind the branches, so that all loads go out first
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       const int idx = t * 256 + 4 * lane;
       if (idx + 4 <= V) {
-        T q[4];
-        __builtin_memcpy(q, z + idx, sizeof q);  // rows may start at any element
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[4 * t + v] = plus_zero((float)q[v]);
+        __builtin_memcpy(q[t], z + idx, sizeof q[t]);  // rows may start at any element
       } else {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x[4 * t + v] = idx + v < V ? plus_zero((float)z[idx + v]) : -INFINITY;
+        for (int v = 0; v < 4; ++v) q[t][v] = idx + v < V ? z[idx + v] : (T)-INFINITY;
       }
     }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = plus_zero((float)q[i >> 2][i & 3]);
   }
   // Makes the logits new values to the compiler, which would otherwise compute
   // all bins, places and weights once, ahead, and spill them.
@@ -549,16 +549,48 @@ struct BlockRow {
       for (int v = 0; v < VEC; ++v) x[v] = idx + v < V ? (float)z[idx + v] + 0.f : -INFINITY;
     }
   }
-  // f(part, load, logits) for this wave's parts, a part's loads ahead; end(part)
+  // A part's logits as they are stored; whether it ends inside the row is the
+  // same for all lanes, and the loads of one that does go out together.
+  struct Raw {
+    T q[AHEAD][VEC];
+  };
+  __device__ __forceinline__ void load(int p, Raw& raw) const {
+    if ((p + 1) * PART <= V) {
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) __builtin_memcpy(raw.q[a], z + index(p, a), sizeof raw.q[a]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const int idx = index(p, a) + v;
+          raw.q[a][v] = idx < V ? z[idx] : (T)-INFINITY;
+        }
+    }
+  }
+  // f(part, load, logits) for this wave's parts, the next one's loads ahead;
+  // end(part)
   template <class F, class E>
   __device__ __forceinline__ void parts(F&& f, E&& end) const {
-    for (int p = p0 + wv; p < p1; p += NW) {
-      float x[AHEAD][VEC];
+    int p = p0 + wv;
+    if (p >= p1) return;
+    Raw raw;
+    load(p, raw);
+    for (;;) {
+      Raw next;
+      const bool more = p + NW < p1;
+      if (more) load(p + NW, next);
 #pragma unroll
-      for (int a = 0; a < AHEAD; ++a) load(p, a, x[a]);
+      for (int a = 0; a < AHEAD; ++a) {
+        float x[VEC];
 #pragma unroll
-      for (int a = 0; a < AHEAD; ++a) f(p, a, x[a]);
+        for (int v = 0; v < VEC; ++v) x[v] = (float)raw.q[a][v] + 0.f;
+        f(p, a, x);
+      }
       end(p);
+      if (!more) return;
+      raw = next;
+      p += NW;
     }
   }
   // f(idx, logit) for this lane's elements, one load at a time (rare passes)
@@ -1041,7 +1073,7 @@ struct BlockRow {
 // row, makes the draw.  What they share lies in the workspace.  (Left to the
 // last workgroup of the third launch to finish, the draw took longer: the
 // device-wide fences that this needs cost 10 to 40 us.)
-constexpr int kSplitThreads = 256, kSplitBins = 2048, kSplitParts = 1024, kMostSplits = 256;
+constexpr int kSplitThreads = 512, kSplitBins = 2048, kSplitParts = 1024, kMostSplits = 256;
 enum Finish { kNone, kGreedy, kFromParts, kFromList, kWholeList, kAlone };
 struct Split {
   u64 hist[kSplitBins];
@@ -1252,11 +1284,13 @@ __global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Spli
 }
 
 // Workgroups to a row of the split, 0 where rows are not split: at least 4
-// parts (4096 logits) each, and no more in all than two to a CU.
+// parts (4096 logits) each, and no more in all than one to a CU: each adds its
+// histogram's 2048 bins to the row's (64 x 131071: 41 us, with two to a CU of
+// 256 lanes 44, with four 58).
 static int splits_of(int64_t N, int V) {
   if (V <= 16384 || N > 128) return 0;
   const int nparts = (V + 1023) / 1024;
-  const int64_t a = (nparts + 3) / 4, b = 512 / N;
+  const int64_t a = (nparts + 3) / 4, b = 256 / N;
   const int64_t S = a < b ? a : b;
   return (int)(S < kMostSplits ? S : kMostSplits);
 }
