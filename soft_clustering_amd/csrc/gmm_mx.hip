@@ -263,17 +263,18 @@ template <int CT>
 __device__ __forceinline__ void put_c(typename Elem<CT>::T* p, float x) { *p = Elem<CT>::put(x); }
 
 // Large products: WM x WN waves, each with TM x TN blocks of 32 x 32.  A step
-// is one group (128 values, 64 bytes of a row); S LDS buffers are filled by LDS
-// DMA S - 1 steps ahead.  Chunk c (block c of the group) of row r sits at slot
-// c ^ swz(r) of its 64 bytes, so 8 consecutive rows' reads of one chunk touch
-// all banks.  v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the
+// is one group (128 values, 64 bytes of a row); S LDS buffers of GPS groups are
+// filled by LDS DMA S - 1 buffers ahead.  Chunk c (16 bytes) of row r sits at
+// slot c ^ swz(r) of its 64 GPS bytes, so 8 consecutive rows' reads of one
+// chunk touch all banks.  v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the
 // block 2 g + h of a group in its step h: any assignment serves as long as both
 // sides share it, and this one makes a lane's two scale bytes neighbours.
 // Scales come for 4 steps at a time, in 16 bytes of each row (the last 4 groups
 // at the end); SHORT rows of fewer groups have them placed by hand.
 // Tiles are numbered so that each XCD has a contiguous range of them, in
 // bands of 8 row tiles: 32 neighbours share 8 + 4 panels in the XCD's L2.
-__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 2)) & 3; }
+template <int GPS>
+__device__ __forceinline__ int swz(int r) { return GPS == 1 ? (r ^ (r >> 2)) & 3 : r & 7; }
 
 // Orders a wave's LDS accesses before its later ones (other lanes' included).
 __device__ __forceinline__ void wave_sync() {
@@ -320,17 +321,18 @@ __device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
   m = 8 * b + in - n * rows;
 }
 
-template <int WM, int WN, int TM, int TN, int S, bool SHORT, bool STREAM, int CT>
+template <int WM, int WN, int TM, int TN, int GPS, int S, bool SHORT, bool STREAM, int CT>
 __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
     k_mx_tile(const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ as, int64_t ldas, int M,
               const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ bs, int64_t ldbs, int N, int G,
               const float* __restrict__ bias, typename Elem<CT>::T* __restrict__ C, int64_t ldc, int tm, int tn) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, NW = WM * WN;
   constexpr int ROWS = BM + BN;               // A's rows, then B's
-  constexpr int STEP = ROWS * 64;              // code bytes of a step
-  constexpr int OPS = ROWS / 16 / NW;          // DMA instructions of a wave in a step
+  constexpr int STEP = ROWS * 64 * GPS;        // code bytes of a buffer: GPS groups
+  constexpr int CH = 4 * GPS, RPI = 64 / CH;   // chunks of a row in a buffer, rows of a DMA instruction
+  constexpr int OPS = ROWS / RPI / NW;         // DMA instructions of a wave for a buffer
   constexpr int SOPS = (ROWS / 64 + NW - 1) / NW;  // and for the scales of 4 steps
-  static_assert(ROWS % (16 * NW) == 0 && S >= 2 && S <= 4 && BM % 64 == 0 && BN % 64 == 0, "tile shape");
+  static_assert(ROWS % (RPI * NW) == 0 && (GPS == 1 || GPS == 2) && S >= 2 && S <= 4 / GPS && BM % 64 == 0 && BN % 64 == 0, "tile shape");
   constexpr int PITCH = 32 * TN + 4;  // floats of a row of results; rows 4 apart start 16 banks apart
   constexpr int OUT = NW * 32 * PITCH * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[S * STEP > OUT ? S * STEP : OUT];
@@ -344,14 +346,14 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   const int m0 = mt * BM, n0 = nt * BN;
 
   // This lane's source of each DMA instruction, relative to its panel's first
-  // row: 16 rows an instruction, 4 lanes a row.  Rows past the end repeat the
-  // last one and are not stored.
+  // row: CH lanes a row.  Rows past the end repeat the last one and are not
+  // stored.
   unsigned voff[OPS], soff[SOPS];
 #pragma unroll
   for (int i = 0; i < OPS; ++i) {
-    const int r = (w * OPS + i) * 16 + (lane >> 2);
+    const int r = (w * OPS + i) * RPI + lane / CH;
     voff[i] = (r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)lda : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldb) +
-              ((lane & 3) ^ swz(r)) * 16;
+              ((lane & (CH - 1)) ^ swz<GPS>(r)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SOPS; ++i) {
@@ -362,13 +364,14 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   const uint8_t* const pb = B + (int64_t)n0 * ldb;
   const uint8_t* const qsa = as + (int64_t)m0 * ldas;
   const uint8_t* const qsb = bs + (int64_t)n0 * ldbs;
-  // step k into its buffer; past the last one the last again, which nobody
-  // reads (no branch: one straight run of instructions)
-  auto stage = [&](int k) {
-    const int64_t off = 64 * (int64_t)min(k, G - 1);
-    const unsigned dst = lds0 + (unsigned)(k % S) * STEP + w * (OPS * 1024);
+  // groups GPS p .. into their buffer, the row's last GPS groups where it ends
+  // before; past the end these again, which nobody reads (no branch: one
+  // straight run of instructions)
+  auto stage = [&](int p) {
+    const int64_t off = 64 * (int64_t)min(GPS * p, G - GPS);
+    const unsigned dst = lds0 + (unsigned)(p % S) * STEP + w * (OPS * 1024);
 #pragma unroll
-    for (int i = 0; i < OPS; ++i) lds_dma16(voff[i], ((w * OPS + i) * 16 < BM ? pa : pb) + off, dst + i * 1024);
+    for (int i = 0; i < OPS; ++i) lds_dma16(voff[i], ((w * OPS + i) * RPI < BM ? pa : pb) + off, dst + i * 1024);
   };
   // scales of groups k .. k + 3 (k a multiple of 4), or of a row's last 4
   auto stage_scales = [&](int k, u64 on) {
@@ -397,66 +400,78 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   // whose operands this wave has then in registers.
   f16v acc[TM][TN] = {};
   i4 fa[2][TM], fb[2][TN];
-  int qa[2][TM], qb[2][TN];  // scales of even and odd steps, this lane's half in the low bits
+  int qa[2][TM], qb[2][TN];  // scales of even and odd steps: this lane's two bytes
   auto read = [&](int k, int h) {
-    const uint8_t* cb = lds + (k % S) * STEP;
-    const int c = ((2 * g + h) ^ swz(r32)) * 16;
+    const int p = k / GPS, half = GPS == 1 ? 0 : min(k - min(GPS * p, G - GPS), 1);
+    const uint8_t* cb = lds + (p % S) * STEP;
+    const int c = ((4 * half + 2 * g + h) ^ swz<GPS>(r32)) * 16;
+    constexpr int ROW = 64 * GPS;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[h][i] = *reinterpret_cast<const i4*>(cb + ((wm * TM + i) * 32 + r32) * 64 + c);
+    for (int i = 0; i < TM; ++i) fa[h][i] = *reinterpret_cast<const i4*>(cb + ((wm * TM + i) * 32 + r32) * ROW + c);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[h][j] = *reinterpret_cast<const i4*>(cb + (BM + (wn * TN + j) * 32 + r32) * 64 + c);
+    for (int j = 0; j < TN; ++j) fb[h][j] = *reinterpret_cast<const i4*>(cb + (BM + (wn * TN + j) * 32 + r32) * ROW + c);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto read_scales = [&](int k, int e) {  // of step k, into set e
     const int c = k - min(k & ~3, G - 4);
-    const unsigned* sb = reinterpret_cast<const unsigned*>(scales[(k >> 2) & 1]) + min(c, 3);
+    const unsigned short* sb = reinterpret_cast<const unsigned short*>(scales[(k >> 2) & 1]) + 2 * min(c, 3) + g;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) qa[e][i] = (int)(sb[4 * ((wm * TM + i) * 32 + r32)] >> (16 * g));
+    for (int i = 0; i < TM; ++i) qa[e][i] = sb[8 * ((wm * TM + i) * 32 + r32)];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) qb[e][j] = (int)(sb[4 * (BM + (wn * TN + j) * 32 + r32)] >> (16 * g));
+    for (int j = 0; j < TN; ++j) qb[e][j] = sb[8 * (BM + (wn * TN + j) * 32 + r32)];
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Step k is in LDS for everyone, and step k - 1 read by everyone; its buffer
-  // takes step k + S - 1.  The scales of the next 4 steps follow 3 steps ahead
-  // at the latest, which is as far as the wait leaves DMA outstanding.
-  auto arrive = [&](int k) {
-    arrived<(S - 2) * OPS>();
+  // Behind a barrier step k is in LDS for everyone, and what lies before it was
+  // read by everyone; the buffer before takes the groups S - 1 buffers on.  The
+  // scales of the next 4 steps follow 2 steps ahead at the latest, which is
+  // further than the wait leaves DMA outstanding.
+  auto refill = [&](int k) {
     if constexpr (!SHORT) stage_scales((k & ~3) + 4, (k & 3) == 0 ? ~0ull : 0ull);
-    stage(k + S - 1);
+    stage(k / GPS + S - 1);
   };
-  // one half step's products: block Q of a lane's two, scales of set E
-#define GMM_MX_HALF(Q, E)                                                                                          \
+  // Products of a half step: rows I .. J - 1 of a wave's blocks, block Q of a
+  // lane's two, scales of set E.
+#define GMM_MX_ROWS(I, J, Q, E)                                                                                    \
   do {                                                                                                             \
-    _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =      \
+    _Pragma("unroll") for (int i = I; i < J; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =       \
         __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fa[Q][i]), operand(fb[Q][j]), acc[i][j], 4, 4, Q,  \
                                                         qa[E][i], Q, qb[E][j]);                                    \
     __builtin_amdgcn_sched_barrier(0);                                                                             \
   } while (0)
+  // Step k with scales of set E: each half starts with products, whose
+  // operands are there, so that the matrix unit works while the next half's
+  // reads and the DMA go out.
+#define GMM_MX_STEP(K, E)                  \
+  do {                                     \
+    GMM_MX_ROWS(0, 1, 0, E);               \
+    read(K, 1);                            \
+    GMM_MX_ROWS(1, TM, 0, E);              \
+    if (GPS == 1 || E == 1) arrived<(S - 2) * OPS>(); \
+    GMM_MX_ROWS(0, 1, 1, E);               \
+    read_scales((K) + 1, 1 - E);           \
+    read((K) + 1, 0);                      \
+    GMM_MX_ROWS(1, 2, 1, E);               \
+    if (GPS == 1 || E == 1) refill((K) + 1); \
+    __builtin_amdgcn_sched_barrier(0);     \
+    GMM_MX_ROWS(2, TM, 1, E);              \
+  } while (0)
 
-  arrive(0);
+  arrived<(S - 2) * OPS>();
+  refill(0);
   read_scales(0, 0);
   read(0, 0);
   int k = 0;
   for (; k + 1 < G; k += 2) {
-    read(k, 1);
-    GMM_MX_HALF(0, 0);
-    arrive(k + 1);
-    read_scales(k + 1, 1);
-    read(k + 1, 0);
-    GMM_MX_HALF(1, 0);
-    read(k + 1, 1);
-    GMM_MX_HALF(0, 1);
-    arrive(k + 2);
-    read_scales(k + 2, 0);
-    read(k + 2, 0);
-    GMM_MX_HALF(1, 1);
+    GMM_MX_STEP(k, 0);
+    GMM_MX_STEP(k + 1, 1);
   }
   if (G & 1) {
     read(k, 1);
-    GMM_MX_HALF(0, 0);
-    GMM_MX_HALF(1, 0);
+    GMM_MX_ROWS(0, TM, 0, 0);
+    GMM_MX_ROWS(0, TM, 1, 0);
   }
-#undef GMM_MX_HALF
+#undef GMM_MX_STEP
+#undef GMM_MX_ROWS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the buffers are reused
 
   // The result goes through LDS so that it leaves in 16-byte stores along
@@ -714,7 +729,7 @@ static void few_rows(const MxProduct& p, int G, hipStream_t s) {
     few_rows_nt<AT, MT, MT == 4 ? 4 : 2, CT>(p, G, s);
 }
 
-template <int WM, int WN, int TM, int TN, int S, int CT>
+template <int WM, int WN, int TM, int TN, int GPS, int S, int CT>
 static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
@@ -730,10 +745,26 @@ static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
   // and 1024 x 100003, whose rows end inside lines, 187 us against 175.
   constexpr int64_t size = sizeof(typename Elem<CT>::T);
   const bool stream = p.M * p.N * size > ((int64_t)256 << 20) && ((uintptr_t)p.C & 127) == 0 && p.ldc * size % 128 == 0;
-  if (G < 4)
-    stream ? launch(k_mx_tile<WM, WN, TM, TN, S, true, true, CT>) : launch(k_mx_tile<WM, WN, TM, TN, S, true, false, CT>);
-  else
-    stream ? launch(k_mx_tile<WM, WN, TM, TN, S, false, true, CT>) : launch(k_mx_tile<WM, WN, TM, TN, S, false, false, CT>);
+  constexpr bool LARGE = WM * WN == 8, SMALL = TM * TN == 4;  // no short rows come with LARGE, no such result with SMALL
+  if constexpr (!LARGE) {
+    if (G < 4) {
+      if constexpr (!SMALL) {
+        if (stream) {
+          launch(k_mx_tile<WM, WN, TM, TN, 1, 2, true, true, CT>);
+          return hipGetLastError();
+        }
+      }
+      launch(k_mx_tile<WM, WN, TM, TN, 1, 2, true, false, CT>);
+      return hipGetLastError();
+    }
+  }
+  if constexpr (!SMALL) {
+    if (stream) {
+      launch(k_mx_tile<WM, WN, TM, TN, GPS, S, false, true, CT>);
+      return hipGetLastError();
+    }
+  }
+  launch(k_mx_tile<WM, WN, TM, TN, GPS, S, false, false, CT>);
   return hipGetLastError();
 }
 
@@ -756,13 +787,17 @@ static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
   }
   // The tile.  Large ones read less from L2 and LDS for each product, small
   // ones fill the 256 CUs and let a workgroup's stores overlap another's
-  // products.  Measured (us): 8192 x 8192 x 8192 330 with 256 x 256, 368 with
-  // 256 x 128, 439 with 128 x 128; 1024 x 100003 x 128 142, 114 and 131;
-  // 128 x 16384 x 4096 35, 26 and 20.
+  // products.  Measured (us): 8192 x 8192 x 8192 311 with 256 x 256, 368 with
+  // 256 x 128, 439 with 128 x 128; 1024 x 100003 x 128 142, 111 and 131;
+  // 128 x 16384 x 4096 35, 26 and 19.
+  // Two groups to a buffer make the DMA read whole 128-byte lines and halve the
+  // barriers (one and two groups: 8192^3 330 and 311, 512 x 16384 x 4096 with
+  // 128 x 128 tiles 32 and 30), but leave room for one workgroup of 256 x 128
+  // on a CU instead of two (1024 x 100096 x 768: 111 and 136).
   const int64_t cus = 256;
-  if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 3, CT>(p, G, s);
-  if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 2, CT>(p, G, s);
-  return tiles<2, 2, 2, 2, 2, CT>(p, G, s);
+  if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 2, 2, CT>(p, G, s);
+  if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 1, 2, CT>(p, G, s);
+  return tiles<2, 2, 2, 2, 2, 2, CT>(p, G, s);
 }
 
 hipError_t launch_mx_product(const MxProduct& p0, void* workspace, hipStream_t s) {
