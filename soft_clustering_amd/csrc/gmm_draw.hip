@@ -218,10 +218,13 @@ __device__ __forceinline__ u64 weight(const Scale& s, float x) {
   constexpr double kOnes = 4503599627370496.0;  // 2^52: the rounded integer stands in the sum's low bits
   return (u64)__double_as_longlong(fixed_exp2(((double)x - s.M) * s.c) + kOnes) & 0xFFFFFFFFFFFFFull;
 }
-// The same as a float64, in which sums of up to 2048 weights are exact; 0 if
-// it is below dmin.
+// The same as a float64, in which sums of up to 2048 weights are exact, and 0
+// if it is below dmin.
+__device__ __forceinline__ double whole_weight(const Scale& s, float x) {
+  return __builtin_rint(fixed_exp2(((double)x - s.M) * s.c));
+}
 __device__ __forceinline__ double weight_if(const Scale& s, float x) {
-  const double q = __builtin_rint(fixed_exp2(((double)x - s.M) * s.c));
+  const double q = whole_weight(s, x);
   return q >= s.dmin ? q : 0.0;
 }
 // bins are ordered as the logits are, and the last one has no weight
@@ -813,16 +816,21 @@ struct BlockRow {
   // cut so far keeps.
   __device__ __forceinline__ void histogram(bool by_weight, u64 cut) {
     clear();
-    parts(
-        [&](int p, int a, float (&x)[VEC]) {
+    const auto count = [&](auto kept) {
+      parts(
+          [&](int p, int a, float (&x)[VEC]) {
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const int q = bin_of<NB>(s, x[v]);
-            if (q < NB - 1 && (cut == kNoCut || place_of(x[v], index(p, a) + v) <= cut))
-              atomicAdd(&sh.hist[q], by_weight ? weight(s, x[v]) : 1ull);
-          }
-        },
-        [](int) {});
+            for (int v = 0; v < VEC; ++v) {
+              const int q = bin_of<NB>(s, x[v]);
+              if (q < NB - 1 && kept(x[v], index(p, a) + v)) atomicAdd(&sh.hist[q], by_weight ? weight(s, x[v]) : 1ull);
+            }
+          },
+          [](int) {});
+    };
+    if (cut == kNoCut)
+      count([](float, int) { return true; });
+    else
+      count([&](float x, int idx) { return place_of(x, idx) <= cut; });
     __syncthreads();
   }
   // Collects the elements of the parts up to bin b.
@@ -845,12 +853,13 @@ struct BlockRow {
 #pragma unroll
           for (int v = 0; v < VEC; ++v) {
             const int q = b == NB ? -1 : bin_of<NB>(s, x[v]);
-            const double add = weight_if(s, x[v]);
-            sum += q < b ? add : 0.0;
+            const double w = whole_weight(s, x[v]);
+            const bool stays = w >= s.dmin;
+            sum += stays && q < b ? w : 0.0;
             if (q == b) {
               const u64 place = place_of(x[v], index(p, a) + v);
               if (known)
-                sum += place <= cut ? add : 0.0;
+                sum += stays && place <= cut ? w : 0.0;
               else if (place <= kcut)
                 append(count, list, x[v], index(p, a) + v);
             }
