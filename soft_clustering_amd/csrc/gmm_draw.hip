@@ -871,88 +871,96 @@ struct BlockRow {
           sum = 0;
         });
   }
+  // Up to 512 entries of the list in order, each counting those in front of it
+  // (L lanes for the entries, G groups of them that look at a share each), and
+  // with sums the running sums of the weights w (exact), which lane tid has for
+  // entry tid.  A bitonic sort of 95 entries takes 12000 cycles, most of them
+  // waits between its steps.
+  struct Order {
+    int rank;
+    double before, total;
+  };
+  __device__ __forceinline__ Order order(int n, double w, bool sums) {
+    int L = 64;
+    while (L < n) L <<= 1;
+    const int G = THREADS / L, i = tid & (L - 1), group = tid / L;
+    const int share = (n + G - 1) / G, j0 = min(n, group * share), j1 = min(n, j0 + share);
+    int* const ranks = reinterpret_cast<int*>(sh.hist);                      // THREADS
+    double* const sorted = reinterpret_cast<double*>(sh.hist + THREADS / 2);  // L
+    Order o = {0, 0, 0};
+    if ((i & ~63) < n) {  // waves without an entry have nothing to count
+      const u64 own = i < n ? sh.list[i] : 0;
+#pragma unroll 4
+      for (int j = j0; j < j1; ++j) o.rank += sh.list[j] < own;
+    }
+    ranks[tid] = o.rank;
+    if (tid >= n && tid < L) sorted[tid] = 0;
+    __syncthreads();
+    const bool mine = tid < n;
+    if (mine) {
+      for (int g = 1; g < G; ++g) o.rank += ranks[g * L + tid];
+      if (sums) sorted[o.rank] = w;
+    }
+    __syncthreads();
+    if (!sums) return o;
+    if (wv < L / 64) {
+      const double run = wave_scan(sorted[tid]);
+      sorted[tid] = run;
+      if (lane == 63) sh.wave[wv] = (u64)__double_as_longlong(run);
+    }
+    __syncthreads();
+    if (mine) o.before = sorted[o.rank] - w;
+    for (int x = 0; x < L / 64; ++x) {
+      const double t = __longlong_as_double((long long)sh.wave[x]);
+      o.before += x < (o.rank >> 6) ? t : 0.0;
+      o.total += t;
+    }
+    __syncthreads();
+    return o;
+  }
   // From the n <= CAP entries of the list.  whole: they are all that can stay
   // by rank; the draw from them.  Otherwise the members of the cut's bin: sets
   // the cut, adds what stays of them to the parts' sums, and returns -2.
-  // Up to 512 entries the lanes count what ranks in front of each (a bitonic
-  // sort of 95 entries takes 12000 cycles, most of them waits between its
-  // steps); more are sorted.
   __device__ __forceinline__ int from_list(int n, bool whole, u64 need, bool by_weight, float u, int top_k, float top_p,
                                            u64& cut) {
     if (n <= 512 && n <= THREADS) {
-      // L lanes for the entries, G groups of them that each look at a share
-      int L = 64;
-      while (L < n) L <<= 1;
-      const int G = THREADS / L, i = tid & (L - 1), group = tid / L;
-      const int share = (n + G - 1) / G, j0 = min(n, group * share), j1 = min(n, j0 + share);
-      struct Entry {
-        u64 place;
-        double w;
-      };
-      Entry* const es = reinterpret_cast<Entry*>(sh.hist);        // L entries (sums of up to 512 weights are exact),
-      double* const sums = reinterpret_cast<double*>(es + L);     // THREADS sums,
-      int* const ranks = reinterpret_cast<int*>(sums + THREADS);  // THREADS counts
-      static_assert(sizeof sh.hist + sizeof sh.list >= (THREADS < 512 ? THREADS : 512) * 16 + THREADS * 12,
-                    "these lie over hist and, once its entries are read, over list, which follows it");
-      const bool mine = group == 0 && i < n;
-      const u64 own = i < n ? sh.list[i] : kNoCut;
-      const double w = i < n ? (double)weight(s, place_value(own)) : 0.0;
-      if (group == 0) es[i] = {own, w};
-      if (tid == 0) sh.id = -1;
-      __syncthreads();
-      int rank = 0;
-      double before = 0;
-      if ((i & ~63) < n) {  // waves without an entry have nothing to count
-#pragma unroll 4
-        for (int j = j0; j < j1; ++j) {
-          const Entry e = es[j];
-          const bool front = e.place < own;
-          rank += front;
-          before += front ? e.w : 0.0;
-        }
-      }
-      sums[tid] = before;
-      ranks[tid] = rank;
-      __syncthreads();
-      if (mine)
-        for (int g = 1; g < G; ++g) {
-          rank += ranks[g * L + i];
-          before += sums[g * L + i];
-        }
+      static_assert(THREADS / 2 + 2 * (THREADS < 512 ? THREADS : 512) <= NB, "ranks, sums and weights lie over hist");
+      const bool mine = tid < n;
+      const u64 own = mine ? sh.list[tid] : kNoCut;
+      const double w = mine ? (double)weight(s, place_value(own)) : 0.0;
+      const Order o = order(n, w, whole ? top_p < 1.f : by_weight);
       const int idx = place_index(own);
       if (!whole) {
-        const bool stay = mine && (by_weight ? before < (double)need : (u64)rank < need);
-        if (stay && (by_weight ? (double)need <= before + w : (u64)rank + 1 == need)) sh.before = own;
+        const bool stay = mine && (by_weight ? o.before < (double)need : (u64)o.rank < need);
+        if (stay && (by_weight ? (double)need <= o.before + w : (u64)o.rank + 1 == need)) sh.before = own;
         if (stay && w >= s.dmin) atomicAdd(&sh.part[idx / PART], (u64)w);
         __syncthreads();
         cut = sh.before;
         return -2;
       }
-      bool stay = mine && rank < top_k;
+      bool stay = mine && o.rank < top_k;
       if (top_p < 1.f) {  // an entry that ranks below top_k has only such entries in front of it
         const u64 sum = block_sum(stay ? (u64)w : 0);
-        stay = stay && before < (double)mass_target(top_p, sum);
+        stay = stay && o.before < (double)mass_target(top_p, sum);
       }
-      // what stays, close together: (index, weight)
-      const double q = stay && w >= s.dmin ? w : 0.0;
-      if (tid == 0) sh.count = 0;
-      __syncthreads();
-      if (q > 0) es[atomicAdd(&sh.count, 1)] = {(u64)idx, q};
-      __syncthreads();
-      const int m = sh.count;
-      if (tid < m) {
-        const Entry me = es[tid];
-        double total = 0;
-        before = 0;
-#pragma unroll 4
-        for (int j = 0; j < m; ++j) {
-          const Entry e = es[j];
-          total += e.w;
-          before += e.place < me.place ? e.w : 0.0;
-        }
-        const double want = (double)draw_target(u, (u64)total);
-        if (before < want && want <= before + me.w) sh.id = (int)me.place;
+      // what stays, close together: indices and weights
+      double* const ws = reinterpret_cast<double*>(sh.hist + THREADS / 2 + (THREADS < 512 ? THREADS : 512));
+      if (tid == 0) {
+        sh.count = 0;
+        sh.id = -1;
       }
+      __syncthreads();
+      if (stay && w >= s.dmin) {
+        const int at = atomicAdd(&sh.count, 1);
+        sh.list[at] = (u64)idx;
+        ws[at] = w;
+      }
+      __syncthreads();
+      const int m = sh.count, id = tid < m ? (int)sh.list[tid] : -1;
+      const double q = tid < m ? ws[tid] : 0.0;
+      const Order d = order(m, q, true);
+      const double want = (double)draw_target(u, (u64)d.total);
+      if (tid < m && d.before < want && want <= d.before + q) sh.id = id;
       __syncthreads();
       return sh.id;
     }
