@@ -1302,8 +1302,8 @@ __global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Spli
 
 // Workgroups to a row of the split, 0 where rows are not split: at least 4
 // parts (4096 logits) each, and no more in all than one to a CU: each adds its
-// histogram's 2048 bins to the row's (64 x 131071: 41 us, with two to a CU of
-// 256 lanes 44, with four 58).
+// histogram's 2048 bins to the row's (64 x 131071: 41 us when measured, with two to
+// a CU of 256 lanes 44, with four 58).
 static int splits_of(int64_t N, int V) {
   if (V <= 16384 || N > 128) return 0;
   const int nparts = (V + 1023) / 1024;

@@ -41,7 +41,7 @@ def _declare():
 _declare()
 
 
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice  # the tensors are on a GPU: it is initialised
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the hipStream_t of a device's current stream
 
 
@@ -91,6 +91,14 @@ def _out(out, shape, dtype, device, name="out"):
     if out.device != device:
         raise ValueError(f"{name} must be on {device}, got {out.device}")
     return out
+
+
+def _matrix(out, N, D, dtype, device):
+    """(result, row stride): out, checked, or a new matrix."""
+    if out is None:
+        return torch.empty((N, D), dtype=dtype, device=device), D
+    out = _out(out, (N, D), dtype, device)
+    return out, _rows(out, "out")[3]
 
 
 class MXRows:
@@ -175,10 +183,10 @@ def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.T
     _mx(rows, "rows")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    device = rows.device
-    X = _out(out, (len(rows), rows.dim), dtype, device)
-    code, N, D, ld = _rows(X, "out")
-    _call(device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), code, ld)
+    device = rows.codes.device
+    N, D = rows.codes.shape[0], rows.dim
+    X, ld = _matrix(out, N, D, dtype, device)
+    _call(device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), _TYPES[dtype], ld)
     return X
 
 
@@ -206,13 +214,12 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
             raise TypeError("bias must be a float32 tensor")
         if bias.shape != (N,) or bias.device != device or not bias.is_contiguous():
             raise ValueError(f"bias must be {N} contiguous values on {device}")
-    C = _out(out, (M, N), dtype, device)
-    c_type, _, _, ldc = _rows(C, "out")
+    C, ldc = _matrix(out, M, N, dtype, device)
     need = _lib.gmm_mx_product_workspace(a_type, M, N, D)
     # the workspace belongs to this call: torch's allocator hands it on in stream order
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _call(device, _lib.gmm_mx_product, a, a_type, lda, a_scales, ldas, M, *B._args(), N, D,
-          None if bias is None else bias.data_ptr(), C.data_ptr(), c_type, ldc,
+          None if bias is None else bias.data_ptr(), C.data_ptr(), _TYPES[dtype], ldc,
           None if ws is None else ws.data_ptr(), need)
     return C
 
@@ -243,7 +250,7 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     if u.shape != (N,) or u.device != dev or not u.is_contiguous():
         raise ValueError(f"u must be {N} contiguous values on {dev}")
     ids = _out(out, (N,), torch.int32, dev)
-    if not ids.is_contiguous():
+    if out is not None and not ids.is_contiguous():
         raise ValueError("out must be contiguous")
     t_ptr, t = _setting(temperature, torch.float32, N, dev, "temperature")
     k_ptr, k = _setting(top_k, torch.int32, N, dev, "top_k")
