@@ -389,3 +389,40 @@ def test_compressed_topk():
     np.put_along_axis(nearer, i, False, 1)
     assert (score[nearer] <= (last[:, None] + 2 * tol)[nearer]).all()
     assert ivf_probe.compressed_topk(Q[:0], rows, X, k)[0].shape == (0, k)
+
+
+def test_calls_from_two_host_threads():
+    import threading
+
+    g = gen(9)
+    B = sc.mx_quantize(randn(g, 20_000, 256) / 16)
+    xs = [randn(g, n, 256) for n in (5, 90)]
+    us = [torch.rand(len(x), generator=g, device=DEV) for x in xs]
+
+    def work(i):
+        logits = sc.mx_product(xs[i], B)
+        return logits, sc.draw(logits, us[i], top_k=100, top_p=0.9)
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got[i].append(work(i))
+            stream.synchronize()
+        except Exception as e:  # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and [len(v) for v in got] == [20, 20]
+    for i in range(2):
+        for logits, ids in got[i]:
+            assert torch.equal(logits, want[i][0]) and torch.equal(ids, want[i][1])
