@@ -1305,7 +1305,7 @@ __global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Spli
 // histogram's 2048 bins to the row's (64 x 131071: 41 us when measured, with two to
 // a CU of 256 lanes 44, with four 58).
 static int splits_of(int64_t N, int V) {
-  if (V <= 16384 || N > 128) return 0;
+  if (N < 1 || V <= 16384 || N > 128) return 0;
   const int nparts = (V + 1023) / 1024;
   const int64_t a = (nparts + 3) / 4, b = 256 / N;
   const int64_t S = a < b ? a : b;

@@ -288,6 +288,13 @@ def test_equal_weights_divide_evenly():
         assert torch.equal(sc.draw(z, u[pick]).long(), pick)
 
 
+@pytest.mark.parametrize("width", [1, 1000, 16384, 16385, 131072, 2 ** 20])
+def test_draw_of_no_rows(width):
+    """Also at the widths whose rows would be split."""
+    z, u = torch.empty(0, width, device=DEV), torch.empty(0, device=DEV)
+    assert sc.draw(z, u, top_k=3, top_p=0.9).shape == (0,)
+
+
 # ---- workspaces, graphs and streams
 
 def test_workspace_contents_do_not_matter():

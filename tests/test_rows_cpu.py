@@ -1,10 +1,12 @@
 """The row operators without a GPU: the header and the binding agree, every
 refusal comes before the device is touched, and the references that the GPU
 tests use agree with hand-made cases."""
+import ast
 import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -205,3 +207,19 @@ def test_compressed_scan_refusals():
             ivf_probe.compressed_topk(X, rows, X, k, short)
     with pytest.raises(ValueError, match="on a GPU"):
         ivf_probe.compressed_topk(X, rows, X, 2, 4)
+
+
+def test_draw_workspace_sizes():
+    """The query at its smallest and largest arguments, no rows among them
+    (in a child: it has to answer, not end the process)."""
+    code = ("import soft_clustering_amd as sc; f = sc.raw_library().gmm_draw_workspace; "
+            "print([[f(n, v) for v in (1, 16384, 16385, 131072, 1 << 20)] for n in (0, 1, 128, 129, 1 << 30)])")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0, out.returncode
+    none, one, most, more, all_ = ast.literal_eval(out.stdout.splitlines()[-1])
+    assert none == more == all_ == [0] * 5
+    assert one[:2] == most[:2] == [0, 0]
+    assert one[2] == one[3] == one[4] > 0 and most[2:] == [128 * one[2]] * 3
+    f = sc.raw_library().gmm_draw_workspace
+    for bad in ((-1, 20000), ((1 << 30) + 1, 20000), (4, 0), (4, -5), (4, (1 << 20) + 1)):
+        assert f(*bad) == 0
