@@ -69,6 +69,8 @@ def _rows(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
     N, D = t.shape
+    if D >= 1 << 31:  # widths are int32 in the C ABI, which refuses the others
+        raise ValueError(f"{name} has rows of {D} values")
     ld, one = t.stride()
     if one != 1 and D > 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride(1) == 1)")

@@ -288,6 +288,16 @@ def test_equal_weights_divide_evenly():
         assert torch.equal(sc.draw(z, u[pick]).long(), pick)
 
 
+def test_rows_past_the_largest_width_are_refused():
+    """Among them one whose width is 5 in its low 32 bits."""
+    z, u = torch.zeros(1, 2 ** 32 + 5, dtype=torch.bfloat16, device=DEV), torch.full((1,), 0.5, device=DEV)
+    for call in (lambda: sc.draw(z, u), lambda: sc.mx_quantize(z)):
+        with pytest.raises(ValueError, match="rows of"):
+            call()
+    with pytest.raises(sc.GMMError, match="V must be"):
+        sc.draw(z[:, :2 ** 20 + 1], u)
+
+
 @pytest.mark.parametrize("width", [1, 1000, 16384, 16385, 131072, 2 ** 20])
 def test_draw_of_no_rows(width):
     """Also at the widths whose rows would be split."""

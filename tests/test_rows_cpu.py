@@ -223,3 +223,16 @@ def test_draw_workspace_sizes():
     f = sc.raw_library().gmm_draw_workspace
     for bad in ((-1, 20000), ((1 << 30) + 1, 20000), (4, 0), (4, -5), (4, (1 << 20) + 1)):
         assert f(*bad) == 0
+
+
+def test_widths_past_32_bits_are_refused():
+    """The C ABI's widths are int32: a wider row must not be taken for a short one."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    from soft_clustering_amd.rows import _rows
+
+    with FakeTensorMode():
+        for width in (2 ** 31, 2 ** 32 + 5, 2 ** 40 + 128):
+            x = torch.empty(1, width, dtype=torch.bfloat16, device="cuda")
+            with pytest.raises(ValueError, match="rows of"):
+                _rows(x, "logits")
+        assert _rows(torch.empty(3, 2 ** 31 - 1, dtype=torch.bfloat16, device="cuda"), "X")[2] == 2 ** 31 - 1
