@@ -107,7 +107,7 @@ def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortli
     out_i, out_d = [], []
     for s in range(0, Q.shape[0], batch):
         q = Q[s:s + batch]
-        cand = torch.topk(mx_product(q, rows, bias=bias), shortlist, dim=1, sorted=False).indices
+        cand = torch.topk(mx_product(q.detach(), rows, bias=bias.detach()), shortlist, dim=1, sorted=False).indices
         d2 = (X[cand].to(torch.float64) - q[:, None].to(torch.float64)).square().sum(2)
         top = torch.topk(_keys(d2, cand), k, dim=1, largest=False, sorted=True).values
         out_i.append(top & ((1 << ID_BITS) - 1))

@@ -4,7 +4,9 @@ held in 4 bits, their products, and draws from rows of logits.
 Argument marshalling only, as in the binding of the mixture calls: tensors are
 checked for dtype, device, layout and shape, then the HIP kernels run on the
 current stream of the tensors' device.  Outputs come from torch's allocator;
-the calls synchronise nothing and can be captured into a graph.
+the calls synchronise nothing and can be captured into a graph.  None has a
+backward: rows, products and results that require gradients are refused while
+gradients are on (a draw's ids are whole numbers and never have one).
 """
 from __future__ import annotations
 
@@ -81,6 +83,12 @@ def _rows(t, name):
     return code, N, D, ld
 
 
+def _no_gradient(t, name):
+    """There is no backward: what would need one is refused."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires gradients, which this call does not compute (detach it, or use no_grad)")
+
+
 def _out(out, shape, dtype, device, name="out"):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -100,6 +108,7 @@ def _matrix(out, N, D, dtype, device):
     if out is None:
         return torch.empty((N, D), dtype=dtype, device=device), D
     out = _out(out, (N, D), dtype, device)
+    _no_gradient(out, "out")
     return out, _rows(out, "out")[3]
 
 
@@ -170,6 +179,7 @@ def _mx(t, name):
 def mx_quantize(X: torch.Tensor, out: MXRows | None = None) -> MXRows:
     """The rows of X (float32, bfloat16 or float16) in 4 bits."""
     code, N, D, ld = _rows(X, "X")
+    _no_gradient(X, "X")
     device = X.device
     if out is None:
         out = MXRows._empty(N, D, device)
@@ -205,6 +215,7 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
         a_type, (a, lda, a_scales, ldas) = TYPE_MX, A._args()
     else:
         a_type, M, D, lda = _rows(A, "A")
+        _no_gradient(A, "A")
         a, a_scales, ldas = A.data_ptr(), None, 0
     if D != B.dim:
         raise ValueError(f"A has rows of {D} values, B of {B.dim}")
@@ -216,6 +227,7 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
             raise TypeError("bias must be a float32 tensor")
         if bias.shape != (N,) or bias.device != device or not bias.is_contiguous():
             raise ValueError(f"bias must be {N} contiguous values on {device}")
+        _no_gradient(bias, "bias")
     C, ldc = _matrix(out, M, N, dtype, device)
     need = _lib.gmm_mx_product_workspace(a_type, M, N, D)
     # the workspace belongs to this call: torch's allocator hands it on in stream order

@@ -443,3 +443,19 @@ def test_binding_refusals():
         sc.draw(x, u, temperature=-1.0)
     with pytest.raises(TypeError, match="out"):
         sc.draw(x, u, out=torch.empty(4, dtype=torch.int64, device=DEV))
+
+
+def test_gradients_are_refused_or_off():
+    x = randn(gen(10), 4, 128)
+    B, bias, u = sc.mx_quantize(x), randn(gen(11), 4), torch.rand(4, device=DEV)
+    want, ids = sc.mx_product(x, B, bias=bias), sc.draw(x, u)
+    x.requires_grad_(), bias.requires_grad_()
+    with pytest.raises(ValueError, match="A requires"):
+        sc.mx_product(x, B)
+    with pytest.raises(ValueError, match="X requires"):
+        sc.mx_quantize(x)
+    assert torch.equal(sc.draw(x, u), ids)
+    assert torch.equal(sc.mx_product(x.detach(), B, bias=bias.detach()), want)
+    with torch.no_grad():
+        assert torch.equal(sc.mx_product(x, B, bias=bias), want)
+        assert torch.equal(sc.mx_quantize(x).codes, B.codes)

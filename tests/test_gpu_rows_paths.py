@@ -408,6 +408,15 @@ def test_compressed_topk():
     assert ivf_probe.compressed_topk(Q[:0], rows, X, k)[0].shape == (0, k)
 
 
+def test_compressed_topk_of_tensors_with_gradients():
+    """Its results are whole numbers: nothing to refuse."""
+    g = gen(10)
+    X = torch.randint(0, 50, (300, 40), generator=g, device=DEV).float()
+    rows, want = sc.mx_quantize(X), ivf_probe.exact_topk(X[:5], X, 3)
+    got = ivf_probe.compressed_topk(X[:5].clone().requires_grad_(), rows, X.clone().requires_grad_(), 3, 300)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_calls_from_two_host_threads():
     import threading
 

@@ -236,3 +236,26 @@ def test_widths_past_32_bits_are_refused():
             with pytest.raises(ValueError, match="rows of"):
                 _rows(x, "logits")
         assert _rows(torch.empty(3, 2 ** 31 - 1, dtype=torch.bfloat16, device="cuda"), "X")[2] == 2 ** 31 - 1
+
+
+def test_inputs_that_need_gradients_are_refused():
+    """The products have no backward: a result without a graph would be a wrong
+    gradient.  Without gradients (no_grad, detach) the same tensors are taken."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    with FakeTensorMode():
+        x = torch.empty(4, 128, device="cuda", requires_grad=True)
+        plain = torch.empty(4, 128, device="cuda")
+        rows = sc.MXRows(torch.empty(4, 64, dtype=torch.uint8, device="cuda"),
+                         torch.empty(4, 4, dtype=torch.uint8, device="cuda"), 128)
+        bias = torch.empty(4, device="cuda", requires_grad=True)
+        with pytest.raises(ValueError, match="X requires"):
+            sc.mx_quantize(x)
+        with pytest.raises(ValueError, match="A requires"):
+            sc.mx_product(x, rows)
+        with pytest.raises(ValueError, match="bias requires"):
+            sc.mx_product(plain, rows, bias=bias)
+        with pytest.raises(ValueError, match="out requires"):
+            sc.mx_dequantize(rows, out=x)
+        with pytest.raises(ValueError, match="out requires"):
+            sc.mx_product(rows, rows, out=torch.empty(4, 4, device="cuda", requires_grad=True))
