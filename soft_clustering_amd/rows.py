@@ -43,8 +43,10 @@ def _declare():
 _declare()
 
 
-_current_device = torch._C._cuda_getDevice  # the tensors are on a GPU: it is initialised
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the hipStream_t of a device's current stream
+# The tensors of a call are on a GPU, so it is initialised; a torch without GPU
+# support has neither function and never makes a call.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the hipStream_t of a device's current stream
 
 
 def _call(device, fn, *args):

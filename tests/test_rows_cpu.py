@@ -259,3 +259,16 @@ def test_inputs_that_need_gradients_are_refused():
             sc.mx_dequantize(rows, out=x)
         with pytest.raises(ValueError, match="out requires"):
             sc.mx_product(rows, rows, out=torch.empty(4, 4, device="cuda", requires_grad=True))
+
+
+def test_import_on_a_torch_without_gpu_support():
+    """The package, its generators and the probe do not need torch's GPU bindings."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda')]: delattr(torch._C, n)\n"
+            "import soft_clustering_amd as sc\n"
+            "from soft_clustering_amd import datagen, ivf_probe\n"
+            "X = torch.arange(12.0).reshape(4, 3)\n"
+            "print(ivf_probe.exact_topk(X, X, 1)[0].flatten().tolist())\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.splitlines()[-1] == "[0, 1, 2, 3]"
