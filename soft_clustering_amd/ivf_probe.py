@@ -84,18 +84,41 @@ def exact_topk(Q: torch.Tensor, X: torch.Tensor, k: int = 10, batch: int = 64):
     return torch.cat(out_i), torch.cat(out_d)
 
 
-def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortlist: int = 200, batch: int = 256):
-    """Top-k as exact_topk, among the `shortlist` rows of X whose 4-bit copies
-    (rows = mx_quantize(X)) score best against the query: q.x - |x|^2 / 2 orders
-    by distance, the product taken from the 4-bit rows with the query rounded
-    to 4 bits on the way, the norms exact.  The shortlist is ranked by exact
-    distances.  The scan reads 68 bytes for 128 values instead of 512."""
+def scan_bias(X: torch.Tensor, part: int = 1 << 24) -> torch.Tensor:
+    """-|x|^2 / 2 of each row of X, rounded once to float32 (formed in float64,
+    `part` values at a time): the bias of compressed_topk's products, kept
+    beside mx_quantize(X)."""
+    if X.dtype != torch.float32 or X.dim() != 2:
+        raise TypeError("X must be a 2-D float32 tensor")
+    n, dim = X.shape
+    bias = torch.empty(n, dtype=torch.float32, device=X.device)
+    step = max(1, part // max(1, dim))
+    for s in range(0, n, step):
+        x = X[s:s + step].detach()
+        _check_integral(x, "X")
+        bias[s:s + step] = x.to(torch.float64).square_().sum(1) / -2
+    return bias
+
+
+def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortlist: int = 200, batch: int = 256,
+                    bias: torch.Tensor | None = None):
+    """Top-k as exact_topk (of integer-valued vectors, as there), among the
+    `shortlist` rows of X whose 4-bit copies (rows = mx_quantize(X)) score best
+    against the query: q.x - |x|^2 / 2 orders by distance, the product taken
+    from the 4-bit rows with the query rounded to 4 bits on the way, the norms
+    from X.  The shortlist is ranked by exact distances.
+
+    With bias = scan_bias(X), kept by the caller, a call reads 68 bytes for
+    each 128 stored values (and 4 a row) and the shortlisted rows of X, the
+    only ones then checked for integer values; without it, it forms the bias
+    first, from 512 bytes for each 128 values."""
     from .rows import MXRows, mx_product
 
     _check_integral(Q, "Q")
-    _check_integral(X, "X")
     if not isinstance(rows, MXRows):
         raise TypeError("rows must be MXRows")
+    if X.dtype != torch.float32 or X.dim() != 2:
+        raise TypeError("X must be a 2-D float32 tensor")
     n, dim = X.shape
     if len(rows) != n or rows.dim != dim or Q.shape[1] != dim:
         raise ValueError("Q, rows and X must have rows of the same width, rows and X as many")
@@ -103,12 +126,22 @@ def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortli
         raise ValueError("too many base vectors for the id packing")
     if not 1 <= k <= shortlist <= n:
         raise ValueError("k and shortlist must satisfy 1 <= k <= shortlist <= rows")
-    bias = (X.to(torch.float64).square().sum(1) / -2).to(torch.float32)
+    kept = bias is not None
+    if not kept:
+        bias = scan_bias(X)
+    elif not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32:
+        raise TypeError("bias must be a float32 tensor")
+    elif bias.shape != (n,) or bias.device != X.device:
+        raise ValueError(f"bias must be {n} values on {X.device}")
+    bias = bias.detach().contiguous()
     out_i, out_d = [], []
     for s in range(0, Q.shape[0], batch):
-        q = Q[s:s + batch]
-        cand = torch.topk(mx_product(q.detach(), rows, bias=bias.detach()), shortlist, dim=1, sorted=False).indices
-        d2 = (X[cand].to(torch.float64) - q[:, None].to(torch.float64)).square().sum(2)
+        q = Q[s:s + batch].detach()
+        cand = torch.topk(mx_product(q, rows, bias=bias), shortlist, dim=1, sorted=False).indices
+        x = X[cand].detach()
+        if kept:
+            _check_integral(x.flatten(0, 1), "X")
+        d2 = (x.to(torch.float64) - q[:, None].to(torch.float64)).square().sum(2)
         top = torch.topk(_keys(d2, cand), k, dim=1, largest=False, sorted=True).values
         out_i.append(top & ((1 << ID_BITS) - 1))
         out_d.append(top >> ID_BITS)
@@ -180,4 +213,4 @@ def dco_identity(offsets: torch.Tensor, n_rows: int, nprobe: int) -> float:
     return nprobe * n_rows * (nnz / n_rows) / K
 
 
-__all__ = ["probe", "exact_topk", "compressed_topk", "search", "recall", "dco_identity"]
+__all__ = ["probe", "exact_topk", "scan_bias", "compressed_topk", "search", "recall", "dco_identity"]

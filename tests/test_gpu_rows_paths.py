@@ -417,6 +417,42 @@ def test_compressed_topk_of_tensors_with_gradients():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_compressed_topk_with_a_kept_bias():
+    """The same results; X is then read at the shortlist alone, whose rows are
+    still checked."""
+    g = gen(11)
+    X = torch.randint(0, 200, (20_000, 96), generator=g, device=DEV).float()
+    Q = torch.randint(0, 200, (9, 96), generator=g, device=DEV).float()
+    rows, bias = sc.mx_quantize(X), ivf_probe.scan_bias(X)
+    want = ivf_probe.compressed_topk(Q, rows, X, 10, 100)
+    got = ivf_probe.compressed_topk(Q, rows, X, 10, 100, bias=bias)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    far = torch.topk(sc.mx_product(Q, rows, bias=bias), 101, dim=1).indices.unique()
+    left_out = torch.ones(20_000, dtype=torch.bool, device=DEV).index_fill(0, far, False)
+    Y = torch.where(left_out[:, None], 0.5, X)   # what no shortlist holds
+    got = ivf_probe.compressed_topk(Q, rows, Y, 10, 100, bias=bias)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    Y[want[0][3, 2], 5] += 0.25
+    with pytest.raises(ValueError, match="integer values"):
+        ivf_probe.compressed_topk(Q, rows, Y, 10, 100, bias=bias)
+
+
+def test_compressed_topk_makes_no_copy_of_the_base():
+    """2^21 x 128 values are 1 GiB, 2 GiB in float64."""
+    X = torch.randint(0, 200, (2 ** 21, 128), generator=gen(12), device=DEV, dtype=torch.int16).float()
+    rows = sc.mx_quantize(X)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    ivf_probe.compressed_topk(X[:1].clone(), rows, X)
+    assert torch.cuda.max_memory_allocated() - before < 2 ** 29
+    torch.cuda.reset_peak_memory_stats()
+    ivf_probe.compressed_topk(X[:1].clone(), rows, X, bias=torch.zeros(2 ** 21, device=DEV))
+    # no part of X in float64, 2^24 values or 2^27 bytes: the bias and the scores are 2^23
+    # bytes each, and topk, whose memory is the library's, holds a few 2^21 values of 12 bytes
+    assert torch.cuda.max_memory_allocated() - before < 2 ** 27
+
+
 def test_calls_from_two_host_threads():
     import threading
 

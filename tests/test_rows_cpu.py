@@ -272,3 +272,24 @@ def test_import_on_a_torch_without_gpu_support():
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert out.returncode == 0, out.stderr
     assert out.stdout.splitlines()[-1] == "[0, 1, 2, 3]"
+
+
+def test_scan_bias():
+    from soft_clustering_amd import ivf_probe
+
+    g = torch.Generator().manual_seed(1)
+    X = torch.randint(-300, 300, (5000, 37), generator=g).float()
+    want = (X.double() ** 2).sum(1).div(-2).float()
+    assert torch.equal(ivf_probe.scan_bias(X), want)
+    assert torch.equal(ivf_probe.scan_bias(X, part=1000), want)   # parts of 27 rows
+    assert torch.equal(ivf_probe.scan_bias(X, part=1), want)      # of one row
+    assert ivf_probe.scan_bias(X[:0]).shape == (0,)
+    X[4999, 36] += 0.5
+    with pytest.raises(ValueError, match="integer values"):
+        ivf_probe.scan_bias(X, part=1000)
+    with pytest.raises(TypeError, match="float32"):
+        ivf_probe.scan_bias(X.double())
+    rows = sc.MXRows(torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4, dtype=torch.uint8), 37)
+    for bad in (want[:7], want[:8].double(), want[:8, None]):
+        with pytest.raises((TypeError, ValueError), match="bias"):
+            ivf_probe.compressed_topk(X[:2], rows, X[:8], 2, 4, bias=bad)
