@@ -167,6 +167,47 @@ def test_product_of_whole_numbers_is_exact(m, n, dim):
     assert np.array_equal(f64(sc.mx_product(x, B)), want)
 
 
+# scale bytes of A and B: the smallest with the largest, products below float32's
+# normal range, below its smallest value, and near its largest
+@pytest.mark.parametrize("sa,sb", [(0, 254), (254, 0), (1, 126), (60, 60), (62, 40), (40, 60), (0, 110), (0, 0), (254, 100),
+                                   (120, 240)])
+@pytest.mark.parametrize("m,n,dim", [(2, 64, 256), (20, 65, 2304), (50, 64, 384), (70, 64, 256), (300, 130, 2304),
+                                     (4096, 4097, 2176)])
+def test_product_at_the_ends_of_the_range(m, n, dim, sa, sb):
+    """A term is a multiple of 2^-149 or off by less than one such step, as is
+    every sum of such terms below 2^-126 (exact there): dim steps in all, on
+    top of the dim 2^-23 of the sums above."""
+    r = np.random.default_rng(m + dim + 1000 * sa + sb)
+
+    def rows(k, scale):  # whole groups: padding would have to be zero
+        codes = r.integers(0, 256, (k, 64 * R.groups(dim)), dtype=np.uint8)
+        # neighbouring blocks a power of two apart, but for the ends
+        scales = np.clip(scale + r.integers(-1, 2, (k, 4 * R.groups(dim))), 0, 254).astype(np.uint8)
+        return sc.MXRows(torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), dim), codes, scales
+
+    A, ac, as_ = rows(m, sa)
+    B, bc, bs = rows(n, sb)
+    a, b = R.values(ac[-64:], as_[-64:], dim), R.values(bc[-64:], bs[-64:], dim)
+    got = f64(sc.mx_product(A, B)[-64:, -64:])
+    want, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    assert mag.max() < 2.0 ** 127 and np.isfinite(got).all()
+    tol = (dim + 2) * 2.0 ** -23 * mag + dim * 2.0 ** -149
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("m", [2, 40, 70])
+def test_product_past_the_range(m):
+    """Terms above float32's range: infinite, not a number where both signs meet."""
+    def rows(k, code, scale):
+        return sc.MXRows(torch.full((k, 64), code, dtype=torch.uint8, device=DEV),
+                         torch.full((k, 4), scale, dtype=torch.uint8, device=DEV), 128)
+
+    B = rows(33, 0x77, 200)
+    assert bool((sc.mx_product(rows(m, 0x77, 254), B) == float("inf")).all())
+    assert bool((sc.mx_product(rows(m, 0xFF, 254), B) == float("-inf")).all())
+    assert not bool(torch.isfinite(sc.mx_product(rows(m, 0xF7, 254), B)).any())
+
+
 def test_product_float_rows_equal_quantized_rows():
     for m in (1, 7, 16, 17, 64, 65, 200):
         g = gen(m)
