@@ -69,10 +69,10 @@ gmm_status gmm_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8
  * the way (a_scales is ignored), so the results are the same.
  * Products are summed in float32.  Each is exact where it lies within
  * float32's range (at most 8 bits of significand): one below 2^-149 counts to
- * within 2^-149, one above the range, or a partial sum there, is infinite and
- * gives NaN where it meets one of the other sign.  bias (float32[N]) may be
- * NULL; each result is rounded once to c_type (float, bfloat16 or half).  ldc
- * in elements, >= N.  A block of scale 255 makes its row's results NaN.
+ * within 2^-149; where the magnitudes of a result's products sum past the
+ * range, the result may be infinite or NaN.  bias (float32[N]) may be NULL;
+ * each result is rounded once to c_type (float, bfloat16 or half).  ldc in
+ * elements, >= N.  A block of scale 255 makes its row's results NaN.
  * workspace: gmm_mx_product_workspace bytes, 16-byte aligned, used by this
  * call alone until it completes; NULL where that is 0. */
 size_t gmm_mx_product_workspace(int32_t a_type, int64_t M, int64_t N, int32_t D);

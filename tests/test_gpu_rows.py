@@ -197,7 +197,9 @@ def test_product_at_the_ends_of_the_range(m, n, dim, sa, sb):
 
 @pytest.mark.parametrize("m", [2, 40, 70])
 def test_product_past_the_range(m):
-    """Terms above float32's range: infinite, not a number where both signs meet."""
+    """Terms above float32's range: infinite, but where both signs meet, as here
+    with a true sum of 0, that sum or no finite number (the matrix unit adds the
+    terms of one step before it rounds)."""
     def rows(k, code, scale):
         return sc.MXRows(torch.full((k, 64), code, dtype=torch.uint8, device=DEV),
                          torch.full((k, 4), scale, dtype=torch.uint8, device=DEV), 128)
@@ -205,7 +207,8 @@ def test_product_past_the_range(m):
     B = rows(33, 0x77, 200)
     assert bool((sc.mx_product(rows(m, 0x77, 254), B) == float("inf")).all())
     assert bool((sc.mx_product(rows(m, 0xFF, 254), B) == float("-inf")).all())
-    assert not bool(torch.isfinite(sc.mx_product(rows(m, 0xF7, 254), B)).any())
+    both = sc.mx_product(rows(m, 0xF7, 254), B)
+    assert bool(((both == 0) | ~torch.isfinite(both)).all())
 
 
 def test_product_float_rows_equal_quantized_rows():
