@@ -68,7 +68,7 @@ gmm_status gmm_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8
  * with row stride lda elements, which are quantised as by gmm_mx_quantize on
  * the way (a_scales is ignored), so the results are the same.
  * Products are summed in float32.  Each is exact where it lies within
- * float32's range (at most 8 bits of significand): one below 2^-149 counts to
+ * float32's range (at most 4 bits of significand): one below 2^-149 counts to
  * within 2^-149; where the magnitudes of a result's products sum past the
  * range, the result may be infinite or NaN.  bias (float32[N]) may be NULL;
  * each result is rounded once to c_type (float, bfloat16 or half).  ldc in
@@ -99,8 +99,10 @@ gmm_status gmm_mx_product(const void *A, int32_t a_type, int64_t lda, const uint
  * A logit of -inf has no weight.  A row that holds a NaN or +inf, or nothing
  * but -inf, has no distribution: ids[n] = -1.
  * Each setting is a device array of N values or, where that is NULL, one
- * value for all rows.  Weights are evaluated to 2^-43 of the largest and
- * summed as integers, so results do not depend on the order of the sums.
+ * value for all rows.  Weights are whole multiples of 2^-42 of the largest,
+ * each within 1.2 * 2^-43 (of the largest) of its value, so those below 2^-43
+ * are zero, and a sum of n of them is within n times that.  They are summed as
+ * integers, so results do not depend on the order of the sums.
  * 1 <= V <= 2^20, N <= 2^30.  workspace as gmm_mx_product. */
 size_t gmm_draw_workspace(int64_t N, int32_t V);
 gmm_status gmm_draw(const void *logits, int32_t type, int64_t N, int32_t V, int64_t ld, const float *u,

@@ -6,9 +6,12 @@
 // an integer.  Integer sums have no rounding, so a histogram of weights built
 // with LDS atomics, a sum over waves and a running sum agree whatever their
 // order, and every comparison with a border is made on one and the same
-// number.  The exponential is evaluated in float64 (a float32 one would move
-// the borders of the cumulative weights by 1e-7 of the sum, enough to change
-// draws); 2^42 V stays below 2^63 for V <= 2^20.
+// number.  The exponential is evaluated in float64: a weight is off by up to
+// 2^-43 of the largest from rounding and less than 2^-45.8 from the polynomial,
+// a sum by 1.2 V 2^-43 at most.  That comes to 1e-7 of the sum only where V is
+// near 2^20 and one element has nearly all the weight; float32 weights are off
+// by 6e-8 of themselves at any V, and their sums depend on the order.  2^42 V
+// stays below 2^63 for V <= 2^20.
 //
 // Rank order is the order of the pairs (logit descending, index ascending),
 // held as one integer, the place: inverted order key of the logit above the
@@ -77,7 +80,7 @@ __device__ __forceinline__ double fma_const(double a, double b, double c) {
 }
 // 2^42 2^t for t <= 0 (below 1/2 for t < -43 and NaN).  t = n + f with n whole
 // and |f| <= 1/2; 2^f = 1 + f q(f), q of degree 8 fitted to the least largest
-// error (2^-45.8); n goes into the exponent.
+// error (below 2^-45.8; 2^-45.3 of the result); n goes into the exponent.
 __device__ __forceinline__ double fixed_exp2(double t) {
   constexpr double kWhole = 6755399441055744.0 + kFix;  // 1.5 * 2^52: sums with it are whole, in the low bits
   t = fmax(t, -100.0);

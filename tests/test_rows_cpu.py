@@ -293,3 +293,24 @@ def test_scan_bias():
     for bad in (want[:7], want[:8].double(), want[:8, None]):
         with pytest.raises((TypeError, ValueError), match="bias"):
             ivf_probe.compressed_topk(X[:2], rows, X[:8], 2, 4, bias=bad)
+
+
+def test_accuracy_of_the_weights():
+    """The header promises weights within 1.2 * 2^-43 of the largest, V times that
+    for a sum: half of a step of 2^-42 from rounding and the error of the
+    polynomial of 2^f, |f| <= 1/2, which is found here from its constants (the
+    weight is 2^n 2^f with n <= 0; the float64 operations add less than 2^-48)."""
+    src = open(os.path.join(ROOT, "soft_clustering_amd", "csrc", "gmm_draw.hip")).read()
+    body = src[src.index("double fixed_exp2("):]
+    body = body[:body.index("return __hiloint2double")]
+    c = [float.fromhex(v) for v in re.findall(r"0x1\.[0-9a-f]+p[+-]\d+", body)]
+    assert len(c) == 9 and "q = fma(q, f, 1.0)" in body
+    f = np.linspace(-0.5, 0.5, 400_001).astype(np.longdouble)
+    q = np.zeros_like(f)
+    for k in c + [1.0]:
+        q = q * f + np.longdouble(k)
+    worst = float(np.abs(q - np.exp2(f)).max())
+    assert worst <= 2.0 ** -45.8
+    assert 2.0 ** -43 + worst + 2.0 ** -48 <= 1.2 * 2.0 ** -43
+    header = open(os.path.join(ROOT, "include", "flashgmm_rows.h")).read()
+    assert "within 1.2 * 2^-43" in header
