@@ -8,6 +8,7 @@ the default recompiles everything.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -20,6 +21,10 @@ LIB = os.path.join(HERE, "libflashgmm.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["gmm_kernels.hip", "gmm_assign.hip", "gmm_lists.hip", "gmm_api.hip", "gmm_mx.hip", "gmm_draw.hip",
            "gmm_rows_api.hip"]
+# Kernels with inline assembly that have to keep their values in registers:
+# variants that spilled vector registers gave wrong results, so a spill there
+# ends the build.
+NO_SPILL = ["gmm_mx.hip", "gmm_draw.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -50,12 +55,24 @@ def _stale(src: str, obj: str) -> bool:
     return os.path.getmtime(obj) < newest
 
 
+def spilled(msgs: str) -> list:
+    """(kernel, spilled vector registers) of the kernels that spill, from the
+    compiler's resource remarks."""
+    out, name = [], "?"
+    for kernel, spill in re.findall(r"remark: +(?:Function Name: (\S+)|VGPRs Spill: (\d+))", msgs):
+        if kernel:
+            name = kernel
+        elif int(spill):
+            out.append((name, int(spill)))
+    return out
+
+
 def _compile(src: str, verbose: bool, resource: bool, incremental: bool = False) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     if incremental and not resource and not _stale(src, obj):
         return obj
     cmd = [hipcc(), *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-    if resource:
+    if resource or src in NO_SPILL:
         cmd += ["-Rpass-analysis=kernel-resource-usage"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -64,6 +81,12 @@ def _compile(src: str, verbose: bool, resource: bool, incremental: bool = False)
                      if "packed-fp32-ops" not in l)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{msgs}")
+    if src in NO_SPILL:
+        bad = spilled(msgs)
+        if bad or "VGPRs Spill: " not in msgs:
+            os.remove(obj)
+            what = ", ".join(f"{k} ({n})" for k, n in bad) or "not reported by the compiler"
+            raise RuntimeError(f"{src}: spilled vector registers: {what}")
     if msgs.strip() and (verbose or resource):
         print(msgs, flush=True)
     return obj
