@@ -314,3 +314,16 @@ def test_accuracy_of_the_weights():
     assert 2.0 ** -43 + worst + 2.0 ** -48 <= 1.2 * 2.0 ** -43
     header = open(os.path.join(ROOT, "include", "flashgmm_rows.h")).read()
     assert "within 1.2 * 2^-43" in header
+
+
+def test_sanitizer_exercise_covers_the_row_operators():
+    """tests/native/rows_exercise.cpp calls every function of the header, and the
+    host build under sanitizers holds every source of the library."""
+    native = os.path.join(ROOT, "tests", "native")
+    called = set(re.findall(r"\b(gmm_[a-z_]+)\s*\(", open(os.path.join(native, "rows_exercise.cpp")).read()))
+    assert set(sc.ROW_EXPORTS) <= called
+    script = open(os.path.join(native, "build_sanitized.sh")).read()
+    sources = set(re.search(r"for src in ([a-z_ ]+); do", script).group(1).split())
+    built = re.search(r"SOURCES = \[(.*?)\]", open(os.path.join(ROOT, "soft_clustering_amd", "build.py")).read(), re.S)
+    assert sources == {v[:-4] for v in re.findall(r'"([a-z_]+\.hip)"', built.group(1))}
+    assert "rows_exercise" in script
