@@ -288,15 +288,18 @@ __device__ __forceinline__ unsigned lds_address(const void* p) {
 // LDS DMA: 16 bytes from base + off (a lane's own) to LDS at dst + 16 lane.
 // base and dst are uniform.  In assembly because the compiler, which cannot
 // tell the buffers apart, would otherwise wait for every DMA under way before
-// each LDS read; the waits in front of the barriers order them here.
+// each LDS read; the waits in front of the barriers order them here.  (That
+// LDS is written is said by the clobber: no LDS access moves across, which
+// reorders a few scalar instructions and costs nothing measurable.)
 __device__ __forceinline__ void lds_dma16(unsigned off, const uint8_t* base, unsigned dst) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
                "s"(__builtin_amdgcn_readfirstlane((int)dst))
-               : "m0");
+               : "m0", "memory");
 }
 
 // The same where on is ~0, nothing where it is 0: without a branch, across
-// which the compiler would move matrix instructions.
+// which the compiler would move matrix instructions.  EXEC, all ones here, is
+// the same again when the statement ends.
 __device__ __forceinline__ void lds_dma16_if(u64 on, unsigned off, const uint8_t* base, unsigned dst) {
   u64 all;
   asm volatile(
@@ -304,7 +307,7 @@ __device__ __forceinline__ void lds_dma16_if(u64 on, unsigned off, const uint8_t
       "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
       : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane((int)dst)), "s"(on)
-      : "m0");
+      : "m0", "memory");
 }
 
 template <int N>
