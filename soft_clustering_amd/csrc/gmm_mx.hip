@@ -263,10 +263,10 @@ template <int CT>
 __device__ __forceinline__ void put_c(typename Elem<CT>::T* p, float x) { *p = Elem<CT>::put(x); }
 
 // Large products: WM x WN waves, each with TM x TN blocks of 32 x 32.  A step
-// is one group (128 values, 64 bytes of a row); S LDS buffers of GPS groups are
-// filled by LDS DMA S - 1 buffers ahead.  Chunk c (16 bytes) of row r sits at
-// slot c ^ swz(r) of its 64 GPS bytes, so 8 consecutive rows' reads of one
-// chunk touch all banks.  v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the
+// is one group (128 values, 64 bytes of a row); two LDS buffers of GPS groups
+// are filled by LDS DMA, one while the other is read.  Chunk c (16 bytes) of
+// row r sits at slot c ^ swz(r) of its 64 GPS bytes, so 8 consecutive rows'
+// reads of one chunk touch all banks.  v_mfma_scale 32x32x64 takes two blocks of a row, lane half g the
 // block 2 g + h of a group in its step h: any assignment serves as long as both
 // sides share it, and this one makes a lane's two scale bytes neighbours.
 // Scales come for 4 steps at a time, in 16 bytes of each row (the last 4 groups
@@ -310,9 +310,8 @@ __device__ __forceinline__ void lds_dma16_if(u64 on, unsigned off, const uint8_t
       : "m0", "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void arrived() {  // all but the last N of this wave's DMA, its LDS accesses, everyone's
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+__device__ __forceinline__ void arrived() {  // this wave's DMA and LDS accesses, then everyone's
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
@@ -324,8 +323,8 @@ __device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
   m = 8 * b + in - n * rows;
 }
 
-template <int WM, int WN, int TM, int TN, int GPS, int S, bool SHORT, bool STREAM, int CT>
-__global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
+template <int WM, int WN, int TM, int TN, int GPS, bool SHORT, bool STREAM, int CT>
+__global__ void __launch_bounds__(64 * WM* WN, 2)
     k_mx_tile(const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ as, int64_t ldas, int M,
               const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ bs, int64_t ldbs, int N, int G,
               const float* __restrict__ bias, typename Elem<CT>::T* __restrict__ C, int64_t ldc, int tm, int tn) {
@@ -335,10 +334,10 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   constexpr int CH = 4 * GPS, RPI = 64 / CH;   // chunks of a row in a buffer, rows of a DMA instruction
   constexpr int OPS = ROWS / RPI / NW;         // DMA instructions of a wave for a buffer
   constexpr int SOPS = (ROWS / 64 + NW - 1) / NW;  // and for the scales of 4 steps
-  static_assert(ROWS % (RPI * NW) == 0 && (GPS == 1 || GPS == 2) && S >= 2 && S <= 4 / GPS && BM % 64 == 0 && BN % 64 == 0, "tile shape");
+  static_assert(ROWS % (RPI * NW) == 0 && (GPS == 1 || GPS == 2) && BM % 64 == 0 && BN % 64 == 0, "tile shape");
   constexpr int PITCH = 32 * TN + 4;  // floats of a row of results; rows 4 apart start 16 banks apart
   constexpr int OUT = NW * 32 * PITCH * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S * STEP > OUT ? S * STEP : OUT];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STEP > OUT ? 2 * STEP : OUT];
   __shared__ __attribute__((aligned(16))) uint4 scales[2][ROWS];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w % WM, wn = w / WM;
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   // straight run of instructions)
   auto stage = [&](int p) {
     const int64_t off = 64 * (int64_t)min(GPS * p, G - GPS);
-    const unsigned dst = lds0 + (unsigned)(p % S) * STEP + w * (OPS * 1024);
+    const unsigned dst = lds0 + (unsigned)(p % 2) * STEP + w * (OPS * 1024);
 #pragma unroll
     for (int i = 0; i < OPS; ++i) lds_dma16(voff[i], ((w * OPS + i) * RPI < BM ? pa : pb) + off, dst + i * 1024);
   };
@@ -395,8 +394,7 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   } else {
     stage_scales(0, ~0ull);
   }
-#pragma unroll
-  for (int k = 0; k < S - 1; ++k) stage(k);
+  stage(0);
 
   // Operands of a half step are read from LDS while the matrix unit works on
   // the half before; the barrier stands in front of a step's second half,
@@ -406,7 +404,7 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
   int qa[2][TM], qb[2][TN];  // scales of even and odd steps: this lane's two bytes
   auto read = [&](int k, int h) {
     const int p = k / GPS, half = GPS == 1 ? 0 : min(k - min(GPS * p, G - GPS), 1);
-    const uint8_t* cb = lds + (p % S) * STEP;
+    const uint8_t* cb = lds + (p % 2) * STEP;
     const int c = ((4 * half + 2 * g + h) ^ swz<GPS>(r32)) * 16;
     constexpr int ROW = 64 * GPS;
 #pragma unroll
@@ -425,12 +423,12 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
     __builtin_amdgcn_sched_barrier(0);
   };
   // Behind a barrier step k is in LDS for everyone, and what lies before it was
-  // read by everyone; the buffer before takes the groups S - 1 buffers on.  The
-  // scales of the next 4 steps follow 2 steps ahead at the latest, which is
-  // further than the wait leaves DMA outstanding.
+  // read by everyone; the buffer before takes the next groups.  The scales of
+  // the next 4 steps follow 2 steps ahead at the latest, so that a wait lies
+  // between them and their first use.
   auto refill = [&](int k) {
     if constexpr (!SHORT) stage_scales((k & ~3) + 4, (k & 3) == 0 ? ~0ull : 0ull);
-    stage(k / GPS + S - 1);
+    stage(k / GPS + 1);
   };
   // Products of a half step: rows I .. J - 1 of a wave's blocks, block Q of a
   // lane's two, scales of set E.
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
     GMM_MX_ROWS(0, 1, 0, E);               \
     read(K, 1);                            \
     GMM_MX_ROWS(1, TM, 0, E);              \
-    if (GPS == 1 || E == 1) arrived<(S - 2) * OPS>(); \
+    if (GPS == 1 || E == 1) arrived(); \
     GMM_MX_ROWS(0, 1, 1, E);               \
     read_scales((K) + 1, 1 - E);           \
     read((K) + 1, 0);                      \
@@ -459,7 +457,7 @@ __global__ void __launch_bounds__(64 * WM* WN, TM * TN >= 16 ? 1 : 2)
     GMM_MX_ROWS(2, TM, 1, E);              \
   } while (0)
 
-  arrived<(S - 2) * OPS>();
+  arrived();
   refill(0);
   read_scales(0, 0);
   read(0, 0);
@@ -732,7 +730,7 @@ static void few_rows(const MxProduct& p, int G, hipStream_t s) {
     few_rows_nt<AT, MT, MT == 4 ? 4 : 2, CT>(p, G, s);
 }
 
-template <int WM, int WN, int TM, int TN, int GPS, int S, int CT>
+template <int WM, int WN, int TM, int TN, int GPS, int CT>
 static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
@@ -753,21 +751,21 @@ static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
     if (G < 4) {
       if constexpr (!SMALL) {
         if (stream) {
-          launch(k_mx_tile<WM, WN, TM, TN, 1, 2, true, true, CT>);
+          launch(k_mx_tile<WM, WN, TM, TN, 1, true, true, CT>);
           return hipGetLastError();
         }
       }
-      launch(k_mx_tile<WM, WN, TM, TN, 1, 2, true, false, CT>);
+      launch(k_mx_tile<WM, WN, TM, TN, 1, true, false, CT>);
       return hipGetLastError();
     }
   }
   if constexpr (!SMALL) {
     if (stream) {
-      launch(k_mx_tile<WM, WN, TM, TN, GPS, S, false, true, CT>);
+      launch(k_mx_tile<WM, WN, TM, TN, GPS, false, true, CT>);
       return hipGetLastError();
     }
   }
-  launch(k_mx_tile<WM, WN, TM, TN, GPS, S, false, false, CT>);
+  launch(k_mx_tile<WM, WN, TM, TN, GPS, false, false, CT>);
   return hipGetLastError();
 }
 
@@ -798,9 +796,9 @@ static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
   // 128 x 128 tiles 32 and 30), but leave room for one workgroup of 256 x 128
   // on a CU instead of two (1024 x 100096 x 768: 111 and 136).
   const int64_t cus = 256;
-  if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 2, 2, CT>(p, G, s);
-  if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 1, 2, CT>(p, G, s);
-  return tiles<2, 2, 2, 2, 2, 2, CT>(p, G, s);
+  if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 2, CT>(p, G, s);
+  if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 1, CT>(p, G, s);
+  return tiles<2, 2, 2, 2, 2, CT>(p, G, s);
 }
 
 hipError_t launch_mx_product(const MxProduct& p0, void* workspace, hipStream_t s) {
