@@ -437,6 +437,33 @@ def test_compressed_topk_with_a_kept_bias():
         ivf_probe.compressed_topk(Q, rows, Y, 10, 100, bias=bias)
 
 
+def test_compressed_topk_with_the_norms_of_the_rows():
+    """The shortlist is then what lies nearest to the query among the values
+    that the 4-bit rows stand for, query rounded as well: all of it exact, as
+    the values are multiples of 2 below 2^8 (scales of 2^0 up), their squares'
+    sums below 2^24 and half of those multiples of 1/2."""
+    g = gen(13)
+    centre = torch.randint(40, 200, (300, 1, 64), generator=g, device=DEV).float()
+    X = (centre + torch.randint(-12, 13, (300, 20, 64), generator=g, device=DEV)).reshape(-1, 64)
+    Q = X[::71] + torch.randint(-3, 4, (85, 64), generator=g, device=DEV)
+    rows, (k, short) = sc.mx_quantize(X), (5, 40)
+    bias = ivf_probe.scan_bias(rows)
+    xh, qh = f64(sc.mx_dequantize(rows)), f64(sc.mx_dequantize(sc.mx_quantize(Q)))
+    assert np.array_equal(f64(bias), (xh ** 2).sum(1) / -2)
+    assert torch.equal(ivf_probe.scan_bias(rows, part=1000), bias)
+    got, d = ivf_probe.compressed_topk(Q, rows, X, k, short, bias=bias)
+    dh = ((qh[:, None] - xh[None]) ** 2).sum(2)
+    border = np.sort(dh, 1)[:, short - 1:short]
+    exact = ((f64(Q)[:, None] - f64(X)[None]) ** 2).sum(2)
+    for i in range(len(Q)):
+        inside = np.flatnonzero(dh[i] < border[i])          # in every shortlist; ties at the border may be
+        may = np.flatnonzero(dh[i] <= border[i])
+        best = np.sort(exact[i, inside])[:k]
+        assert set(got[i].tolist()) <= set(may.tolist())
+        assert np.array_equal(exact[i, got[i].cpu().numpy()], d[i].cpu().numpy())
+        assert (f64(d[i])[:len(best)] <= best).all()
+
+
 def test_compressed_topk_makes_no_copy_of_the_base():
     """2^21 x 128 values are 1 GiB, 2 GiB in float64."""
     X = torch.randint(0, 200, (2 ** 21, 128), generator=gen(12), device=DEV, dtype=torch.int16).float()

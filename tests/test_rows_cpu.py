@@ -289,6 +289,8 @@ def test_scan_bias():
         ivf_probe.scan_bias(X, part=1000)
     with pytest.raises(TypeError, match="float32"):
         ivf_probe.scan_bias(X.double())
+    with pytest.raises(TypeError, match="MXRows"):
+        ivf_probe.scan_bias([1.0])
     rows = sc.MXRows(torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4, dtype=torch.uint8), 37)
     for bad in (want[:7], want[:8].double(), want[:8, None]):
         with pytest.raises((TypeError, ValueError), match="bias"):
