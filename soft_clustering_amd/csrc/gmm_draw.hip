@@ -505,8 +505,8 @@ struct WaveRow {
 // ---------------------------------------------------------------------------
 // Longer rows: one workgroup of THREADS lanes to a row, which is read again in
 // every pass (kept in LDS, it left one workgroup to a CU, whose barriers nothing
-// covered: 4096 x 16384 324 us against 244, 4096 x 4096 52 against 41).  A part
-// is a run of AHEAD * 64 * VEC elements, which a wave takes in AHEAD loads of
+// covered: a third slower at 4096 x 16384 and a quarter at 4096 x 4096, when
+// both forms were there).  A part is a run of AHEAD * 64 * VEC elements, which a wave takes in AHEAD loads of
 // VEC a lane; parts go to the waves in turn.
 //
 // Passes over the row: the largest logit; a histogram (of counts for top-k, of
@@ -1109,7 +1109,11 @@ struct Split {
 // A wave takes `batch` (at most 32) consecutive rows, whose settings its lanes
 // read at once.  CUTS = false takes the rows without a cut by rank or mass, true
 // the others, or all where it runs alone.  (The next row's logits fetched during
-// a draw cost registers, and so waves: 91 us against 87 for 65536 x 1024.)
+// a draw cost registers, and so waves: 5 % more at 65536 x 1024.)  65536 x 1024
+// float32 without cuts: 86 us, 3.1 TB/s; what bounds it are the exponentials (42
+// vector instructions to a weight).  With cuts a weight is evaluated up to three
+// times, at 4 waves to a SIMD: 162 us with top-k 50, 236 with top-p 0.9, 268
+// with both.
 template <int TYPE, int TILES, bool CUTS>
 __global__ void __launch_bounds__(256, CUTS ? 4 : 6) k_draw_wave(DrawArgs a, int batch, int alone) {
   using R = WaveRow<TYPE, TILES, CUTS>;
@@ -1305,8 +1309,9 @@ __global__ void __launch_bounds__(1024) k_draw_split_pick(DrawArgs a, const Spli
 
 // Workgroups to a row of the split, 0 where rows are not split: at least 4
 // parts (4096 logits) each, and no more in all than one to a CU: each adds its
-// histogram's 2048 bins to the row's (64 x 131071: 41 us when measured, with two to
-// a CU of 256 lanes 44, with four 58).
+// histogram's 2048 bins to the row's (64 x 131071: 37 us, the same with two to a
+// CU).  128 x 131072 with top-p takes 80 us split, 129 rows, unsplit, 110: one
+// workgroup to a row leaves half of the CUs without work there.
 static int splits_of(int64_t N, int V) {
   if (N < 1 || V <= 16384 || N > 128) return 0;
   const int nparts = (V + 1023) / 1024;
@@ -1337,8 +1342,8 @@ static hipError_t split_rows(const DrawArgs& a, void* workspace, int S, hipStrea
 template <int TYPE, int TILES>
 static void wave_rows(const DrawArgs& a, hipStream_t s) {
   // enough rows to a wave that 4096 waves (4 to a SIMD) take them all, 4 at most
-  // (65536 x 1024: 123 us at 4 and 8, 128 at 16; one row to a wave, where each
-  // starts by waiting for its settings, then for its logits: 136)
+  // (65536 x 1024 in one run: 93 us at 4 and 8, 102 at 16; one row to a wave,
+  // where each starts by waiting for its settings, then for its logits: 105)
   int batch = (int)(a.N / 4096 < 1 ? 1 : a.N / 4096 > 4 ? 4 : a.N / 4096);
   // a launch has less than 2^32 lanes: at most 2^25 waves here
   if (a.N > (int64_t)batch << 25) batch = (int)((a.N + (1 << 25) - 1) >> 25);
@@ -1365,9 +1370,9 @@ static hipError_t draw_type(const DrawArgs& a, void* workspace, hipStream_t s) {
   else if (a.V <= 1024)
     wave_rows<TYPE, 4>(a, s);
   else if (a.V <= 4096)
-    block_rows<TYPE, 128, 1024, 4>(a, s);  // 4096 x 2000: 36 us; 256 lanes 51, 512 100
+    block_rows<TYPE, 128, 1024, 4>(a, s);  // 4096 x 2000, top-p: 46 us; 256 lanes 64
   else
-    block_rows<TYPE, 512, 2048, 1024>(a, s);  // 4096 x 16384: 244 us; 256 lanes 262, 1024 334
+    block_rows<TYPE, 512, 2048, 1024>(a, s);  // 4096 x 16384, top-p: 212 us; 256 lanes 207 to 233, 1024 330
   return hipGetLastError();
 }
 

@@ -227,8 +227,8 @@ static hipError_t dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* s
       hipLaunchKernelGGL(kernel, unit_blocks(rows, U, kDequantRuns), dim3(256), 0, s, codes + n * ldc, (unsigned)ldc,
                          scales + n * lds, (unsigned)lds, (unsigned)rows, D, (T*)X + n * ldx, ldx, U, 256 / U, 256 % U);
     };
-    // 10^6 x 128 float32 values take 93 us past the caches and 167 us through
-    // them, 8191 x 5120 bfloat16 (84 MB) 16 and 24 us
+    // 10^6 x 128 float32 values take 81 us past the caches and 101 us through
+    // them, 8191 x 5120 bfloat16 (84 MB) 16.5 and 17.1 us
     if (N * D * (int64_t)sizeof(T) > ((int64_t)32 << 20))
       launch(k_mx_dequantize<TYPE, true>);
     else
@@ -688,8 +688,8 @@ static int waves_for(int G, int most) {
 // Rows that are not in 4 bits are quantised inside the few-rows kernel where
 // that is at most one block for each of its threads.  Above, each of the
 // N / 32 workgroups would repeat more work than a kernel of its own costs:
-// 8 rows of 4096 float32 against 16384 rows take 19 us inside, 9 us and 2.5 us
-// apart; one row 10.4 us inside.
+// 8 rows of 4096 float32 against 16384 rows take 18.8 us inside, 13.5 us apart;
+// one row of bfloat16 10.7 us inside, 12.3 apart.
 static bool quantised_inside(int a_type, int64_t M, int G) {
   return a_type != kMx && M <= 16 && M * 4 * G <= 64 * waves_for(G, few_waves(1));
 }
@@ -719,9 +719,9 @@ static void few_rows_nt(const MxProduct& p, int G, hipStream_t s) {
     few_rows_as<AT, MT, NT, false, CT>(p, G, s);
 }
 // Blocks of 16 B rows to a wave: one where two would leave CUs idle (1 x 1024
-// x 8192: 6.7 us against 9.8), otherwise two (1 x 16384 x 4096: 8.9 us against
-// 10.1 with one), four where A has more rows to bring (64 x 16384 x 4096: 18 us
-// against 21 with two).
+// x 8192: 6.1 us against 8.4), otherwise two (1 x 16384 x 4096: 8.7 us against
+// 10.6 with one), four where A has more rows to bring (64 x 16384 x 4096: 16.1
+// us against 20.6 with two).
 template <int AT, int MT, int CT>
 static void few_rows(const MxProduct& p, int G, hipStream_t s) {
   if (p.N <= 16 * 512)
@@ -741,9 +741,9 @@ static hipError_t tiles(const MxProduct& p, int G, hipStream_t s) {
                        p.ldc, (int)tm, (int)tn);
   };
   // Past the caches go results that are larger than the last of them and whose
-  // rows are whole lines: 1024 x 100096 float32 of 768 products each 113 us
-  // against 144; but 8192 x 8192 bfloat16 of 128 products 39 us against 32,
-  // and 1024 x 100003, whose rows end inside lines, 187 us against 175.
+  // rows are whole lines: 1024 x 100096 float32 of 768 products each 108 us
+  // against 135; but 8192 x 8192 bfloat16 of 128 products 39 us against 29,
+  // and 1024 x 100003, whose rows end inside lines, 183 us against 169.
   constexpr int64_t size = sizeof(typename Elem<CT>::T);
   const bool stream = p.M * p.N * size > ((int64_t)256 << 20) && ((uintptr_t)p.C & 127) == 0 && p.ldc * size % 128 == 0;
   constexpr bool LARGE = WM * WN == 8, SMALL = TM * TN == 4;  // no short rows come with LARGE, no such result with SMALL
@@ -788,13 +788,13 @@ static hipError_t product(const MxProduct& p, int G, hipStream_t s) {
   }
   // The tile.  Large ones read less from L2 and LDS for each product, small
   // ones fill the 256 CUs and let a workgroup's stores overlap another's
-  // products.  Measured (us): 8192 x 8192 x 8192 311 with 256 x 256, 368 with
-  // 256 x 128, 439 with 128 x 128; 1024 x 100003 x 128 142, 111 and 131;
-  // 128 x 16384 x 4096 35, 26 and 19.
+  // products.  Measured (us): 8192 x 8192 x 8192 288 with 256 x 256, 345 with
+  // 256 x 128, 365 with 128 x 128; 1024 x 100003 x 128 109 with 256 x 128 and
+  // 105 with 128 x 128; 128 x 16384 x 4096 28.5 and 18.8.
   // Two groups to a buffer make the DMA read whole 128-byte lines and halve the
-  // barriers (one and two groups: 8192^3 330 and 311, 512 x 16384 x 4096 with
-  // 128 x 128 tiles 32 and 30), but leave room for one workgroup of 256 x 128
-  // on a CU instead of two (1024 x 100096 x 768: 111 and 136).
+  // barriers (6 % at 8192^3 and with 128 x 128 tiles at 512 x 16384 x 4096), but
+  // leave room for one workgroup of 256 x 128 on a CU instead of two (a fifth
+  // slower at 1024 x 100096 x 768).
   const int64_t cus = 256;
   if (G >= 16 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return tiles<2, 4, 4, 2, 2, CT>(p, G, s);
   if (((p.M + 255) / 256) * ((p.N + 127) / 128) >= 2 * cus) return tiles<2, 2, 4, 2, 1, CT>(p, G, s);
