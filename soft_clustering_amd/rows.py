@@ -6,7 +6,8 @@ checked for dtype, device, layout and shape, then the HIP kernels run on the
 current stream of the tensors' device.  Outputs come from torch's allocator;
 the calls synchronise nothing and can be captured into a graph.  None has a
 backward: rows, products and results that require gradients are refused while
-gradients are on (a draw's ids are whole numbers and never have one).
+gradients are on (a draw's ids are whole numbers and never have one).  A result
+that is given (out) must not share memory with an input.
 """
 from __future__ import annotations
 
@@ -89,6 +90,36 @@ def _no_gradient(t, name):
     """There is no backward: what would need one is refused."""
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires gradients, which this call does not compute (detach it, or use no_grad)")
+
+
+def _overlap(a, b):
+    """Whether two tensors of contiguous rows (or one) share memory; where both
+    have several rows at different strides, whether their ranges do."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+
+    def span(t):  # first byte, bytes of a row, of the step between rows, of all
+        row = (t.shape[-1] if t.dim() > 1 else t.numel()) * t.element_size()
+        step = t.stride(0) * t.element_size() if t.dim() > 1 and t.shape[0] > 1 else 0
+        return t.data_ptr(), row, step, (t.shape[0] - 1) * step + row
+
+    (pa, ra, sa, na), (pb, rb, sb, nb) = span(a), span(b)
+    if pa + na <= pb or pb + nb <= pa:
+        return False
+    step = sa or sb
+    if not step or (sa and sb and sa != sb):
+        return True
+    at = (pb - pa) % step  # b's rows seen from a's: in the gaps between them or not
+    return at < ra or at + rb > step
+
+
+def _apart(out, *inputs):
+    """A result that is given must not lie over what the call reads."""
+    for t in inputs:
+        if isinstance(t, MXRows):
+            _apart(out, t.codes, t.scales)
+        elif isinstance(t, torch.Tensor) and _overlap(out, t):
+            raise ValueError("out shares memory with an input")
 
 
 def _out(out, shape, dtype, device, name="out"):
@@ -187,6 +218,9 @@ def mx_quantize(X: torch.Tensor, out: MXRows | None = None) -> MXRows:
         out = MXRows._empty(N, D, device)
     elif len(_mx(out, "out")) != N or out.dim != D or out.device != device:
         raise ValueError(f"out must hold {N} rows of {D} values on {device}")
+    else:
+        _apart(out.codes, X)
+        _apart(out.scales, X)
     _call(device, _lib.gmm_mx_quantize, X.data_ptr(), code, N, D, ld, *out._args())
     return out
 
@@ -200,6 +234,8 @@ def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.T
     device = rows.codes.device
     N, D = rows.codes.shape[0], rows.dim
     X, ld = _matrix(out, N, D, dtype, device)
+    if out is not None:
+        _apart(out, rows)
     _call(device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), _TYPES[dtype], ld)
     return X
 
@@ -231,6 +267,8 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
             raise ValueError(f"bias must be {N} contiguous values on {device}")
         _no_gradient(bias, "bias")
     C, ldc = _matrix(out, M, N, dtype, device)
+    if out is not None:
+        _apart(out, A, B, bias)
     need = _lib.gmm_mx_product_workspace(a_type, M, N, D)
     # the workspace belongs to this call: torch's allocator hands it on in stream order
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
@@ -272,6 +310,8 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     k_ptr, k = _setting(top_k, torch.int32, N, dev, "top_k")
     p_ptr, p = _setting(top_p, torch.float32, N, dev, "top_p")
     m_ptr, m = _setting(min_p, torch.float32, N, dev, "min_p")
+    if out is not None:
+        _apart(out, logits, u, temperature, top_k, top_p, min_p)
     need = _lib.gmm_draw_workspace(N, V)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(dev, _lib.gmm_draw, logits.data_ptr(), code, N, V, ld, u.data_ptr(), t_ptr, float(t), k_ptr,

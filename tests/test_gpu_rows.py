@@ -503,3 +503,25 @@ def test_gradients_are_refused_or_off():
     with torch.no_grad():
         assert torch.equal(sc.mx_product(x, B, bias=bias), want)
         assert torch.equal(sc.mx_quantize(x).codes, B.codes)
+
+
+def test_results_over_inputs_are_refused():
+    g = gen(12)
+    x, u = randn(g, 6, 128), torch.rand(6, generator=g, device=DEV)
+    B = sc.mx_quantize(randn(g, 128, 128))
+    k, t = torch.full((6,), 3, dtype=torch.int32, device=DEV), torch.ones(6, device=DEV)
+    kept = x.clone()
+    for call in (lambda: sc.mx_product(x, B, out=x), lambda: sc.mx_product(x[:4], B, out=x[2:]),
+                 lambda: sc.mx_product(x, B, bias=x[5], out=x.new_empty(0).set_(x.untyped_storage(), 0, (6, 128), (128, 1))),
+                 lambda: sc.draw(x, u, top_k=k, out=k), lambda: sc.draw(x, u, out=u.view(torch.int32)),
+                 lambda: sc.draw(x, u, temperature=t, out=t.view(torch.int32)),
+                 lambda: sc.draw(x, u, out=x[1, 3:9].view(torch.int32)),
+                 lambda: sc.mx_dequantize(B[:8], out=B.codes.view(-1)[:8 * 128 * 4].view(torch.float32).view(8, 128)),
+                 lambda: sc.mx_quantize(x, out=sc.MXRows(x.view(torch.uint8)[:, :64], B.scales[:6], 128))):
+        with pytest.raises(ValueError, match="shares memory"):
+            call()
+    assert torch.equal(x, kept)
+    # neighbours in one buffer do not overlap
+    both = torch.zeros(6, 256, device=DEV)
+    both[:, :128] = x
+    assert torch.equal(sc.mx_product(both[:, :128], B, out=both[:, 128:]), sc.mx_product(x, B))

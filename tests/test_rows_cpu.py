@@ -329,3 +329,22 @@ def test_sanitizer_exercise_covers_the_row_operators():
     built = re.search(r"SOURCES = \[(.*?)\]", open(os.path.join(ROOT, "soft_clustering_amd", "build.py")).read(), re.S)
     assert sources == {v[:-4] for v in re.findall(r'"([a-z_]+\.hip)"', built.group(1))}
     assert "rows_exercise" in script
+
+
+def test_memory_shared_by_a_result_and_an_input():
+    """By brute force over the bytes of views of one buffer."""
+    from soft_clustering_amd.rows import _overlap
+
+    buf = torch.arange(60 * 20, dtype=torch.int16).reshape(60, 20)
+    views = [buf[0:10, 0:5], buf[0:10, 5:9], buf[0:10, 4:9], buf[3:30, 18:20], buf[3:30, 0:20], buf[10:20, 0:5],
+             buf[9, 0:5], buf[9, 6:20], buf[9:10, 5:20], buf[0:0], buf.view(-1)[7:1100], buf.view(30, 40)[2:9, 20:25],
+             buf.view(30, 40)[2:9, 0:20], buf[2:3, 19:20], buf.view(-1)[9 * 20 + 5:9 * 20 + 17], buf[:, 7]]
+    whole = [v for v in views if v.dim() == 2 or v.is_contiguous()]
+    for a in whole:
+        for b in whole:
+            shared = bool(set(a.flatten().tolist()) & set(b.flatten().tolist()))
+            found = _overlap(a, b)
+            # never missed; views whose rows lie at different strides may be taken to overlap
+            assert found or not shared, (a.shape, b.shape)
+            same = a.shape[0] < 2 or b.shape[0] < 2 or a.stride(0) == b.stride(0) or a.dim() == 1 or b.dim() == 1
+            assert found == shared or not same, (a.shape, b.shape)
