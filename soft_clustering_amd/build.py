@@ -44,7 +44,8 @@ def hipcc() -> str:
 
 
 HEADERS = [os.path.join(CSRC, "gmm_device.h"), os.path.join(CSRC, "gmm_internal.h"),
-           os.path.join(CSRC, "gmm_rows.h"), os.path.join(ROOT, "include", "flashgmm.h"),
+           os.path.join(CSRC, "gmm_rows.h"), os.path.join(CSRC, "gmm_rows_device.h"),
+           os.path.join(ROOT, "include", "flashgmm.h"),
            os.path.join(ROOT, "include", "flashgmm_rows.h")]
 
 
