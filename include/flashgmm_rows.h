@@ -1,6 +1,6 @@
 /*
  * flashgmm_rows.h - C ABI of the row operators for AMD Instinct MI355X
- * (gfx950): rows held in 4 bits, their products, and draws from rows of
+ * (gfx950): rows held in 4 or 8 bits, their products, and draws from rows of
  * logits.
  *
  * They serve what the mixture library (flashgmm.h) leaves a user with: many
@@ -33,7 +33,8 @@ typedef enum {
     GMM_TYPE_FLOAT = 0,    /* float32 */
     GMM_TYPE_BFLOAT = 1,   /* bfloat16 */
     GMM_TYPE_HALF = 2,     /* float16 */
-    GMM_TYPE_MX = 3        /* 4-bit codes and block scales (below) */
+    GMM_TYPE_MX = 3,       /* 4-bit codes and block scales (below) */
+    GMM_TYPE_BYTE = 4      /* 8-bit codes and block scales (below) */
 } gmm_type;
 
 /* Rows in 4 bits: the microscaling format MXFP4 of the OCP Microscaling
@@ -81,6 +82,51 @@ gmm_status gmm_mx_product(const void *A, int32_t a_type, int64_t lda, const uint
                           int64_t ld_b_scales, int64_t N, int32_t D, const float *bias,
                           void *C, int32_t c_type, int64_t ldc, void *workspace, size_t workspace_bytes,
                           void *hip_stream);
+
+/* Rows in 8 bits: E4M3 elements (OCP 8-bit Floating Point Specification 1.0:
+ * 1 sign, 4 exponent and 3 fraction bits, largest value 448, no infinities)
+ * and one power of two for each block of 128 consecutive values of a row.
+ *   value = e4m3(code) * 2^(scale - 127)
+ * Layout: a row of D values is padded to G = ceil(D / 128) groups of 128.
+ * codes: 128 G bytes a row; scales: 4 ceil(G / 4) bytes a row, the first G one
+ * for each group; padding has code 0 and scale 0.  Row strides are in bytes:
+ * ld_codes >= 128 G and a multiple of 16, ld_scales >= 4 ceil(G / 4) and a
+ * multiple of 4, both at most 2^23; codes 16-byte and scales 4-byte aligned.
+ * 1 <= D <= 2^20, at most 2^30 rows. */
+
+/* Quantisation: for each block, with m its largest magnitude,
+ *   e = max(ceil(log2(m / 448)), -127), scale = e + 127 (0 for a block of zeros),
+ *   code = x / 2^e rounded to the nearest E4M3 value (ties to the even code);
+ * the sign is kept, also of zeros.  No value is above 448 2^e.  A block that
+ * holds a NaN or an infinity gets scale 255 and codes 0: it stands for NaN
+ * throughout.  X has row stride ldx (elements, >= D). */
+gmm_status gmm_byte_quantize(const void *X, int32_t type, int64_t N, int32_t D, int64_t ldx,
+                             uint8_t *codes, int64_t ld_codes, uint8_t *scales, int64_t ld_scales,
+                             void *hip_stream);
+
+/* The values that 8-bit rows stand for, rounded once to the type of X (exact
+ * in float32, and in bfloat16 from 2^-130 on). */
+gmm_status gmm_byte_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales,
+                               int64_t N, int32_t D, void *X, int32_t type, int64_t ldx, void *hip_stream);
+
+/* Products of rows: C[m, n] = sum_d A[m, d] B[n, d] + bias[n], B in 8 bits, as
+ * gmm_mx_product: a_type GMM_TYPE_BYTE takes A's codes and scales, any other
+ * rows of that type, quantised as by gmm_byte_quantize on the way (the results
+ * are the same).  Products are summed in float32.  With float32 results each is
+ * exact where it lies within float32's range; a value of A or B below 2^-130
+ * counts to within 2^-134.  With 16-bit results a product may also lose what
+ * lies below 2^-13 of the largest among the 8 products of its place (d / 8):
+ * 1.4e-5 of the results of normal operands, before the rounding to 16 bits.
+ * Where the magnitudes of a result's products sum past float32's range, the
+ * result may be infinite or NaN.  A block of scale 255 makes its
+ * row's results NaN.  workspace: gmm_byte_product_workspace bytes, otherwise as
+ * gmm_mx_product. */
+size_t gmm_byte_product_workspace(int32_t a_type, int64_t M, int64_t N, int32_t D);
+gmm_status gmm_byte_product(const void *A, int32_t a_type, int64_t lda, const uint8_t *a_scales,
+                            int64_t ld_a_scales, int64_t M, const uint8_t *b_codes, int64_t ldb,
+                            const uint8_t *b_scales, int64_t ld_b_scales, int64_t N, int32_t D, const float *bias,
+                            void *C, int32_t c_type, int64_t ldc, void *workspace, size_t workspace_bytes,
+                            void *hip_stream);
 
 /* Draws: ids[n] is a component of row n of the logits (N x V, row stride ld
  * elements), drawn with the random number u[n] in [0, 1).  With z_i the row's

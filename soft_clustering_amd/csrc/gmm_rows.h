@@ -1,5 +1,6 @@
 // Internal interface of the row operators: gmm_rows_api.hip (argument checks)
-// calls the launchers of gmm_mx.hip and gmm_draw.hip.
+// calls the launchers of gmm_mx.hip, gmm_byte.hip, gmm_draw.hip and
+// gmm_losses.hip.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -12,7 +13,7 @@ namespace gmm {
 void set_free_error(const char* msg) noexcept;
 
 // Element types (values of gmm_type).
-constexpr int kFloat = 0, kBfloat = 1, kHalf = 2, kMx = 3;
+constexpr int kFloat = 0, kBfloat = 1, kHalf = 2, kMx = 3, kByte = 4;
 
 constexpr int kMxGroup = 128;  // values per group: 64 code bytes, 4 scale bytes
 inline int mx_groups(int D) { return (D + kMxGroup - 1) / kMxGroup; }
@@ -42,6 +43,18 @@ struct MxProduct {
 };
 size_t mx_product_workspace(int a_type, int64_t M, int64_t N, int D);
 hipError_t launch_mx_product(const MxProduct& p, void* workspace, hipStream_t s);
+
+constexpr int kByteGroup = 128;  // values per group: 128 code bytes, one scale byte
+inline int byte_groups(int D) { return (D + kByteGroup - 1) / kByteGroup; }
+constexpr int byte_scales(int G) { return (G + 3) & ~3; }  // scale bytes of a row
+
+hipError_t launch_byte_quantize(const void* X, int type, int64_t N, int D, int64_t ldx, uint8_t* codes, int64_t ldc,
+                                uint8_t* scales, int64_t lds, hipStream_t s);
+hipError_t launch_byte_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N,
+                                  int D, void* X, int type, int64_t ldx, hipStream_t s);
+using ByteProduct = MxProduct;  // the same fields, codes and scales of 8-bit rows
+size_t byte_product_workspace(int a_type, int64_t M, int64_t N, int D);
+hipError_t launch_byte_product(const ByteProduct& p, void* workspace, hipStream_t s);
 
 struct DrawArgs {
   const void* z;

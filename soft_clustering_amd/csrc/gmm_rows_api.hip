@@ -1,5 +1,5 @@
 // C ABI of the row operators (declared in include/flashgmm_rows.h): argument
-// checks, then one launcher of gmm_mx.hip or gmm_draw.hip.  Nothing here
+// checks, then one launcher of gmm_mx.hip, gmm_byte.hip or gmm_draw.hip.  Nothing here
 // allocates, synchronises or keeps state.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -67,20 +67,31 @@ gmm_status check_rows(const void* X, int32_t type, int64_t N, int32_t D, int64_t
   return GMM_OK;
 }
 
-gmm_status check_mx(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N, int32_t D,
-                    const char* name) {
+gmm_status check_held(const uint8_t* codes, int64_t ldc, int min_codes, const uint8_t* scales, int64_t lds,
+                      int min_scales, int64_t N, const char* name) {
   if (N == 0) return GMM_OK;
   if (!codes || !scales) return refuse(GMM_ERR_INVALID_ARG, "%s: codes and scales must be non-NULL", name);
   if (!aligned(codes, 16) || !aligned(scales, 4))
     return refuse(GMM_ERR_INVALID_ARG, "%s: codes must be 16-byte and scales 4-byte aligned", name);
-  const int G = gmm::mx_groups(D);
-  if (ldc < (int64_t)64 * G || (ldc & 15) || ldc > kMaxStride)
-    return refuse(GMM_ERR_INVALID_ARG, "%s: code stride must be in [%d, 2^23] and a multiple of 16 (got %lld)", name, 64 * G,
+  if (ldc < min_codes || (ldc & 15) || ldc > kMaxStride)
+    return refuse(GMM_ERR_INVALID_ARG, "%s: code stride must be in [%d, 2^23] and a multiple of 16 (got %lld)", name, min_codes,
                   (long long)ldc);
-  if (lds < (int64_t)4 * G || (lds & 3) || lds > kMaxStride)
-    return refuse(GMM_ERR_INVALID_ARG, "%s: scale stride must be in [%d, 2^23] and a multiple of 4 (got %lld)", name, 4 * G,
+  if (lds < min_scales || (lds & 3) || lds > kMaxStride)
+    return refuse(GMM_ERR_INVALID_ARG, "%s: scale stride must be in [%d, 2^23] and a multiple of 4 (got %lld)", name, min_scales,
                   (long long)lds);
   return GMM_OK;
+}
+
+gmm_status check_mx(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N, int32_t D,
+                    const char* name) {
+  const int G = gmm::mx_groups(D);
+  return check_held(codes, ldc, 64 * G, scales, lds, 4 * G, N, name);
+}
+
+gmm_status check_byte(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N, int32_t D,
+                      const char* name) {
+  const int G = gmm::byte_groups(D);
+  return check_held(codes, ldc, 128 * G, scales, lds, gmm::byte_scales(G), N, name);
 }
 
 gmm_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -88,6 +99,18 @@ gmm_status check_workspace(const void* ws, size_t have, size_t need) {
   if (!ws || have < need)
     return refuse(GMM_ERR_CAPACITY, "workspace of %zu bytes, the call needs %zu", ws ? have : (size_t)0, need);
   if (!aligned(ws, 16)) return refuse(GMM_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+  return GMM_OK;
+}
+
+// a product's bias and result
+gmm_status check_result(int64_t M, int64_t N, const float* bias, const void* C, int32_t c_type, int64_t ldc) {
+  if (!float_type(c_type)) return refuse(GMM_ERR_INVALID_ARG, "C: unknown element type %d", c_type);
+  if (M == 0 || N == 0) return GMM_OK;
+  if (!C) return refuse(GMM_ERR_INVALID_ARG, "C is NULL");
+  if (!aligned(C, type_size(c_type))) return refuse(GMM_ERR_INVALID_ARG, "C is not aligned to its elements");
+  if (ldc < N || ldc > ((int64_t)1 << 40))
+    return refuse(GMM_ERR_INVALID_ARG, "C: row stride %lld for rows of %lld", (long long)ldc, (long long)N);
+  if (bias && !aligned(bias, 4)) return refuse(GMM_ERR_INVALID_ARG, "bias is not aligned to its elements");
   return GMM_OK;
 }
 
@@ -134,19 +157,61 @@ gmm_status gmm_mx_product(const void* A, int32_t a_type, int64_t lda, const uint
     st = a_type == GMM_TYPE_MX ? check_mx((const uint8_t*)A, lda, a_scales, ld_a_scales, M, D, "A")
                                : check_rows(A, a_type, M, D, lda, "A");
   if (!st) st = check_mx(b_codes, ldb, b_scales, ld_b_scales, N, D, "B");
-  if (st) return st;
-  if (!float_type(c_type)) return refuse(GMM_ERR_INVALID_ARG, "C: unknown element type %d", c_type);
-  if (M == 0 || N == 0) return GMM_OK;
-  if (!C) return refuse(GMM_ERR_INVALID_ARG, "C is NULL");
-  if (!aligned(C, type_size(c_type))) return refuse(GMM_ERR_INVALID_ARG, "C is not aligned to its elements");
-  if (ldc < N || ldc > ((int64_t)1 << 40))
-    return refuse(GMM_ERR_INVALID_ARG, "C: row stride %lld for rows of %lld", (long long)ldc, (long long)N);
-  if (bias && !aligned(bias, 4)) return refuse(GMM_ERR_INVALID_ARG, "bias is not aligned to its elements");
+  if (!st) st = check_result(M, N, bias, C, c_type, ldc);
+  if (st || M == 0 || N == 0) return st;
   if ((st = check_workspace(workspace, workspace_bytes, gmm::mx_product_workspace(a_type, M, N, D)))) return st;
   if ((st = check_device())) return st;
   gmm::MxProduct p{A, a_type, lda, a_scales, ld_a_scales, M, b_codes, ldb, b_scales, ld_b_scales, N, D, bias, C,
                    c_type, ldc};
   return launched(gmm::launch_mx_product(p, workspace, (hipStream_t)hip_stream), "product launch");
+}
+
+gmm_status gmm_byte_quantize(const void* X, int32_t type, int64_t N, int32_t D, int64_t ldx, uint8_t* codes,
+                             int64_t ld_codes, uint8_t* scales, int64_t ld_scales, void* hip_stream) {
+  gmm_status st = check_sizes(N, D, "N", "D");
+  if (!st) st = check_rows(X, type, N, D, ldx, "X");
+  if (!st) st = check_byte(codes, ld_codes, scales, ld_scales, N, D, "output");
+  if (st || N == 0) return st;
+  if ((st = check_device())) return st;
+  return launched(gmm::launch_byte_quantize(X, type, N, D, ldx, codes, ld_codes, scales, ld_scales,
+                                            (hipStream_t)hip_stream), "quantise launch");
+}
+
+gmm_status gmm_byte_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
+                               int64_t N, int32_t D, void* X, int32_t type, int64_t ldx, void* hip_stream) {
+  gmm_status st = check_sizes(N, D, "N", "D");
+  if (!st) st = check_byte(codes, ld_codes, scales, ld_scales, N, D, "input");
+  if (!st) st = check_rows(X, type, N, D, ldx, "X");
+  if (st || N == 0) return st;
+  if ((st = check_device())) return st;
+  return launched(gmm::launch_byte_dequantize(codes, ld_codes, scales, ld_scales, N, D, X, type, ldx,
+                                              (hipStream_t)hip_stream), "dequantise launch");
+}
+
+size_t gmm_byte_product_workspace(int32_t a_type, int64_t M, int64_t N, int32_t D) {
+  if ((!float_type(a_type) && a_type != GMM_TYPE_BYTE) || M < 0 || M > kMaxRows || N < 0 || N > kMaxRows || D < 1 ||
+      D > kMaxWidth)
+    return 0;
+  return gmm::byte_product_workspace(a_type, M, N, D);
+}
+
+gmm_status gmm_byte_product(const void* A, int32_t a_type, int64_t lda, const uint8_t* a_scales, int64_t ld_a_scales,
+                            int64_t M, const uint8_t* b_codes, int64_t ldb, const uint8_t* b_scales,
+                            int64_t ld_b_scales, int64_t N, int32_t D, const float* bias, void* C, int32_t c_type,
+                            int64_t ldc, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  gmm_status st = check_sizes(M, D, "M", "D");
+  if (!st) st = check_sizes(N, D, "N", "D");
+  if (!st)
+    st = a_type == GMM_TYPE_BYTE ? check_byte((const uint8_t*)A, lda, a_scales, ld_a_scales, M, D, "A")
+                                 : check_rows(A, a_type, M, D, lda, "A");
+  if (!st) st = check_byte(b_codes, ldb, b_scales, ld_b_scales, N, D, "B");
+  if (!st) st = check_result(M, N, bias, C, c_type, ldc);
+  if (st || M == 0 || N == 0) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, gmm::byte_product_workspace(a_type, M, N, D)))) return st;
+  if ((st = check_device())) return st;
+  gmm::ByteProduct p{A, a_type, lda, a_scales, ld_a_scales, M, b_codes, ldb, b_scales, ld_b_scales, N, D, bias, C,
+                     c_type, ldc};
+  return launched(gmm::launch_byte_product(p, workspace, (hipStream_t)hip_stream), "product launch");
 }
 
 size_t gmm_draw_workspace(int64_t N, int32_t V) {

@@ -1,5 +1,5 @@
 """Row operators of libflashgmm.so (C ABI in include/flashgmm_rows.h): rows
-held in 4 bits, their products, and draws from rows of logits.
+held in 4 or 8 bits, their products, and draws from rows of logits.
 
 Argument marshalling only, as in the binding of the mixture calls: tensors are
 checked for dtype, device, layout and shape, then the HIP kernels run on the
@@ -17,9 +17,10 @@ import torch
 
 from ._lib import GMM_OK, GMMError, raw_library
 
-TYPE_FLOAT, TYPE_BFLOAT, TYPE_HALF, TYPE_MX = 0, 1, 2, 3
+TYPE_FLOAT, TYPE_BFLOAT, TYPE_HALF, TYPE_MX, TYPE_BYTE = 0, 1, 2, 3, 4
 _TYPES = {torch.float32: TYPE_FLOAT, torch.bfloat16: TYPE_BFLOAT, torch.float16: TYPE_HALF}
 ROW_EXPORTS = ["gmm_mx_quantize", "gmm_mx_dequantize", "gmm_mx_product_workspace", "gmm_mx_product",
+               "gmm_byte_quantize", "gmm_byte_dequantize", "gmm_byte_product_workspace", "gmm_byte_product",
                "gmm_draw_workspace", "gmm_draw"]
 
 _lib = raw_library()
@@ -35,6 +36,8 @@ def _declare():
         "gmm_draw_workspace": (sz, [i64, i32]),
         "gmm_draw": (i32, [vp, i32, i64, i32, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, sz, vp]),
     }
+    for name in ("quantize", "dequantize", "product_workspace", "product"):
+        sig["gmm_byte_" + name] = sig["gmm_mx_" + name]
     for name, (res, args) in sig.items():
         fn = getattr(_lib, name)
         fn.restype = res
@@ -116,7 +119,7 @@ def _overlap(a, b):
 def _apart(out, *inputs):
     """A result that is given must not lie over what the call reads."""
     for t in inputs:
-        if isinstance(t, MXRows):
+        if isinstance(t, _HeldRows):
             _apart(out, t.codes, t.scales)
         elif isinstance(t, torch.Tensor) and _overlap(out, t):
             raise ValueError("out shares memory with an input")
@@ -145,18 +148,21 @@ def _matrix(out, N, D, dtype, device):
     return out, _rows(out, "out")[3]
 
 
-class MXRows:
-    """Rows in 4 bits: codes uint8 (N, 64 G) and scales uint8 (N, 4 G) of rows
-    of ``dim`` values, G = ceil(dim / 128).  Slicing with a step of one gives
-    the rows in the slice, sharing memory."""
+class _HeldRows:
+    """Rows in codes and block scales (MXRows, ByteRows)."""
 
     __slots__ = ("codes", "scales", "dim")
+
+    @staticmethod
+    def _widths(groups):  # code and scale bytes of a row of so many groups of 128 values
+        raise NotImplementedError
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, dim: int):
         groups = -(-int(dim) // 128)
         if dim < 1:
             raise ValueError("dim must be >= 1")
-        for t, width, unit, name in ((codes, 64 * groups, 16, "codes"), (scales, 4 * groups, 4, "scales")):
+        code_width, scale_width = self._widths(groups)
+        for t, width, unit, name in ((codes, code_width, 16, "codes"), (scales, scale_width, 4, "scales")):
             if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
                 raise TypeError(f"{name} must be a uint8 tensor")
             if t.dim() != 2 or t.shape[1] != width:
@@ -173,7 +179,7 @@ class MXRows:
     def __getitem__(self, rows: slice):
         if not isinstance(rows, slice) or rows.step not in (None, 1):
             raise TypeError("rows are taken with a slice of step 1")
-        return MXRows(self.codes[rows], self.scales[rows], self.dim)
+        return type(self)(self.codes[rows], self.scales[rows], self.dim)
 
     @property
     def device(self):
@@ -183,52 +189,73 @@ class MXRows:
     def nbytes(self):
         return self.codes.numel() + self.scales.numel()
 
-    @staticmethod
-    def _empty(N, D, device):
+    @classmethod
+    def _empty(cls, N, D, device):
         """Rows to be written (nothing to check)."""
-        G = -(-D // 128)
-        rows = object.__new__(MXRows)
-        rows.codes = torch.empty((N, 64 * G), dtype=torch.uint8, device=device)
-        rows.scales = torch.empty((N, 4 * G), dtype=torch.uint8, device=device)
+        code_width, scale_width = cls._widths(-(-D // 128))
+        rows = object.__new__(cls)
+        rows.codes = torch.empty((N, code_width), dtype=torch.uint8, device=device)
+        rows.scales = torch.empty((N, scale_width), dtype=torch.uint8, device=device)
         rows.dim = D
         return rows
 
     def _args(self):
         c, s = self.codes, self.scales
-        N, wc = c.shape
-        if N > 1:
+        if c.shape[0] > 1:
             return c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0)
-        return c.data_ptr(), wc, s.data_ptr(), wc // 16
+        return c.data_ptr(), c.shape[1], s.data_ptr(), s.shape[1]
 
 
-def _mx(t, name):
-    if not isinstance(t, MXRows):
-        raise TypeError(f"{name} must be MXRows")
+class MXRows(_HeldRows):
+    """Rows in 4 bits: codes uint8 (N, 64 G) and scales uint8 (N, 4 G) of rows
+    of ``dim`` values, G = ceil(dim / 128).  Slicing with a step of one gives
+    the rows in the slice, sharing memory."""
+
+    __slots__ = ()
+
+    @staticmethod
+    def _widths(groups):
+        return 64 * groups, 4 * groups
+
+
+class ByteRows(_HeldRows):
+    """Rows in 8 bits (E4M3, a power of two for each block of 128 values): codes
+    uint8 (N, 128 G) and scales uint8 (N, 4 ceil(G / 4)) of rows of ``dim``
+    values, G = ceil(dim / 128).  Slicing with a step of one gives the rows in
+    the slice, sharing memory."""
+
+    __slots__ = ()
+
+    @staticmethod
+    def _widths(groups):
+        return 128 * groups, -(-groups // 4) * 4
+
+
+def _held(t, kind, name):
+    if not isinstance(t, kind):
+        raise TypeError(f"{name} must be {kind.__name__}")
     if not t.codes.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
     return t
 
 
-def mx_quantize(X: torch.Tensor, out: MXRows | None = None) -> MXRows:
-    """The rows of X (float32, bfloat16 or float16) in 4 bits."""
+def _quantize(kind, fn, X, out):
     code, N, D, ld = _rows(X, "X")
     _no_gradient(X, "X")
     device = X.device
     if out is None:
-        out = MXRows._empty(N, D, device)
-    elif len(_mx(out, "out")) != N or out.dim != D or out.device != device:
+        out = kind._empty(N, D, device)
+    elif len(_held(out, kind, "out")) != N or out.dim != D or out.device != device:
         raise ValueError(f"out must hold {N} rows of {D} values on {device}")
     else:
         _apart(out.codes, X)
         _apart(out.scales, X)
-    _call(device, _lib.gmm_mx_quantize, X.data_ptr(), code, N, D, ld, *out._args())
+    _call(device, fn, X.data_ptr(), code, N, D, ld, *out._args())
     return out
 
 
-def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
-    """The values that 4-bit rows stand for, rounded once to dtype (exact in
-    float32 and bfloat16)."""
-    _mx(rows, "rows")
+def _dequantize(kind, fn, rows, dtype, out):
+    _held(rows, kind, "rows")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
     device = rows.codes.device
@@ -236,21 +263,18 @@ def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.T
     X, ld = _matrix(out, N, D, dtype, device)
     if out is not None:
         _apart(out, rows)
-    _call(device, _lib.gmm_mx_dequantize, *rows._args(), N, D, X.data_ptr(), _TYPES[dtype], ld)
+    _call(device, fn, *rows._args(), N, D, X.data_ptr(), _TYPES[dtype], ld)
     return X
 
 
-def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
-               out: torch.Tensor | None = None) -> torch.Tensor:
-    """A B^T + bias as a (rows of A) x (rows of B) matrix of dtype.  A: MXRows,
-    or a tensor of rows that is quantised on the way (the same results)."""
-    _mx(B, "B")
+def _product(kind, held_type, workspace, fn, A, B, bias, dtype, out):
+    _held(B, kind, "B")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
     device = B.device
-    if isinstance(A, MXRows):
+    if isinstance(A, kind):
         M, D = len(A), A.dim
-        a_type, (a, lda, a_scales, ldas) = TYPE_MX, A._args()
+        a_type, (a, lda, a_scales, ldas) = held_type, A._args()
     else:
         a_type, M, D, lda = _rows(A, "A")
         _no_gradient(A, "A")
@@ -269,13 +293,51 @@ def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtyp
     C, ldc = _matrix(out, M, N, dtype, device)
     if out is not None:
         _apart(out, A, B, bias)
-    need = _lib.gmm_mx_product_workspace(a_type, M, N, D)
+    need = workspace(a_type, M, N, D)
     # the workspace belongs to this call: torch's allocator hands it on in stream order
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _call(device, _lib.gmm_mx_product, a, a_type, lda, a_scales, ldas, M, *B._args(), N, D,
+    _call(device, fn, a, a_type, lda, a_scales, ldas, M, *B._args(), N, D,
           None if bias is None else bias.data_ptr(), C.data_ptr(), _TYPES[dtype], ldc,
           None if ws is None else ws.data_ptr(), need)
     return C
+
+
+def mx_quantize(X: torch.Tensor, out: MXRows | None = None) -> MXRows:
+    """The rows of X (float32, bfloat16 or float16) in 4 bits."""
+    return _quantize(MXRows, _lib.gmm_mx_quantize, X, out)
+
+
+def mx_dequantize(rows: MXRows, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that 4-bit rows stand for, rounded once to dtype (exact in
+    float32 and bfloat16)."""
+    return _dequantize(MXRows, _lib.gmm_mx_dequantize, rows, dtype, out)
+
+
+def mx_product(A, B: MXRows, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """A B^T + bias as a (rows of A) x (rows of B) matrix of dtype.  A: MXRows,
+    or a tensor of rows that is quantised on the way (the same results)."""
+    return _product(MXRows, TYPE_MX, _lib.gmm_mx_product_workspace, _lib.gmm_mx_product, A, B, bias, dtype, out)
+
+
+def byte_quantize(X: torch.Tensor, out: ByteRows | None = None) -> ByteRows:
+    """The rows of X (float32, bfloat16 or float16) in 8 bits."""
+    return _quantize(ByteRows, _lib.gmm_byte_quantize, X, out)
+
+
+def byte_dequantize(rows: ByteRows, dtype: torch.dtype = torch.float32,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that 8-bit rows stand for, rounded once to dtype (exact in
+    float32, and in bfloat16 from 2^-130 on)."""
+    return _dequantize(ByteRows, _lib.gmm_byte_dequantize, rows, dtype, out)
+
+
+def byte_product(A, B: ByteRows, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """A B^T + bias as a (rows of A) x (rows of B) matrix of dtype.  A: ByteRows,
+    or a tensor of rows that is quantised on the way (the same results)."""
+    return _product(ByteRows, TYPE_BYTE, _lib.gmm_byte_product_workspace, _lib.gmm_byte_product, A, B, bias, dtype,
+                    out)
 
 
 def _setting(value, dtype, N, device, name):
@@ -320,4 +382,5 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     return ids
 
 
-__all__ = ["MXRows", "mx_quantize", "mx_dequantize", "mx_product", "draw", "ROW_EXPORTS"]
+__all__ = ["MXRows", "mx_quantize", "mx_dequantize", "mx_product", "ByteRows", "byte_quantize", "byte_dequantize",
+           "byte_product", "draw", "ROW_EXPORTS"]

@@ -72,7 +72,20 @@ void without_device() {
             gmm_mx_product_workspace(0, 1, 1, 0) == 0 && gmm_mx_product_workspace(0, 1, 1, kWidth + 1) == 0,
         "product_workspace sizes");
 
+  for (int32_t t : {0, 1, 2, 4})
+    for (int64_t m : {(int64_t)0, (int64_t)1, (int64_t)16, (int64_t)65, kRows})
+      for (int32_t d : {1, 128, 129, kWidth}) {
+        const size_t need = gmm_byte_product_workspace(t, m, kRows, d);
+        check(need <= (size_t)m * 132 * (size_t)groups(d) && (t != GMM_TYPE_BYTE || need == 0), "byte_product_workspace");
+      }
+  for (int32_t t : {-1, 3, 5, INT32_MIN, INT32_MAX})
+    check(gmm_byte_product_workspace(t, 1, 1, 1) == 0, "byte_product_workspace type");
+
   std::printf("stage: empty calls\n");
+  expect(gmm_byte_quantize(nullptr, 0, 0, 8, 8, nullptr, 128, nullptr, 4, nullptr), GMM_OK, "byte_quantize N=0");
+  expect(gmm_byte_dequantize(nullptr, 128, nullptr, 4, 0, 8, nullptr, 0, 8, nullptr), GMM_OK, "byte_dequantize N=0");
+  expect(gmm_byte_product(nullptr, 0, 8, nullptr, 0, 0, nullptr, 128, nullptr, 4, 0, 8, nullptr, nullptr, 0, 0, nullptr, 0,
+                          nullptr), GMM_OK, "byte_product M=N=0");
   expect(gmm_mx_quantize(nullptr, 0, 0, 8, 8, nullptr, 64, nullptr, 4, nullptr), GMM_OK, "quantize N=0");
   expect(gmm_mx_dequantize(nullptr, 64, nullptr, 4, 0, 8, nullptr, 0, 8, nullptr), GMM_OK, "dequantize N=0");
   expect(gmm_mx_product(nullptr, 0, 8, nullptr, 0, 0, nullptr, 64, nullptr, 4, 0, 8, nullptr, nullptr, 0, 0, nullptr, 0,
@@ -104,6 +117,13 @@ void without_device() {
          "product ldc");
   expect(gmm_mx_product(f, 0, 8, nullptr, 0, 100, mem, 64, mem, 4, 1, 8, nullptr, f, 0, 1, nullptr, 0, nullptr),
          GMM_ERR_CAPACITY, "product workspace");
+  expect(gmm_byte_quantize(f, 0, 1, 8, 8, mem, 64, mem, 4, nullptr), bad, "byte_quantize ld_codes");
+  expect(gmm_byte_quantize(f, 0, 1, 8, INT64_MAX, mem, 128, mem, 4, nullptr), bad, "byte_quantize ldx large");
+  expect(gmm_byte_dequantize(mem, 128, mem + 1, 4, 1, 8, f, 0, 8, nullptr), bad, "byte_dequantize scales");
+  expect(gmm_byte_product(f, 3, 128, mem, 4, 1, mem, 128, mem, 4, 1, 8, nullptr, f, 0, 1, nullptr, 0, nullptr), bad,
+         "byte_product a_type");
+  expect(gmm_byte_product(f, 0, 8, nullptr, 0, 100, mem, 128, mem, 4, 1, 8, nullptr, f, 0, 1, nullptr, 0, nullptr),
+         GMM_ERR_CAPACITY, "byte_product workspace");
   expect(gmm_draw(f, 0, 1, 0, 1, f, nullptr, 1.f, nullptr, 0, nullptr, 1.f, nullptr, 0.f, ids, nullptr, 0, nullptr), bad,
          "draw V");
   expect(gmm_draw(f, 0, 1, 4, 4, nullptr, nullptr, 1.f, nullptr, 0, nullptr, 1.f, nullptr, 0.f, ids, nullptr, 0, nullptr),
@@ -152,6 +172,36 @@ void with_device() {
       hip_ok(hipFree(ws), "free");
     }
     expect(gmm_mx_dequantize(codes, 64 * G, scales, 4 * G, M + N, (int32_t)D, X, 0, D, nullptr), GMM_OK, "dequantize");
+    hip_ok(hipDeviceSynchronize(), "synchronize");
+    for (void* p : {(void*)X, (void*)codes, (void*)scales, (void*)C, (void*)C2}) hip_ok(hipFree(p), "free");
+  }
+
+  std::printf("stage: rows in 8 bits and their products\n");
+  for (int64_t D : {1, 100, 700, 4096}) {
+    const int64_t G = groups(D), S = (G + 3) / 4 * 4, M = 300, N = 500;
+    std::vector<float> x((size_t)(M + N) * D);
+    for (auto& v : x) v = uniform() - 0.5f;
+    float* X = dev<float>(x.size());
+    hip_ok(hipMemcpy(X, x.data(), x.size() * 4, hipMemcpyHostToDevice), "copy");
+    uint8_t *codes = dev<uint8_t>((size_t)(M + N) * 128 * G), *scales = dev<uint8_t>((size_t)(M + N) * S);
+    float *C = dev<float>((size_t)M * N), *C2 = dev<float>((size_t)M * N);
+    expect(gmm_byte_quantize(X, 0, M + N, (int32_t)D, D, codes, 128 * G, scales, S, nullptr), GMM_OK, "byte_quantize");
+    const uint8_t *b = codes + M * 128 * G, *bs = scales + M * S;
+    for (int64_t m : {(int64_t)1, (int64_t)16, (int64_t)20, (int64_t)64, (int64_t)65, M}) {
+      const size_t need = gmm_byte_product_workspace(0, m, N, (int32_t)D);
+      uint8_t* ws = dev<uint8_t>(need + 1);
+      expect(gmm_byte_product(codes, 4, 128 * G, scales, S, m, b, 128 * G, bs, S, N, (int32_t)D, nullptr, C, 0, N,
+                              nullptr, 0, nullptr), GMM_OK, "product of 8-bit codes");
+      expect(gmm_byte_product(X, 0, D, nullptr, 0, m, b, 128 * G, bs, S, N, (int32_t)D, nullptr, C2, 0, N, ws, need,
+                              nullptr), GMM_OK, "product of floats with 8-bit codes");
+      std::vector<float> c((size_t)m * N), c2((size_t)m * N);
+      hip_ok(hipMemcpy(c.data(), C, c.size() * 4, hipMemcpyDeviceToHost), "copy");
+      hip_ok(hipMemcpy(c2.data(), C2, c2.size() * 4, hipMemcpyDeviceToHost), "copy");
+      check(std::memcmp(c.data(), c2.data(), c.size() * 4) == 0, "rows quantised on the way give other products");
+      hip_ok(hipFree(ws), "free");
+    }
+    expect(gmm_byte_dequantize(codes, 128 * G, scales, S, M + N, (int32_t)D, X, 0, D, nullptr), GMM_OK,
+           "byte_dequantize");
     hip_ok(hipDeviceSynchronize(), "synchronize");
     for (void* p : {(void*)X, (void*)codes, (void*)scales, (void*)C, (void*)C2}) hip_ok(hipFree(p), "free");
   }
