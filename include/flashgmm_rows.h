@@ -1,13 +1,16 @@
 /*
  * flashgmm_rows.h - C ABI of the row operators for AMD Instinct MI355X
- * (gfx950): rows held in 4 or 8 bits, their products, and draws from rows of
- * logits.
+ * (gfx950): rows held in 4 or 8 bits, their products, draws from rows of
+ * logits, and losses over such rows with their gradients.
  *
  * They serve what the mixture library (flashgmm.h) leaves a user with: many
  * stored vectors (base rows, component means) that are scored against other
  * rows, and rows of logits from which a component is picked.  gmm_soft_assign
  * picks the likeliest component and further ones above a threshold; gmm_draw
- * picks one at random by its responsibility.
+ * picks one at random by its responsibility.  The losses train a model of the
+ * components (one that gives a point's logits without the mixture's E-step):
+ * gmm_distill on the largest of the mixture's log-densities, gmm_balance on how
+ * evenly the components are taken.
  *
  * Conventions: as in flashgmm.h, and
  *   - no context: every call works on the current device, on the given HIP
@@ -155,6 +158,70 @@ gmm_status gmm_draw(const void *logits, int32_t type, int64_t N, int32_t V, int6
                     const float *temperatures, float temperature, const int32_t *top_ks, int32_t top_k,
                     const float *top_ps, float top_p, const float *min_ps, float min_p,
                     int32_t *ids, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Distillation from a teacher's top logits.  Row n of the logits (N x V, row
+ * stride ld elements) is the model's, ids[n, 0 .. k) the components that the
+ * teacher lists for it and teacher[n, 0 .. k) their logits (ids of id_bits 32 or
+ * 64, row stride ld_ids elements; teacher of any row type, row stride
+ * ld_teacher).  With T the temperature,
+ *   q = softmax(logits[n] / T) over all V, p = softmax(teacher[n] / T) over the
+ *   listed places: those with an id >= 0 and a teacher's logit above -inf,
+ *   losses[n] = T^2 sum_j p_j (log p_j - log q_ids[n, j]),
+ *   gradient  = w_n T (q_v - sum of the p_j with ids[n, j] = v),
+ * w_n the weight of the row's loss.  An id may be listed several times.  A row
+ * that lists nothing has loss 0 and gradient 0, whatever its logits.  A row with
+ * an id of V or more, a listed logit that is NaN or +inf, a NaN or +inf among
+ * its own logits, or nothing above -inf there has loss and gradient NaN; a
+ * listed component whose own logit is -inf gives loss +inf (and the gradient
+ * above) where its p_j is not 0 in float32.
+ * gmm_distill writes losses (float[N]); stats (float[2 N], may be NULL) for
+ * gmm_distill_backward; and the gradient in the type of the logits (row stride
+ * ld_grad), rounded once, where grad is not NULL, with the row weights given
+ * (weights, float[N], or weight for all where that is NULL).
+ * gmm_distill_backward writes the gradient from the stats of a call on the same
+ * inputs; weights[n * ld_weights] (ld_weights >= 0) is the weight of row n.
+ * grad must overlap nothing else.  2^-60 <= temperature <= 2^60, 1 <= V <= 2^20,
+ * N <= 2^30, 1 <= k <= 1024.  workspace: gmm_distill_workspace bytes, as
+ * gmm_mx_product; the backward needs none. */
+size_t gmm_distill_workspace(int64_t N, int32_t V, int32_t k);
+gmm_status gmm_distill(const void *logits, int32_t type, int64_t N, int32_t V, int64_t ld, const void *ids,
+                       int32_t id_bits, int64_t ld_ids, const void *teacher, int32_t teacher_type,
+                       int64_t ld_teacher, int32_t k, float temperature, float *losses, float *stats,
+                       const float *weights, float weight, void *grad, int64_t ld_grad,
+                       void *workspace, size_t workspace_bytes, void *hip_stream);
+gmm_status gmm_distill_backward(const void *logits, int32_t type, int64_t N, int32_t V, int64_t ld, const void *ids,
+                                int32_t id_bits, int64_t ld_ids, const void *teacher, int32_t teacher_type,
+                                int64_t ld_teacher, int32_t k, float temperature, const float *stats,
+                                const float *weights, int64_t ld_weights, void *grad, int64_t ld_grad,
+                                void *hip_stream);
+
+/* Balance of components and their counts.  ids[n, 0 .. k) are the components
+ * that row n takes (as gmm_draw gives them, or a top-k; negative: none).  With
+ * c_e the number of ids that are e, C their sum, R the rows with an id >= 0 and
+ * p_n = softmax(logits[n]),
+ *   counts[e] = c_e,
+ *   loss     = K / (C R) sum over those rows of d_n, d_n = sum_e c_e p_ne
+ *            = K sum_e (c_e / C) (mean of p_ne), 1 where all is even,
+ *   gradient = w K / (C R) p_ne (c_e - d_n), 0 for the other rows.
+ * The counts are constants of the gradient.  Without any id the loss is 0.  An
+ * id of K or more makes the loss and the whole gradient NaN (it is in no
+ * count); a row that is counted and holds a NaN or +inf, or nothing above -inf,
+ * makes the loss and its own gradient NaN.
+ * gmm_balance writes counts (int64[K]), loss (float[1]), stats
+ * (gmm_balance_stats floats, for gmm_balance_backward) and, where grad is not
+ * NULL, the gradient for weight w, in the type of the logits and rounded once.
+ * gmm_balance_backward writes the gradient from those stats, w = *weight (on
+ * the device).  Nothing may overlap grad.  1 <= K <= 2^20, N <= 2^30,
+ * 1 <= k <= 1024.  With N = 0 counts and loss are written, as zeros. */
+size_t gmm_balance_stats(int64_t N, int32_t K);
+size_t gmm_balance_workspace(int64_t N, int32_t K, int32_t k);
+gmm_status gmm_balance(const void *logits, int32_t type, int64_t N, int32_t K, int64_t ld, const void *ids,
+                       int32_t id_bits, int64_t ld_ids, int32_t k, int64_t *counts, float *loss, float *stats,
+                       float weight, void *grad, int64_t ld_grad,
+                       void *workspace, size_t workspace_bytes, void *hip_stream);
+gmm_status gmm_balance_backward(const void *logits, int32_t type, int64_t N, int32_t K, int64_t ld,
+                                const float *stats, const float *weight, void *grad, int64_t ld_grad,
+                                void *hip_stream);
 
 #ifdef __cplusplus
 }

@@ -20,11 +20,11 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libflashgmm.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["gmm_kernels.hip", "gmm_assign.hip", "gmm_lists.hip", "gmm_api.hip", "gmm_mx.hip", "gmm_byte.hip",
-           "gmm_draw.hip", "gmm_rows_api.hip"]
+           "gmm_draw.hip", "gmm_losses.hip", "gmm_rows_api.hip"]
 # Kernels with inline assembly that have to keep their values in registers:
 # variants that spilled vector registers gave wrong results, so a spill there
 # ends the build.
-NO_SPILL = ["gmm_mx.hip", "gmm_byte.hip", "gmm_draw.hip"]
+NO_SPILL = ["gmm_mx.hip", "gmm_byte.hip", "gmm_draw.hip", "gmm_losses.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

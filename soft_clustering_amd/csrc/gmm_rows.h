@@ -76,4 +76,51 @@ struct DrawArgs {
 size_t draw_workspace(int64_t N, int V);
 hipError_t launch_draw(const DrawArgs& a, void* workspace, hipStream_t s);
 
+struct DistillArgs {
+  const void* z;
+  int type;
+  int64_t N;
+  int V;
+  int64_t ld;
+  const void* ids;
+  bool wide;  // ids of 64 bits
+  int64_t ld_ids;
+  const void* teacher;
+  int teacher_type;
+  int64_t ld_teacher;
+  int k;
+  float temperature;
+  float* losses;         // NULL: stats are read and the gradient is written
+  float* stats;          // [N][2]
+  const float* weights;  // of the rows' losses, ld_weights apart; NULL: weight
+  int64_t ld_weights;
+  float weight;
+  void* grad;
+  int64_t ld_grad;
+};
+size_t distill_workspace(int64_t N, int V, int k);
+hipError_t launch_distill(const DistillArgs& a, void* workspace, hipStream_t s);
+
+struct BalanceArgs {
+  const void* z;
+  int type;
+  int64_t N;
+  int K;
+  int64_t ld;
+  const void* ids;
+  bool wide;
+  int64_t ld_ids;
+  int k;
+  int64_t* counts;
+  float* loss;  // NULL: stats are read and the gradient is written
+  float* stats;
+  const float* weight_at;  // of the loss; NULL: weight
+  float weight;
+  void* grad;
+  int64_t ld_grad;
+};
+size_t balance_stats(int64_t N, int K);
+size_t balance_workspace(int64_t N, int K, int k);
+hipError_t launch_balance(const BalanceArgs& a, void* workspace, hipStream_t s);
+
 }  // namespace gmm

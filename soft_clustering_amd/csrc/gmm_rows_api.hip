@@ -1,5 +1,5 @@
 // C ABI of the row operators (declared in include/flashgmm_rows.h): argument
-// checks, then one launcher of gmm_mx.hip, gmm_byte.hip or gmm_draw.hip.  Nothing here
+// checks, then one launcher of gmm_mx.hip, gmm_byte.hip, gmm_draw.hip or gmm_losses.hip.  Nothing here
 // allocates, synchronises or keeps state.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -112,6 +112,30 @@ gmm_status check_result(int64_t M, int64_t N, const float* bias, const void* C, 
     return refuse(GMM_ERR_INVALID_ARG, "C: row stride %lld for rows of %lld", (long long)ldc, (long long)N);
   if (bias && !aligned(bias, 4)) return refuse(GMM_ERR_INVALID_ARG, "bias is not aligned to its elements");
   return GMM_OK;
+}
+
+// lists of ids: k of 32 or 64 bits for each row
+gmm_status check_ids(const void* ids, int32_t bits, int64_t N, int32_t k, int64_t ld) {
+  if (bits != 32 && bits != 64) return refuse(GMM_ERR_INVALID_ARG, "id_bits must be 32 or 64 (got %d)", bits);
+  if (k < 1 || k > 1024) return refuse(GMM_ERR_INVALID_ARG, "k must be in [1, 1024] (got %d)", k);
+  if (N == 0) return GMM_OK;
+  if (!ids) return refuse(GMM_ERR_INVALID_ARG, "ids is NULL");
+  if (!aligned(ids, (unsigned)bits / 8)) return refuse(GMM_ERR_INVALID_ARG, "ids is not aligned to its elements");
+  if (ld < k || ld > ((int64_t)1 << 40))
+    return refuse(GMM_ERR_INVALID_ARG, "ids: row stride %lld for rows of %d", (long long)ld, k);
+  return GMM_OK;
+}
+
+gmm_status check_distill(const void* logits, int32_t type, int64_t N, int32_t V, int64_t ld, const void* ids,
+                         int32_t id_bits, int64_t ld_ids, const void* teacher, int32_t teacher_type,
+                         int64_t ld_teacher, int32_t k, float temperature) {
+  gmm_status st = check_sizes(N, V, "N", "V");
+  if (!st) st = check_rows(logits, type, N, V, ld, "logits");
+  if (!st) st = check_ids(ids, id_bits, N, k, ld_ids);
+  if (!st) st = check_rows(teacher, teacher_type, N, k, ld_teacher, "teacher");
+  if (!st && !(temperature >= 0x1p-60f && temperature <= 0x1p60f))
+    st = refuse(GMM_ERR_INVALID_ARG, "temperature must be in [2^-60, 2^60] (got %g)", (double)temperature);
+  return st;
 }
 
 }  // namespace
@@ -240,6 +264,93 @@ gmm_status gmm_draw(const void* logits, int32_t type, int64_t N, int32_t V, int6
   gmm::DrawArgs a{logits, type, N, V, ld, u, temperatures, top_ks, top_ps, min_ps, temperature, top_k, top_p, min_p,
                   ids};
   return launched(gmm::launch_draw(a, workspace, (hipStream_t)hip_stream), "draw launch");
+}
+
+size_t gmm_distill_workspace(int64_t N, int32_t V, int32_t k) {
+  if (N < 0 || N > kMaxRows || V < 1 || V > kMaxWidth || k < 1 || k > 1024) return 0;
+  return gmm::distill_workspace(N, V, k);
+}
+
+gmm_status gmm_distill(const void* logits, int32_t type, int64_t N, int32_t V, int64_t ld, const void* ids,
+                       int32_t id_bits, int64_t ld_ids, const void* teacher, int32_t teacher_type, int64_t ld_teacher,
+                       int32_t k, float temperature, float* losses, float* stats, const float* weights, float weight,
+                       void* grad, int64_t ld_grad, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  gmm_status st = check_distill(logits, type, N, V, ld, ids, id_bits, ld_ids, teacher, teacher_type, ld_teacher, k,
+                                temperature);
+  if (!st && grad) st = check_rows(grad, type, N, V, ld_grad, "grad");
+  if (st || N == 0) return st;
+  if (!losses) return refuse(GMM_ERR_INVALID_ARG, "losses is NULL");
+  if (!aligned(losses, 4) || !aligned(stats, 4) || !aligned(weights, 4))
+    return refuse(GMM_ERR_INVALID_ARG, "losses, stats and weights must be 4-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, gmm::distill_workspace(N, V, k)))) return st;
+  if ((st = check_device())) return st;
+  gmm::DistillArgs a{logits, type, N, V, ld, ids, id_bits == 64, ld_ids, teacher, teacher_type, ld_teacher, k,
+                     temperature, losses, stats, weights, 1, weight, grad, ld_grad};
+  return launched(gmm::launch_distill(a, workspace, (hipStream_t)hip_stream), "distillation launch");
+}
+
+gmm_status gmm_distill_backward(const void* logits, int32_t type, int64_t N, int32_t V, int64_t ld, const void* ids,
+                                int32_t id_bits, int64_t ld_ids, const void* teacher, int32_t teacher_type,
+                                int64_t ld_teacher, int32_t k, float temperature, const float* stats,
+                                const float* weights, int64_t ld_weights, void* grad, int64_t ld_grad,
+                                void* hip_stream) {
+  gmm_status st = check_distill(logits, type, N, V, ld, ids, id_bits, ld_ids, teacher, teacher_type, ld_teacher, k,
+                                temperature);
+  if (!st) st = check_rows(grad, type, N, V, ld_grad, "grad");
+  if (st || N == 0) return st;
+  if (!stats || !weights) return refuse(GMM_ERR_INVALID_ARG, "stats and weights must be non-NULL");
+  if (!aligned(stats, 4) || !aligned(weights, 4))
+    return refuse(GMM_ERR_INVALID_ARG, "stats and weights must be 4-byte aligned");
+  if (ld_weights < 0 || ld_weights > ((int64_t)1 << 40))
+    return refuse(GMM_ERR_INVALID_ARG, "weights: stride %lld", (long long)ld_weights);
+  if ((st = check_device())) return st;
+  gmm::DistillArgs a{logits, type, N, V, ld, ids, id_bits == 64, ld_ids, teacher, teacher_type, ld_teacher, k,
+                     temperature, nullptr, const_cast<float*>(stats), weights, ld_weights, 0.f, grad, ld_grad};
+  return launched(gmm::launch_distill(a, nullptr, (hipStream_t)hip_stream), "distillation gradient launch");
+}
+
+size_t gmm_balance_stats(int64_t N, int32_t K) {
+  if (N < 0 || N > kMaxRows || K < 1 || K > kMaxWidth) return 0;
+  return gmm::balance_stats(N, K);
+}
+
+size_t gmm_balance_workspace(int64_t N, int32_t K, int32_t k) {
+  if (N < 0 || N > kMaxRows || K < 1 || K > kMaxWidth || k < 1 || k > 1024) return 0;
+  return gmm::balance_workspace(N, K, k);
+}
+
+gmm_status gmm_balance(const void* logits, int32_t type, int64_t N, int32_t K, int64_t ld, const void* ids,
+                       int32_t id_bits, int64_t ld_ids, int32_t k, int64_t* counts, float* loss, float* stats,
+                       float weight, void* grad, int64_t ld_grad, void* workspace, size_t workspace_bytes,
+                       void* hip_stream) {
+  gmm_status st = check_sizes(N, K, "N", "K");
+  if (!st) st = check_rows(logits, type, N, K, ld, "logits");
+  if (!st) st = check_ids(ids, id_bits, N, k, ld_ids);
+  if (!st && grad) st = check_rows(grad, type, N, K, ld_grad, "grad");
+  if (st) return st;
+  if (!counts || !loss || !stats) return refuse(GMM_ERR_INVALID_ARG, "counts, loss and stats must be non-NULL");
+  if (!aligned(counts, 8) || !aligned(loss, 4) || !aligned(stats, 4))
+    return refuse(GMM_ERR_INVALID_ARG, "counts must be 8-byte, loss and stats 4-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, gmm::balance_workspace(N, K, k)))) return st;
+  if ((st = check_device())) return st;
+  gmm::BalanceArgs a{logits, type, N, K, ld, ids, id_bits == 64, ld_ids, k, counts, loss, stats, nullptr, weight,
+                     grad, ld_grad};
+  return launched(gmm::launch_balance(a, workspace, (hipStream_t)hip_stream), "balance launch");
+}
+
+gmm_status gmm_balance_backward(const void* logits, int32_t type, int64_t N, int32_t K, int64_t ld, const float* stats,
+                                const float* weight, void* grad, int64_t ld_grad, void* hip_stream) {
+  gmm_status st = check_sizes(N, K, "N", "K");
+  if (!st) st = check_rows(logits, type, N, K, ld, "logits");
+  if (!st) st = check_rows(grad, type, N, K, ld_grad, "grad");
+  if (st || N == 0) return st;
+  if (!stats || !weight) return refuse(GMM_ERR_INVALID_ARG, "stats and weight must be non-NULL");
+  if (!aligned(stats, 4) || !aligned(weight, 4))
+    return refuse(GMM_ERR_INVALID_ARG, "stats and weight must be 4-byte aligned");
+  if ((st = check_device())) return st;
+  gmm::BalanceArgs a{logits, type, N, K, ld, nullptr, false, 0, 0, nullptr, nullptr, const_cast<float*>(stats), weight,
+                     0.f, grad, ld_grad};
+  return launched(gmm::launch_balance(a, nullptr, (hipStream_t)hip_stream), "balance gradient launch");
 }
 
 }  // extern "C"

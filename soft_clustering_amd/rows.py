@@ -1,11 +1,13 @@
 """Row operators of libflashgmm.so (C ABI in include/flashgmm_rows.h): rows
-held in 4 or 8 bits, their products, and draws from rows of logits.
+held in 4 or 8 bits, their products, draws from rows of logits, and losses over
+them with their gradients.
 
 Argument marshalling only, as in the binding of the mixture calls: tensors are
 checked for dtype, device, layout and shape, then the HIP kernels run on the
 current stream of the tensors' device.  Outputs come from torch's allocator;
-the calls synchronise nothing and can be captured into a graph.  None has a
-backward: rows, products and results that require gradients are refused while
+the calls synchronise nothing and can be captured into a graph.  distill and
+balance are differentiable in the logits.  Nothing else has a backward: rows,
+products, results and teachers that require gradients are refused while
 gradients are on (a draw's ids are whole numbers and never have one).  A result
 that is given (out) must not share memory with an input.
 """
@@ -21,7 +23,9 @@ TYPE_FLOAT, TYPE_BFLOAT, TYPE_HALF, TYPE_MX, TYPE_BYTE = 0, 1, 2, 3, 4
 _TYPES = {torch.float32: TYPE_FLOAT, torch.bfloat16: TYPE_BFLOAT, torch.float16: TYPE_HALF}
 ROW_EXPORTS = ["gmm_mx_quantize", "gmm_mx_dequantize", "gmm_mx_product_workspace", "gmm_mx_product",
                "gmm_byte_quantize", "gmm_byte_dequantize", "gmm_byte_product_workspace", "gmm_byte_product",
-               "gmm_draw_workspace", "gmm_draw"]
+               "gmm_draw_workspace", "gmm_draw",
+               "gmm_distill_workspace", "gmm_distill", "gmm_distill_backward",
+               "gmm_balance_stats", "gmm_balance_workspace", "gmm_balance", "gmm_balance_backward"]
 
 _lib = raw_library()
 
@@ -36,6 +40,17 @@ def _declare():
         "gmm_draw_workspace": (sz, [i64, i32]),
         "gmm_draw": (i32, [vp, i32, i64, i32, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, sz, vp]),
     }
+    distill = [vp, i32, i64, i32, i64, vp, i32, i64, vp, i32, i64, i32, f32]
+    balance = [vp, i32, i64, i32, i64]
+    sig.update({
+        "gmm_distill_workspace": (sz, [i64, i32, i32]),
+        "gmm_distill": (i32, [*distill, vp, vp, vp, f32, vp, i64, vp, sz, vp]),
+        "gmm_distill_backward": (i32, [*distill, vp, vp, i64, vp, i64, vp]),
+        "gmm_balance_stats": (sz, [i64, i32]),
+        "gmm_balance_workspace": (sz, [i64, i32, i32]),
+        "gmm_balance": (i32, [*balance, vp, i32, i64, i32, vp, vp, vp, f32, vp, i64, vp, sz, vp]),
+        "gmm_balance_backward": (i32, [*balance, vp, vp, vp, i64, vp]),
+    })
     for name in ("quantize", "dequantize", "product_workspace", "product"):
         sig["gmm_byte_" + name] = sig["gmm_mx_" + name]
     for name, (res, args) in sig.items():
@@ -382,5 +397,158 @@ def draw(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=
     return ids
 
 
+def _id_lists(ids, N, device, flat=False):
+    """(pointer, bits, row stride, k) of lists of component ids, N x k (flat: or N)."""
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be an int32 or int64 tensor")
+    if flat and ids.dim() == 1:
+        ids = ids[:, None]
+    if ids.dim() != 2 or ids.shape[0] != N or ids.device != device:
+        raise ValueError(f"ids must have {N} rows on {device}, got {tuple(ids.shape)} on {ids.device}")
+    k = ids.shape[1]
+    if not 1 <= k <= 1024:
+        raise ValueError(f"ids must list between 1 and 1024 components a row, got {k}")
+    ld, one = ids.stride()
+    if one != 1 and k > 1:
+        raise ValueError("ids: rows must be contiguous (stride(1) == 1)")
+    if ld < k:
+        if N > 1:
+            raise ValueError(f"ids: rows must not overlap (stride(0) >= {k})")
+        ld = k
+    return ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, ld, k
+
+
+def _distill_args(logits, ids, teacher, temperature):
+    code, N, V, ld = _rows(logits, "logits")
+    device = logits.device
+    ids_ptr, bits, ld_ids, k = _id_lists(ids, N, device)
+    t_code, t_rows, t_k, ld_teacher = _rows(teacher, "teacher")
+    if (t_rows, t_k) != (N, k) or teacher.device != device:
+        raise ValueError(f"teacher must be {N} x {k} on {device}, got {t_rows} x {t_k} on {teacher.device}")
+    _no_gradient(teacher, "teacher")
+    return (logits.data_ptr(), code, N, V, ld, ids_ptr, bits, ld_ids, teacher.data_ptr(), t_code, ld_teacher, k,
+            float(temperature))
+
+
+def _distill(args, device, stats, weights=None, weight=0.0, grad=None, ld_grad=0):
+    N, V, k = args[2], args[3], args[11]
+    losses = torch.empty(N, dtype=torch.float32, device=device)
+    need = _lib.gmm_distill_workspace(N, V, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _call(device, _lib.gmm_distill, *args, losses.data_ptr(), None if stats is None else stats.data_ptr(), weights,
+          weight, None if grad is None else grad.data_ptr(), ld_grad, None if ws is None else ws.data_ptr(), need)
+    return losses
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, temperature):
+        args = _distill_args(logits, ids, teacher, temperature)
+        stats = torch.empty((args[2], 2), dtype=torch.float32, device=logits.device)
+        losses = _distill(args, logits.device, stats)
+        ctx.save_for_backward(logits, ids, teacher, stats)
+        ctx.temperature = temperature
+        return losses
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, weights):
+        logits, ids, teacher, stats = ctx.saved_tensors
+        args = _distill_args(logits, ids, teacher, ctx.temperature)
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _call(logits.device, _lib.gmm_distill_backward, *args, stats.data_ptr(), weights.data_ptr(),
+              weights.stride(0) if args[2] > 1 else 0, grad.data_ptr(), args[3])
+        return grad, None, None, None
+
+
+def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
+    """Distillation losses of rows of logits (N x V), float32, one for each row:
+    T^2 KL(p || q), p the softmax of the teacher's logits / T over the components
+    ids[n] that it lists (N x k, int32 or int64; negative: none), q the softmax
+    of the row / T over all V.  Differentiable in the logits.  A row that lists
+    nothing has loss and gradient 0; an id of V or more, or logits without a
+    distribution, make a row's loss and gradient NaN."""
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        return _Distill.apply(logits, ids, teacher, temperature)
+    return _distill(_distill_args(logits, ids, teacher, temperature), logits.device, None)
+
+
+def distill_grad(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, weights=1.0, temperature: float = 1.0,
+                 out: torch.Tensor | None = None):
+    """(losses, gradient): the losses of distill and the gradient of
+    sum(weights * losses) in the logits (in their type), in one pass over them.
+    weights: one number or a float32 tensor with one for each row.  For programs
+    that know a row's weight before its loss (a mean: 1 / N) and pass the
+    gradient on themselves (``outputs.backward(gradient)``)."""
+    args = _distill_args(logits, ids, teacher, temperature)
+    _no_gradient(logits, "logits")
+    device = logits.device
+    w_ptr, w = _setting(weights, torch.float32, args[2], device, "weights")
+    grad, ld_grad = _matrix(out, args[2], args[3], logits.dtype, device)
+    if out is not None:
+        _apart(out, logits, ids, teacher, weights)
+    return _distill(args, device, None, w_ptr, float(w), grad, ld_grad), grad
+
+
+def _balance(logits, ids, weight=0.0, grad=None, ld_grad=0):
+    code, N, K, ld = _rows(logits, "logits")
+    device = logits.device
+    ids_ptr, bits, ld_ids, k = _id_lists(ids, N, device, flat=True)
+    counts = torch.empty(K, dtype=torch.int64, device=device)
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    stats = torch.empty(_lib.gmm_balance_stats(N, K), dtype=torch.float32, device=device)
+    need = _lib.gmm_balance_workspace(N, K, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(device, _lib.gmm_balance, logits.data_ptr(), code, N, K, ld, ids_ptr, bits, ld_ids, k, counts.data_ptr(),
+          loss.data_ptr(), stats.data_ptr(), weight, None if grad is None else grad.data_ptr(), ld_grad,
+          ws.data_ptr(), need)
+    return loss, counts, stats
+
+
+class _Balance(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids):
+        loss, counts, stats = _balance(logits, ids)
+        ctx.save_for_backward(logits, stats)
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, weight, _):
+        logits, stats = ctx.saved_tensors
+        code, N, K, ld = _rows(logits, "logits")
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _call(logits.device, _lib.gmm_balance_backward, logits.data_ptr(), code, N, K, ld, stats.data_ptr(),
+              weight.data_ptr(), grad.data_ptr(), K)
+        return grad, None
+
+
+def balance(logits: torch.Tensor, ids: torch.Tensor):
+    """(loss, counts): how evenly components are taken.  ids (N or N x k, int32 or
+    int64) are the components that each row of logits (N x K) takes, as draw or a
+    top-k gives them, negative ones none; counts (int64, K) how often each is.
+    The loss is K sum_e (share of e in the counts) (mean softmax of e over the
+    rows that take one), 1 where all is even.  Differentiable in the logits (the
+    counts are constants).  An id of K or more makes loss and gradient NaN."""
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        return _Balance.apply(logits, ids)
+    return _balance(logits, ids)[:2]
+
+
+def balance_grad(logits: torch.Tensor, ids: torch.Tensor, weight: float = 1.0, out: torch.Tensor | None = None):
+    """(loss, counts, gradient): loss and counts of balance and the gradient of
+    weight * loss in the logits (in their type), in one pass over them."""
+    _, N, K, _ = _rows(logits, "logits")
+    _no_gradient(logits, "logits")
+    grad, ld_grad = _matrix(out, N, K, logits.dtype, logits.device)
+    if out is not None:
+        _apart(out, logits)
+        if isinstance(ids, torch.Tensor):
+            _apart(out, ids if ids.dim() > 1 or ids.is_contiguous() else ids[:, None])
+    loss, counts, _ = _balance(logits, ids, float(weight), grad, ld_grad)
+    return loss, counts, grad
+
+
 __all__ = ["MXRows", "mx_quantize", "mx_dequantize", "mx_product", "ByteRows", "byte_quantize", "byte_dequantize",
-           "byte_product", "draw", "ROW_EXPORTS"]
+           "byte_product", "draw", "distill", "distill_grad", "balance", "balance_grad", "ROW_EXPORTS"]

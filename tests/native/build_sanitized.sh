@@ -31,7 +31,7 @@ stale() {
   return 1
 }
 objs=()
-for src in gmm_kernels gmm_assign gmm_lists gmm_api gmm_mx gmm_byte gmm_draw gmm_rows_api; do
+for src in gmm_kernels gmm_assign gmm_lists gmm_api gmm_mx gmm_byte gmm_draw gmm_losses gmm_rows_api; do
   if stale "$OUT/$src.o" "$CSRC/$src.hip"; then
     rm -f "$OUT/$src.o"
     "$HIPCC" "${COMMON[@]}" "${SAN[@]}" -c "$CSRC/$src.hip" -o "$OUT/$src.o" 2> "$OUT/$src.log" &

@@ -93,6 +93,21 @@ void without_device() {
   expect(gmm_draw(nullptr, 0, 0, kWidth, kWidth, nullptr, nullptr, 1.f, nullptr, 0, nullptr, 1.f, nullptr, 0.f, nullptr,
                   nullptr, 0, nullptr), GMM_OK, "draw N=0");
 
+  expect(gmm_distill(nullptr, 0, 0, 5, 5, nullptr, 32, 2, nullptr, 0, 2, 2, 1.f, nullptr, nullptr, nullptr, 0.f, nullptr, 0,
+                     nullptr, 0, nullptr), GMM_OK, "distill N=0");
+  expect(gmm_distill_backward(nullptr, 0, 0, 5, 5, nullptr, 32, 2, nullptr, 0, 2, 2, 1.f, nullptr, nullptr, 0, nullptr, 5,
+                              nullptr), GMM_OK, "distill_backward N=0");
+  expect(gmm_balance_backward(nullptr, 0, 0, 5, 5, nullptr, nullptr, nullptr, 5, nullptr), GMM_OK, "balance_backward N=0");
+  for (int64_t n : {(int64_t)0, (int64_t)1, (int64_t)129, kRows})
+    for (int32_t v : {1, 16384, 16385, kWidth})
+      for (int32_t k : {1, 1024}) {
+        check(gmm_balance_stats(n, v) >= 3 * (size_t)n + v && gmm_balance_workspace(n, v, k) > 0, "balance sizes");
+        (void)gmm_distill_workspace(n, v, k);
+      }
+  for (int64_t n : {(int64_t)-1, kRows + 1, INT64_MIN, INT64_MAX})
+    check(gmm_balance_stats(n, 5) == 0 && gmm_balance_workspace(n, 5, 1) == 0 && gmm_distill_workspace(n, 5, 1) == 0,
+          "loss sizes N");
+
   std::printf("stage: argument errors\n");
   alignas(16) static uint8_t mem[64];  // addresses only: every call below is refused
   float* const f = reinterpret_cast<float*>(mem);
@@ -134,6 +149,17 @@ void without_device() {
          "draw top_p");
   expect(gmm_draw(f, 0, 1, 20000, 20000, f, nullptr, 1.f, nullptr, 0, nullptr, 1.f, nullptr, 0.f, ids, nullptr, 0,
                   nullptr), GMM_ERR_CAPACITY, "draw workspace");
+  expect(gmm_distill(f, 0, 1, 4, 4, ids, 32, 2, f, 0, 2, 2, 0.f, f, nullptr, nullptr, 0.f, nullptr, 0, nullptr, 0, nullptr),
+         bad, "distill temperature");
+  expect(gmm_distill(f, 0, 1, 4, 4, ids, 32, INT64_MAX, f, 0, 2, 2, 1.f, f, nullptr, nullptr, 0.f, nullptr, 0, nullptr, 0,
+                     nullptr), bad, "distill ld_ids");
+  expect(gmm_distill_backward(f, 0, 1, 4, 4, ids, 32, 2, f, 0, 2, 2, 1.f, f, f, INT64_MIN, f, 4, nullptr), bad,
+         "distill_backward ld_weights");
+  expect(gmm_balance(f, 0, 1, 4, 4, ids, 32, 2, 2, nullptr, f, f, 0.f, nullptr, 0, mem, 64, nullptr), bad,
+         "balance counts");
+  expect(gmm_balance(f, 0, 1, 4, 4, ids, 32, 2, 2, (int64_t*)mem, f, f, 0.f, nullptr, 0, nullptr, 0, nullptr),
+         GMM_ERR_CAPACITY, "balance workspace");
+  expect(gmm_balance_backward(f, 0, 1, 4, 3, f, f, f, 4, nullptr), bad, "balance_backward ld");
   check(std::strlen(gmm_last_error(nullptr)) > 0, "last_error(NULL) empty after a refusal");
 }
 
@@ -231,6 +257,49 @@ void with_device() {
   }
 }
 
+void losses_with_device() {
+  std::printf("stage: losses\n");
+  for (int32_t V : {1, 700, 3000, 20000})
+    for (int64_t N : {(int64_t)1, (int64_t)9, (int64_t)300}) {
+      const int32_t k = V < 4 ? V : 4;
+      std::vector<float> z((size_t)N * V);
+      for (auto& v : z) v = 4.f * uniform();
+      std::vector<int32_t> ids((size_t)N * k);
+      for (size_t i = 0; i < ids.size(); ++i) ids[i] = (int32_t)((i * 7) % V);
+      float *Z = dev<float>(z.size()), *T = dev<float>(ids.size()), *losses = dev<float>(N), *stats = dev<float>(2 * N);
+      float *G = dev<float>(z.size()), *G2 = dev<float>(z.size()), *one = dev<float>(1), *loss = dev<float>(1);
+      float* kept = dev<float>(gmm_balance_stats(N, V));
+      int32_t* I = dev<int32_t>(ids.size());
+      int64_t* counts = dev<int64_t>(V);
+      const float w = 1.f;
+      hip_ok(hipMemcpy(Z, z.data(), z.size() * 4, hipMemcpyHostToDevice), "copy");
+      hip_ok(hipMemcpy(T, z.data(), ids.size() * 4, hipMemcpyHostToDevice), "copy");
+      hip_ok(hipMemcpy(I, ids.data(), ids.size() * 4, hipMemcpyHostToDevice), "copy");
+      hip_ok(hipMemcpy(one, &w, 4, hipMemcpyHostToDevice), "copy");
+      const size_t need = gmm_distill_workspace(N, V, k), room = gmm_balance_workspace(N, V, k);
+      uint8_t *ws = dev<uint8_t>(need + 1), *ws2 = dev<uint8_t>(room);
+      expect(gmm_distill(Z, 0, N, V, V, I, 32, k, T, 0, k, k, 1.f, losses, stats, nullptr, 1.f, G, V, ws, need, nullptr),
+             GMM_OK, "distill");
+      expect(gmm_distill(Z, 0, N, V, V, I, 32, k, T, 0, k, k, 1.f, losses, stats, nullptr, 1.f, nullptr, 0, ws, need,
+                         nullptr), GMM_OK, "distill without a gradient");
+      expect(gmm_distill_backward(Z, 0, N, V, V, I, 32, k, T, 0, k, k, 1.f, stats, one, 0, G2, V, nullptr), GMM_OK,
+             "distill_backward");
+      expect(gmm_balance(Z, 0, N, V, V, I, 32, k, k, counts, loss, kept, 1.f, G, V, ws2, room, nullptr), GMM_OK, "balance");
+      expect(gmm_balance(Z, 0, N, V, V, I, 32, k, k, counts, loss, kept, 1.f, nullptr, 0, ws2, room, nullptr), GMM_OK,
+             "balance without a gradient");
+      expect(gmm_balance_backward(Z, 0, N, V, V, kept, one, G2, V, nullptr), GMM_OK, "balance_backward");
+      hip_ok(hipDeviceSynchronize(), "synchronize");
+      std::vector<int64_t> c(V);
+      hip_ok(hipMemcpy(c.data(), counts, V * 8, hipMemcpyDeviceToHost), "copy");
+      int64_t sum = 0;
+      for (int64_t x : c) sum += x;
+      check(sum == N * k, "counts");
+      for (void* p : {(void*)Z, (void*)T, (void*)losses, (void*)stats, (void*)G, (void*)G2, (void*)one, (void*)loss,
+                      (void*)kept, (void*)I, (void*)counts, (void*)ws, (void*)ws2})
+        hip_ok(hipFree(p), "free");
+    }
+}
+
 }  // namespace
 
 int main() {
@@ -238,7 +307,10 @@ int main() {
   without_device();
   int devices = 0;
   const bool any = hipGetDeviceCount(&devices) == hipSuccess && devices > 0;
-  if (any) with_device();
+  if (any) {
+    with_device();
+    losses_with_device();
+  }
   std::printf("rows_exercise: %s\n", g_fail ? "FAILED" : any ? "ok" : "ok (no device)");
   std::fflush(nullptr);
   std::_Exit(g_fail);  // no exit handlers, as in abi_exercise
