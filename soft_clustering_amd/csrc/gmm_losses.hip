@@ -29,56 +29,69 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
+constexpr int kHeld = 16;  // elements of a lane where rows are held in registers
+
 template <int TYPE>
 constexpr int kVec = TYPE == kFloat ? 4 : 8;  // elements of one 16-byte load
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
 
-// Sum and maximum over the 64 lanes, in all of them.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ float wave_sum(float x) {
-  x += dpp<0xB1>(x);   // neighbours, pairs, quads and halves of a row of 16
-  x += dpp<0x4E>(x);
-  x += dpp<0x124>(x);
-  x += dpp<0x128>(x);
-  x += __shfl_xor(x, 16);
-  x += __shfl_xor(x, 32);
-  return x;
-}
-__device__ __forceinline__ float wave_max(float x) {
-  x = fmaxf(x, dpp<0xB1>(x));
-  x = fmaxf(x, dpp<0x4E>(x));
-  x = fmaxf(x, dpp<0x124>(x));
-  x = fmaxf(x, dpp<0x128>(x));
-  x = fmaxf(x, __shfl_xor(x, 16));
-  x = fmaxf(x, __shfl_xor(x, 32));
-  return x;
-}
-
 // What is known of a row (or a part of it): the largest logit, the sum of
 // exponentials, their c-weighted sum.
 struct Part {
   float m, s, d;
 };
-__device__ __forceinline__ Part joined(Part a, Part b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float fa = exp2_of((a.m - m) * c), fb = exp2_of((b.m - m) * c);
-  return Part{m, a.s * fa + b.s * fb, a.d * fa + b.d * fb};
+// Sum and maximum over a row of 16 lanes, in all of them.
+__device__ __forceinline__ float row_sum(float x) {
+  x += dpp<0xB1>(x);   // neighbours, pairs, quads and halves
+  x += dpp<0x4E>(x);
+  x += dpp<0x124>(x);
+  x += dpp<0x128>(x);
+  return x;
 }
-// Parts of NW waves (a wave's is the same in its lanes), joined in wave order.
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, dpp<0xB1>(x));
+  x = fmaxf(x, dpp<0x4E>(x));
+  x = fmaxf(x, dpp<0x124>(x));
+  x = fmaxf(x, dpp<0x128>(x));
+  return x;
+}
+// The same over the lanes of a group, 16 or a wave.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x = row_sum(x);
+  if constexpr (LANES == 64) {
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+  }
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float x) {
+  x = row_max(x);
+  if constexpr (LANES == 64) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    x = fmaxf(x, __shfl_xor(x, 32));
+  }
+  return x;
+}
+
+// Parts of NW waves (a wave's is the same in its lanes), joined in each row of
+// 16 lanes.  One barrier: `at` is another place the next time.
 template <int NW>
 __device__ __forceinline__ Part block_join(Part p, float c, Part* at) {
   if constexpr (NW == 1) return p;
+  const int w = threadIdx.x >> 6, i = threadIdx.x & 15;
+  if ((threadIdx.x & 63) == 0) at[w] = p;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = p;
-  __syncthreads();
-  p = at[0];
-  for (int w = 1; w < NW; ++w) p = joined(p, at[w], c);
-  return p;
+  p = i < NW ? at[i] : Part{-FLT_MAX, 0.f, 0.f};
+  const float m = row_max(p.m), f = exp2_of((p.m - m) * c);
+  return Part{m, row_sum(p.s * f), row_sum(p.d * f)};
 }
 
 // VEC values of a row from element d on; those past V are -inf.
@@ -155,7 +168,7 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, int64_t n, flo
     l.p[j] = x;
     m = fmaxf(m, x);
   }
-  m = wave_max(m);
+  m = lanes_max<64>(m);
   if constexpr (NT > 64) {
     __syncthreads();
     if ((t & 63) == 0) l.far[t >> 6] = m;
@@ -170,7 +183,7 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, int64_t n, flo
     s += e;
   }
   if (bad) s = __builtin_nanf("");
-  s = wave_sum(s);
+  s = lanes_sum<64>(s);
   if constexpr (NT > 64) {
     __syncthreads();
     if ((t & 63) == 0) l.far[t >> 6] = s;
@@ -211,8 +224,9 @@ __global__ void __launch_bounds__(NT) k_distill_long(DistillArgs a) {
         p.m = m;
         p.s = s;
       }
-      const float m = wave_max(p.m);
-      p = Part{m, wave_sum(p.s * exp2_of((p.m - m) * c)), 0.f};
+      const float m = lanes_max<64>(p.m);
+      p = Part{m, lanes_sum<64>(p.s * exp2_of((p.m - m) * c)), 0.f};
+      __syncthreads();
       p = block_join<NT / 64>(p, c, l.parts);
       if (a.stats && t == 0) {
         a.stats[2 * n] = p.m;
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(NT) k_distill_long(DistillArgs a) {
           sum += e * (((x - tm) * c - lt) - ((Elem<TYPE>::get(row[id]) - p.m) * c - lq));
         }
       }
-      sum = wave_sum(sum);
+      sum = lanes_sum<64>(sum);
       __syncthreads();
       if ((t & 63) == 0) l.far[t >> 6] = sum;
       __syncthreads();
@@ -289,15 +303,208 @@ __global__ void __launch_bounds__(NT) k_distill_long(DistillArgs a) {
   }
 }
 
+// Rows of up to 16 NT elements, in the registers of NT lanes: 16, a wave, or a
+// workgroup.  The list is the business of the row's first 16 or 64 lanes, in
+// the workgroup's case of its first wave.  The gradient takes p from `mass`, a
+// place for each component that is zero but for those listed: they are set, read
+// with the row's own elements, and cleared again.  An id listed twice is found
+// by what stands in its place once all have left their numbers there.
+template <int LANES>
+__device__ __forceinline__ bool lanes_any(bool x) {
+  const u64 b = __ballot(x);
+  if constexpr (LANES == 64) return b != 0;
+  return ((b >> (threadIdx.x & 48)) & 0xffff) != 0;
+}
+
+template <int TYPE, int NT, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_distill_held(DistillArgs a) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = kVec<TYPE>, Q = kHeld / VEC, ROWS = NT < 256 ? 256 / NT : 1, NW = NT > 64 ? NT / 64 : 1;
+  constexpr int LANES = NT < 64 ? NT : 64, LIST = NT > 64 ? kList : 64;
+  __shared__ __attribute__((aligned(16))) float mass_[GRAD ? ROWS : 1][GRAD ? NT * kHeld : 1];
+  __shared__ int ids_[ROWS][NW > 1 ? 2 : 1][LIST];
+  __shared__ float xs_[ROWS][LIST], zs_[STATS ? ROWS : 1][STATS ? LIST : 1];
+  __shared__ Part parts[2][16];
+  __shared__ float ts_[2];
+  const int t = threadIdx.x % NT, r = threadIdx.x / NT, V = a.V, k = a.k;
+  const bool lister = t < LANES;
+  float *const mass = mass_[GRAD ? r : 0], *const xs = xs_[r], *const zs = zs_[STATS ? r : 0];
+  if constexpr (GRAD) {
+    for (int i = t; i < NT * kHeld; i += NT) mass[i] = 0.f;
+    wave_sync();  // a workgroup's: read behind barriers
+  }
+  const float c = kLog2e / a.temperature;
+  int before = 0, turn = 0;  // length of the list whose places are set
+  for (int64_t n0 = (int64_t)blockIdx.x * ROWS; n0 < a.N; n0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+    const bool there = n0 + r < a.N;
+    const int64_t n = there ? n0 + r : a.N - 1;  // lanes without a row repeat the last one and write nothing
+    const T* row = static_cast<const T*>(a.z) + n * a.ld;
+    float e[kHeld];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) load_vec<TYPE>(row, (q * NT + t) * VEC, V, e + q * VEC);
+    int *const ids = ids_[r][NW > 1 ? turn : 0], *const old = ids_[r][NW > 1 ? turn ^ 1 : 0];
+    if constexpr (GRAD && NW == 1) {
+      for (int j = t; j < before; j += LANES)
+        if (old[j] >= 0) mass[old[j]] = 0.f;
+      wave_sync();
+    }
+    float ts = 0.f, tm = -__builtin_inff();
+    if (lister) {
+      bool bad = false;
+      for (int j = t; j < k; j += LANES) {
+        const int id = id_at(a.ids, a.wide, n * a.ld_ids + j, V);
+        const float x = id < 0 ? -__builtin_inff() : float_at(a.teacher, a.teacher_type, n * a.ld_teacher + j);
+        bad |= id >= V || !(x < __builtin_inff());
+        const bool listed = x > -__builtin_inff() && id < V;
+        ids[j] = listed ? id : -1;
+        xs[j] = x;
+        if constexpr (STATS) zs[j] = listed ? Elem<TYPE>::get(row[id]) : 0.f;
+        tm = fmaxf(tm, x);
+      }
+      tm = lanes_max<LANES>(tm);
+      if (!(tm > -__builtin_inff())) tm = 0.f;
+      for (int j = t; j < k; j += LANES) {
+        const float x = (xs[j] - tm) * c;
+        xs[j] = x;
+        ts += exp2_of(x);
+      }
+      if (bad) ts = __builtin_nanf("");
+      ts = lanes_sum<LANES>(ts);
+      if (NW > 1 && t == 0) ts_[turn] = ts;
+    }
+    // e: exponentials from the largest logit that the wave knows; f: what takes them to the row's
+    Part p;
+    float f = 1.f;
+    if constexpr (STATS) {
+      float m = -FLT_MAX, s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) m = fmaxf(m, e[i]);
+      m = lanes_max<LANES>(m);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        e[i] = exp2_of((e[i] - m) * c);
+        s += e[i];
+      }
+      p = block_join<NW>(Part{m, lanes_sum<LANES>(s), 0.f}, c, parts[turn]);
+      f = exp2_of((m - p.m) * c);
+    } else {
+      p = Part{a.stats[2 * n], a.stats[2 * n + 1], 0.f};
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) e[i] = exp2_of((e[i] - p.m) * c);
+      if constexpr (NW > 1) __syncthreads();
+    }
+    if constexpr (NW > 1) ts = ts_[turn];
+    const float by = GRAD ? (a.weights ? a.weights[n * a.ld_weights] : a.weight) * a.temperature : 0.f;
+    if (lister) {
+      if constexpr (STATS) {
+        const float lt = log2_of(ts), ls = log2_of(p.s);
+        float gap = 0.f;
+        for (int j = t; j < k; j += LANES) {
+          const float x = xs[j], w = exp2_of(x);
+          if (ids[j] >= 0 && w != 0.f) gap += w * ((x - lt) - ((zs[j] - p.m) * c - ls));
+        }
+        gap = lanes_sum<LANES>(gap);
+        if (t == 0 && there) {
+          a.losses[n] = ts == 0.f ? 0.f : a.temperature * a.temperature * kLn2 * (gap / ts);
+          if (a.stats) {
+            a.stats[2 * n] = p.m;
+            a.stats[2 * n + 1] = p.s;
+          }
+        }
+      }
+      if constexpr (GRAD) {
+        if constexpr (NW > 1) {
+          for (int j = t; j < before; j += LANES)
+            if (old[j] >= 0) mass[old[j]] = 0.f;
+          wave_sync();
+        }
+        before = k;
+        int* const marks = reinterpret_cast<int*>(mass);
+        for (int j = t; j < k; j += LANES)
+          if (ids[j] >= 0) marks[ids[j]] = j;
+        wave_sync();
+        bool twice = false;
+        for (int j = t; j < k; j += LANES) twice |= ids[j] >= 0 && marks[ids[j]] != j;
+        twice = lanes_any<LANES>(twice);
+        wave_sync();
+        const float part = by / ts;
+        for (int j = t; j < k; j += LANES) {
+          const int id = ids[j];
+          if (id < 0) continue;
+          float w = exp2_of(xs[j]);
+          if (twice) {  // the places of an id share the sum, in the order of the list
+            w = 0.f;
+            for (int i = 0; i < k; ++i)
+              if (ids[i] == id) w += exp2_of(xs[i]);
+          }
+          mass[id] = w * part;
+        }
+        wave_sync();
+      }
+    }
+    if constexpr (GRAD) {
+      if constexpr (NW > 1) __syncthreads();
+      float each = by / p.s * f;
+      if (!(ts > 0.f)) {  // nothing listed, or no answer
+        each = ts;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) e[i] = 0.f;
+      }
+      T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int d = (q * NT + t) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+          const f4 w = *reinterpret_cast<const f4*>(mass + d + i);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[q * VEC + i + y] = e[q * VEC + i + y] * each - w[y];
+        }
+        if (there) store_vec<TYPE>(out, d, V, e + q * VEC);
+      }
+    }
+  }
+}
+
+template <int TYPE, int NT>
+void distill_held(const DistillArgs& a, hipStream_t s) {
+  constexpr int BLOCK = NT < 256 ? 256 : NT, ROWS = BLOCK / NT;
+  const int64_t most = 256 * 2048 / BLOCK, need = (a.N + ROWS - 1) / ROWS;  // workgroups that fit the card at once
+  const dim3 grid((unsigned)(need < most ? need : most)), block(BLOCK);
+  if (!a.grad)
+    hipLaunchKernelGGL((k_distill_held<TYPE, NT, true, false>), grid, block, 0, s, a);
+  else if (a.losses)
+    hipLaunchKernelGGL((k_distill_held<TYPE, NT, true, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_distill_held<TYPE, NT, false, true>), grid, block, 0, s, a);
+}
+
 template <int TYPE>
 hipError_t distill_as(const DistillArgs& a, void* workspace, hipStream_t s) {
-  const dim3 grid((unsigned)(a.N < 65536 ? a.N : 65536)), block(256);
+  if (a.V <= 16 * kHeld && a.k <= 64) {
+    distill_held<TYPE, 16>(a, s);
+    return hipGetLastError();
+  }
+  if (a.V <= 64 * kHeld && a.k <= 64) {
+    distill_held<TYPE, 64>(a, s);
+    return hipGetLastError();
+  }
+  if (a.V <= 1024 * kHeld) {
+    if (a.V <= 256 * kHeld)
+      distill_held<TYPE, 256>(a, s);
+    else if (a.V <= 512 * kHeld)
+      distill_held<TYPE, 512>(a, s);
+    else
+      distill_held<TYPE, 1024>(a, s);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(a.N < 65536 ? a.N : 65536)), block(1024);
   if (!a.grad)
-    hipLaunchKernelGGL((k_distill_long<TYPE, 256, true, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, true, false>), grid, block, 0, s, a);
   else if (a.losses)
-    hipLaunchKernelGGL((k_distill_long<TYPE, 256, true, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, true, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((k_distill_long<TYPE, 256, false, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, false, true>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -325,7 +532,14 @@ int64_t count_blocks(int64_t N, int K, int k) {
   const int64_t b = (N * k + 8191) / 8192, most = K <= 65536 ? 128 : (1 << 23) / K;
   return b < 1 ? 1 : b < most ? b : most;
 }
-int64_t row_blocks(int64_t N) { return N < 4096 ? N : 4096; }
+// Workgroups of the row kernels: as many as the card holds at once, where there
+// are rows for them.
+int64_t row_blocks(int64_t N, int K) {
+  const int lanes = K <= 16 * kHeld ? 16 : K <= 64 * kHeld ? 64 : K <= 256 * kHeld ? 256 : K <= 512 * kHeld ? 512 : 1024;
+  const int64_t rows = lanes < 256 ? 256 / lanes : 1, need = (N + rows - 1) / rows;
+  const int64_t most = 256 * 2048 / (lanes < 256 ? 256 : lanes);
+  return need < most ? need : most;
+}
 
 }  // namespace
 
@@ -333,7 +547,7 @@ int64_t row_blocks(int64_t N) { return N < 4096 ? N : 4096; }
 // each workgroup of the row kernel
 size_t balance_workspace(int64_t N, int K, int k) {
   const int64_t b = count_blocks(N, K, k);
-  return (size_t)(16 * ((b * K * 4 + 15) / 16) + 16 * b + 8 * row_blocks(N));
+  return (size_t)(16 * ((b * K * 4 + 15) / 16) + 16 * b + 8 * row_blocks(N, K));
 }
 
 namespace {
@@ -441,8 +655,9 @@ __global__ void __launch_bounds__(NT) k_balance_long(BalanceArgs a, double* __re
           }
           p = Part{m, s, w};
         }
-        const float m = wave_max(p.m), f = exp2_of((p.m - m) * c);
-        p = Part{m, wave_sum(p.s * f), wave_sum(p.d * f)};
+        const float m = lanes_max<64>(p.m), f = exp2_of((p.m - m) * c);
+        p = Part{m, lanes_sum<64>(p.s * f), lanes_sum<64>(p.d * f)};
+        __syncthreads();
         p = block_join<NT / 64>(p, c, parts);
       }
       m = p.m;
@@ -477,6 +692,90 @@ __global__ void __launch_bounds__(NT) k_balance_long(BalanceArgs a, double* __re
   if (STATS && t == 0) sums[blockIdx.x] = total;
 }
 
+// Rows of up to 16 NT elements, in the registers of NT lanes, with the counts of
+// those elements.
+template <int TYPE, int NT, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_balance_held(BalanceArgs a, double* __restrict__ sums) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = kVec<TYPE>, Q = kHeld / VEC, ROWS = NT < 256 ? 256 / NT : 1, NW = NT > 64 ? NT / 64 : 1;
+  constexpr int LANES = NT < 64 ? NT : 64;
+  __shared__ Part parts[2][16];
+  __shared__ double totals[ROWS];
+  const int t = threadIdx.x % NT, r = threadIdx.x / NT, K = a.K;
+  const int64_t N = a.N;
+  const float* cs = a.stats + BalanceLayout::c_at(N);
+  const float scale = cs[K], c = kLog2e, by = GRAD ? (a.weight_at ? *a.weight_at : a.weight) * scale : 0.f;
+  float w[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int d = (i / VEC * NT + t) * VEC + i % VEC;
+    w[i] = d < K ? cs[d] : 0.f;
+  }
+  double total = 0;
+  int turn = 0;
+  for (int64_t n0 = (int64_t)blockIdx.x * ROWS; n0 < N; n0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+    const bool there = n0 + r < N;
+    const int64_t n = there ? n0 + r : N - 1;  // lanes without a row repeat the last one and write nothing
+    const T* row = static_cast<const T*>(a.z) + n * a.ld;
+    float e[kHeld];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) load_vec<TYPE>(row, (q * NT + t) * VEC, K, e + q * VEC);
+    float inv, d, f = 1.f;
+    if constexpr (STATS) {
+      bool in = false;
+      for (int j = t & (LANES - 1); j < a.k; j += LANES) in |= id_at(a.ids, a.wide, n * a.ld_ids + j, K) >= 0;
+      in = lanes_any<LANES>(in);
+      float m = -FLT_MAX, s = 0.f, x = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) m = fmaxf(m, e[i]);
+      m = lanes_max<LANES>(m);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        e[i] = exp2_of((e[i] - m) * c);
+        s += e[i];
+        x += e[i] * w[i];
+      }
+      const Part p = block_join<NW>(Part{m, lanes_sum<LANES>(s), lanes_sum<LANES>(x)}, c, parts[turn]);
+      f = exp2_of((m - p.m) * c);
+      inv = in ? 1.f / p.s : 0.f;
+      d = in ? p.d * inv : 0.f;
+      if (there) total += d;
+      if (t == 0 && there) {
+        a.stats[n] = p.m;
+        a.stats[N + n] = inv;
+        a.stats[2 * N + n] = d;
+      }
+    } else {
+      const float m = a.stats[n];
+      inv = a.stats[N + n];
+      d = a.stats[2 * N + n];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) e[i] = exp2_of((e[i] - m) * c);
+    }
+    if constexpr (GRAD) {
+      const float each = by * inv * f;
+      if (inv == 0.f) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) e[i] = 0.f;
+      }
+      T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) e[i] *= (w[i] - d) * each;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (there) store_vec<TYPE>(out, (q * NT + t) * VEC, K, e + q * VEC);
+    }
+  }
+  if constexpr (STATS) {
+    if (t == 0) totals[r] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < ROWS; ++i) total += totals[i];
+      sums[blockIdx.x] = total;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) k_balance_loss(BalanceArgs a, int blocks, const double* __restrict__ sums) {
   __shared__ double at[256];
   double s = 0;
@@ -490,11 +789,47 @@ __global__ void __launch_bounds__(256) k_balance_loss(BalanceArgs a, int blocks,
   if (threadIdx.x == 0) *a.loss = (float)(at[0] * (double)a.stats[BalanceLayout::c_at(a.N) + a.K]);
 }
 
+template <int TYPE, int NT, bool HELD>
+void balance_rows(const BalanceArgs& a, int64_t grid, double* sums, hipStream_t s) {
+  const dim3 g((unsigned)grid), b(NT < 256 ? 256 : NT);
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, 0, s, a, sums); };
+  if constexpr (HELD) {
+    if (!a.grad)
+      launch(k_balance_held<TYPE, NT, true, false>);
+    else if (a.loss)
+      launch(k_balance_held<TYPE, NT, true, true>);
+    else
+      launch(k_balance_held<TYPE, NT, false, true>);
+  } else {
+    if (!a.grad)
+      launch(k_balance_long<TYPE, NT, true, false>);
+    else if (a.loss)
+      launch(k_balance_long<TYPE, NT, true, true>);
+    else
+      launch(k_balance_long<TYPE, NT, false, true>);
+  }
+}
+template <int TYPE>
+void balance_rows_for(const BalanceArgs& a, int64_t grid, double* sums, hipStream_t s) {
+  if (a.K <= 16 * kHeld)
+    balance_rows<TYPE, 16, true>(a, grid, sums, s);
+  else if (a.K <= 64 * kHeld)
+    balance_rows<TYPE, 64, true>(a, grid, sums, s);
+  else if (a.K <= 256 * kHeld)
+    balance_rows<TYPE, 256, true>(a, grid, sums, s);
+  else if (a.K <= 512 * kHeld)
+    balance_rows<TYPE, 512, true>(a, grid, sums, s);
+  else if (a.K <= 1024 * kHeld)
+    balance_rows<TYPE, 1024, true>(a, grid, sums, s);
+  else
+    balance_rows<TYPE, 1024, false>(a, grid, sums, s);
+}
+
 template <int TYPE>
 hipError_t balance_as(const BalanceArgs& a, void* workspace, hipStream_t s) {
-  const unsigned grid = (unsigned)row_blocks(a.N);
+  const int64_t grid = row_blocks(a.N, a.K);
   if (!a.loss) {
-    hipLaunchKernelGGL((k_balance_long<TYPE, 256, false, true>), dim3(grid), dim3(256), 0, s, a, nullptr);
+    balance_rows_for<TYPE>(a, grid, nullptr, s);
     return hipGetLastError();
   }
   const int64_t blocks = count_blocks(a.N, a.K, a.k), share = (a.N + blocks - 1) / blocks;
@@ -504,12 +839,7 @@ hipError_t balance_as(const BalanceArgs& a, void* workspace, hipStream_t s) {
   hipLaunchKernelGGL(k_balance_count, dim3((unsigned)blocks, (unsigned)((a.K + kBins - 1) / kBins)), dim3(1024), 0, s, a,
                      share, part, totals);
   hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)((a.K + 255) / 256)), dim3(256), 0, s, a, (int)blocks, part, totals);
-  if (grid) {
-    if (a.grad)
-      hipLaunchKernelGGL((k_balance_long<TYPE, 256, true, true>), dim3(grid), dim3(256), 0, s, a, sums);
-    else
-      hipLaunchKernelGGL((k_balance_long<TYPE, 256, true, false>), dim3(grid), dim3(256), 0, s, a, sums);
-  }
+  if (grid) balance_rows_for<TYPE>(a, grid, sums, s);
   hipLaunchKernelGGL(k_balance_loss, dim3(1), dim3(256), 0, s, a, (int)grid, sums);
   return hipGetLastError();
 }
