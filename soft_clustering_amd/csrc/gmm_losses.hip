@@ -12,13 +12,15 @@
 // again, which a call that wants both still holds in registers.  What bounds
 // them is the logits' bytes.
 //
-// Exponentials are exp2((z - M) log2(e) / T) with M the largest logit seen by
-// the wave or thread, at least the lowest finite float32: a logit of -inf then
-// gives 0, a row of nothing but the lowest float its even weights, a row of
-// nothing but -inf a sum of 0 and from there NaN; what is below 2^-126 of the
-// largest counts as 0.  Sums are float32 over at
-// most 2^20 terms in a fixed tree (a thread's share, its wave, the waves), the
-// sum over rows float64.
+// Exponentials are exp2(z c - m c), c = log2(e) / T, in one fused operation from
+// the rounded m c, with m the largest logit seen by the thread or wave, at least
+// the lowest finite float32: that rounding is the same for all that is compared
+// with m, and drops out.  Where m c is no finite number they are
+// exp2((z - m) c).  A logit of -inf gives 0, a row of nothing but the lowest
+// float its even weights, a row of nothing but -inf a sum of 0 and from there
+// NaN; what is below 2^-126 of the largest counts as 0.  Sums are float32 over
+// at most 2^20 terms in a fixed tree (a thread's share, its wave, the waves),
+// the sum over rows float64.
 #include "gmm_rows_device.h"
 
 #include <float.h>
@@ -29,26 +31,59 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-constexpr int kHeld = 16;  // elements of a lane where rows are held in registers
-
 template <int TYPE>
 constexpr int kVec = TYPE == kFloat ? 4 : 8;  // elements of one 16-byte load
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
 
+// The largest of three; a NaN only where all are.  (As an instruction: fmaxf
+// first copies operands that might be signalling NaNs.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+template <int E>
+__device__ __forceinline__ float max_of(const float (&e)[E]) {
+  float m = -FLT_MAX;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) m = max3(m, e[i], e[i + 1]);
+  return m;
+}
+
+// Exponentials that are compared with m.
+struct Exps {
+  float m, c, mc;
+  bool wide;
+  __device__ __forceinline__ Exps(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), wide(!(fabsf(mc) <= FLT_MAX)) {}
+  __device__ __forceinline__ float log2(float z) const { return wide ? (z - m) * c : fmaf(z, c, -mc); }
+  __device__ __forceinline__ float of(float z) const { return exp2_of(log2(z)); }
+  template <int E>
+  __device__ __forceinline__ void all(float (&e)[E]) const {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = exp2_of((e[i] - m) * c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = exp2_of(fmaf(e[i], c, -mc));
+    }
+  }
+  // what takes exponentials compared with `from` to these (from <= m)
+  __device__ __forceinline__ float factor(float from) const {
+#pragma clang fp contract(off)  // the difference of the two rounded products
+    const float fc = from * c;
+    return wide || !(fabsf(fc) <= FLT_MAX) ? exp2_of((from - m) * c) : exp2_of(fc - mc);
+  }
+};
+
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
 }
-// What is known of a row (or a part of it): the largest logit, the sum of
-// exponentials, their c-weighted sum.
-struct Part {
-  float m, s, d;
-};
 // Sum and maximum over a row of 16 lanes, in all of them.
 __device__ __forceinline__ float row_sum(float x) {
-  x += dpp<0xB1>(x);   // neighbours, pairs, quads and halves
+  x += dpp<0xB1>(x);  // neighbours, pairs, quads and halves
   x += dpp<0x4E>(x);
   x += dpp<0x124>(x);
   x += dpp<0x128>(x);
@@ -61,13 +96,16 @@ __device__ __forceinline__ float row_max(float x) {
   x = fmaxf(x, dpp<0x128>(x));
   return x;
 }
-// The same over the lanes of a group, 16 or a wave.
+// The same over the lanes of a group, 16 or a wave.  The swaps put the values of
+// the other row, the other half, beside a lane's own.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float x) {
   x = row_sum(x);
   if constexpr (LANES == 64) {
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(q[0]) + __uint_as_float(q[1]);
   }
   return x;
 }
@@ -75,240 +113,13 @@ template <int LANES>
 __device__ __forceinline__ float lanes_max(float x) {
   x = row_max(x);
   if constexpr (LANES == 64) {
-    x = fmaxf(x, __shfl_xor(x, 16));
-    x = fmaxf(x, __shfl_xor(x, 32));
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
   }
   return x;
 }
-
-// Parts of NW waves (a wave's is the same in its lanes), joined in each row of
-// 16 lanes.  One barrier: `at` is another place the next time.
-template <int NW>
-__device__ __forceinline__ Part block_join(Part p, float c, Part* at) {
-  if constexpr (NW == 1) return p;
-  const int w = threadIdx.x >> 6, i = threadIdx.x & 15;
-  if ((threadIdx.x & 63) == 0) at[w] = p;
-  __syncthreads();
-  p = i < NW ? at[i] : Part{-FLT_MAX, 0.f, 0.f};
-  const float m = row_max(p.m), f = exp2_of((p.m - m) * c);
-  return Part{m, row_sum(p.s * f), row_sum(p.d * f)};
-}
-
-// VEC values of a row from element d on; those past V are -inf.
-template <int TYPE>
-__device__ __forceinline__ void load_vec(const typename Elem<TYPE>::T* __restrict__ row, int d, int V, float* v) {
-  using T = typename Elem<TYPE>::T;
-  constexpr int VEC = kVec<TYPE>;
-  if (d + VEC <= V) {
-    T t[VEC];
-    __builtin_memcpy(t, row + d, sizeof t);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = Elem<TYPE>::get(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = d + i < V ? Elem<TYPE>::get(row[d + i]) : -__builtin_inff();
-  }
-}
-template <int TYPE>
-__device__ __forceinline__ void store_vec(typename Elem<TYPE>::T* __restrict__ row, int d, int V, const float* v) {
-  using T = typename Elem<TYPE>::T;
-  constexpr int VEC = kVec<TYPE>;
-  T t[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) t[i] = Elem<TYPE>::put(v[i]);
-  if (d + VEC <= V) {
-    store16<false>(row + d, t);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      if (d + i < V) row[d + i] = t[i];
-  }
-}
-
-__device__ __forceinline__ float float_at(const void* p, int type, int64_t i) {
-  if (type == kFloat) return static_cast<const float*>(p)[i];
-  if (type == kBfloat) return (float)static_cast<const __bf16*>(p)[i];
-  return (float)static_cast<const _Float16*>(p)[i];
-}
-// An id, at most `most` (64-bit ids may be larger than an int).
-__device__ __forceinline__ int id_at(const void* p, bool wide, int64_t i, int most) {
-  if (!wide) return min(static_cast<const int*>(p)[i], most);
-  const long long id = static_cast<const long long*>(p)[i];
-  return id < 0 ? -1 : id > most ? most : (int)id;
-}
-
-// ---------------------------------------------------------------------------
-// Distillation
-
-constexpr int kList = 1024;       // teacher's logits of a row at most
-constexpr int kSeenBits = 32768;  // ids seen, by their low bits
-
-struct List {
-  int id[kList];
-  float p[kList];
-  unsigned seen[kSeenBits / 32];
-  Part parts[16];
-  float far[16];
-};
-
-// The teacher's softmax over the ids that row n lists, into the list (p; -1 in
-// place of what is not listed).  tm, ts: largest logit and sum of exponentials;
-// ts = 0 where nothing is listed, NaN where the row has no answer (an id out of
-// range, a NaN or +inf).
-template <int NT>
-__device__ __forceinline__ void teacher_row(const DistillArgs& a, int64_t n, float c, List& l, float& tm, float& ts) {
-  const int t = threadIdx.x;
-  float m = -__builtin_inff();
-  bool bad = false;
-  for (int j = t; j < a.k; j += NT) {
-    const int id = id_at(a.ids, a.wide, n * a.ld_ids + j, a.V);
-    float x = id < 0 ? -__builtin_inff() : float_at(a.teacher, a.teacher_type, n * a.ld_teacher + j);
-    bad |= id >= a.V || !(x < __builtin_inff());
-    l.id[j] = x > -__builtin_inff() && id < a.V ? id : -1;
-    l.p[j] = x;
-    m = fmaxf(m, x);
-  }
-  m = lanes_max<64>(m);
-  if constexpr (NT > 64) {
-    __syncthreads();
-    if ((t & 63) == 0) l.far[t >> 6] = m;
-    __syncthreads();
-    for (int w = 0; w < NT / 64; ++w) m = fmaxf(m, l.far[w]);
-  }
-  float s = 0.f;
-  const float from = m > -__builtin_inff() ? m : 0.f;
-  for (int j = t; j < a.k; j += NT) {
-    const float e = exp2_of((l.p[j] - from) * c);
-    l.p[j] = e;
-    s += e;
-  }
-  if (bad) s = __builtin_nanf("");
-  s = lanes_sum<64>(s);
-  if constexpr (NT > 64) {
-    __syncthreads();
-    if ((t & 63) == 0) l.far[t >> 6] = s;
-    __syncthreads();
-    s = l.far[0];
-    for (int w = 1; w < NT / 64; ++w) s += l.far[w];
-  }
-  tm = from;
-  ts = s;
-}
-
-// One workgroup to a row, which it reads a second time for the gradient.
-// STATS: the row's numbers are found here (and the loss, and they are kept);
-// otherwise they are read.  GRAD: the gradient is written.
-template <int TYPE, int NT, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(NT) k_distill_long(DistillArgs a) {
-  using T = typename Elem<TYPE>::T;
-  constexpr int VEC = kVec<TYPE>;
-  __shared__ List l;
-  const int t = threadIdx.x, V = a.V;
-  const float c = kLog2e / a.temperature;
-  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-    const T* row = static_cast<const T*>(a.z) + n * a.ld;
-    float tm, ts;
-    __syncthreads();
-    teacher_row<NT>(a, n, c, l, tm, ts);
-    Part p{-FLT_MAX, 0.f, 0.f};
-    if constexpr (STATS) {
-      for (int d = t * VEC; d < V; d += NT * VEC) {
-        float v[VEC];
-        load_vec<TYPE>(row, d, V, v);
-        float m = p.m;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) m = fmaxf(m, v[i]);
-        float s = p.s * exp2_of((p.m - m) * c);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s += exp2_of((v[i] - m) * c);
-        p.m = m;
-        p.s = s;
-      }
-      const float m = lanes_max<64>(p.m);
-      p = Part{m, lanes_sum<64>(p.s * exp2_of((p.m - m) * c)), 0.f};
-      __syncthreads();
-      p = block_join<NT / 64>(p, c, l.parts);
-      if (a.stats && t == 0) {
-        a.stats[2 * n] = p.m;
-        a.stats[2 * n + 1] = p.s;
-      }
-      // the loss
-      float sum = 0.f;
-      const float lt = log2_of(ts), lq = log2_of(p.s);
-      for (int j = t; j < a.k; j += NT) {
-        const int id = l.id[j];
-        const float e = l.p[j];
-        if (id >= 0 && e != 0.f) {
-          const float x = float_at(a.teacher, a.teacher_type, n * a.ld_teacher + j);
-          sum += e * (((x - tm) * c - lt) - ((Elem<TYPE>::get(row[id]) - p.m) * c - lq));
-        }
-      }
-      sum = lanes_sum<64>(sum);
-      __syncthreads();
-      if ((t & 63) == 0) l.far[t >> 6] = sum;
-      __syncthreads();
-      if (t == 0) {
-        sum = l.far[0];
-        for (int w = 1; w < NT / 64; ++w) sum += l.far[w];
-        a.losses[n] = ts == 0.f ? 0.f : a.temperature * a.temperature * kLn2 * (sum / ts);
-      }
-    } else {
-      p.m = a.stats[2 * n];
-      p.s = a.stats[2 * n + 1];
-    }
-    if constexpr (GRAD) {
-      T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
-      const float by = (a.weights ? a.weights[n * a.ld_weights] : a.weight) * a.temperature;
-      if (ts == 0.f) {  // nothing listed
-        const float zero[VEC] = {};
-        for (int d = t * VEC; d < V; d += NT * VEC) store_vec<TYPE>(out, d, V, zero);
-        continue;
-      }
-      const float each = ts == ts ? by / p.s : ts;
-      for (int i = t; i < kSeenBits / 32; i += NT) l.seen[i] = 0;
-      for (int d = t * VEC; d < V; d += NT * VEC) {
-        float v[VEC];
-        load_vec<TYPE>(row, d, V, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = exp2_of((v[i] - p.m) * c) * each;
-        store_vec<TYPE>(out, d, V, v);
-      }
-      __syncthreads();  // the row is written
-      bool twice = false;
-      for (int j = t; j < a.k; j += NT) {
-        const int id = l.id[j];
-        if (id >= 0) {
-          const unsigned bit = 1u << (id & 31);
-          twice |= atomicOr(&l.seen[(id & (kSeenBits - 1)) >> 5], bit) & bit;
-        }
-      }
-      const bool some = __syncthreads_or(twice);
-      for (int j = t; j < a.k; j += NT) {
-        const int id = l.id[j];
-        if (id < 0) continue;
-        float e = l.p[j];
-        if (some) {  // perhaps an id is listed twice: its first place takes the sum, in order
-          e = 0.f;
-          bool first = true;
-          for (int i = 0; i < a.k; ++i) {
-            if (l.id[i] != id) continue;
-            first &= i >= j;
-            e += l.p[i];
-          }
-          if (!first) continue;
-        }
-        out[id] = Elem<TYPE>::put(exp2_of((Elem<TYPE>::get(row[id]) - p.m) * c) * each - by * (e / ts));
-      }
-    }
-  }
-}
-
-// Rows of up to 16 NT elements, in the registers of NT lanes: 16, a wave, or a
-// workgroup.  The list is the business of the row's first 16 or 64 lanes, in
-// the workgroup's case of its first wave.  The gradient takes p from `mass`, a
-// place for each component that is zero but for those listed: they are set, read
-// with the row's own elements, and cleared again.  An id listed twice is found
-// by what stands in its place once all have left their numbers there.
 template <int LANES>
 __device__ __forceinline__ bool lanes_any(bool x) {
   const u64 b = __ballot(x);
@@ -316,195 +127,704 @@ __device__ __forceinline__ bool lanes_any(bool x) {
   return ((b >> (threadIdx.x & 48)) & 0xffff) != 0;
 }
 
-template <int TYPE, int NT, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_distill_held(DistillArgs a) {
+// What is known of a row (or a part of it): the largest logit, the sum of the
+// exponentials compared with it, their c-weighted sum.
+struct Part {
+  float m, s, d;
+};
+// Parts of lanes, joined in all of them.
+template <int LANES>
+__device__ __forceinline__ Part lanes_join(Part p, float c) {
+  const Exps x(lanes_max<LANES>(p.m), c);
+  const float f = x.factor(p.m);
+  return Part{x.m, lanes_sum<LANES>(p.s * f), lanes_sum<LANES>(p.d * f)};
+}
+// Parts of NW waves (a wave's is the same in its lanes) of a workgroup, the
+// first of them wave w0, joined in each row of 16 lanes.  One barrier: `at` is
+// another place the next time.
+template <int NW>
+__device__ __forceinline__ Part block_join(Part p, float c, Part* at, int w0) {
+  if constexpr (NW == 1) return p;
+  const int i = threadIdx.x & 15;
+  if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = p;
+  __syncthreads();
+  return lanes_join<16>(i < NW ? at[w0 + i] : Part{-FLT_MAX, 0.f, 0.f}, c);
+}
+
+// Vectors of a row are numbered by lanes; vector i holds elements VEC i on.  One
+// that would reach behind the row's end (of V >= VEC elements) lies at its end
+// instead: its first `skip` elements are others' as well (all, where it would
+// lie behind it altogether).  They have no part in sums; in maxima and results
+// they do no harm, as all who have an element find and write the same for it.
+template <int TYPE>
+struct Vec {
   using T = typename Elem<TYPE>::T;
-  constexpr int VEC = kVec<TYPE>, Q = kHeld / VEC, ROWS = NT < 256 ? 256 / NT : 1, NW = NT > 64 ? NT / 64 : 1;
-  constexpr int LANES = NT < 64 ? NT : 64, LIST = NT > 64 ? kList : 64;
-  __shared__ __attribute__((aligned(16))) float mass_[GRAD ? ROWS : 1][GRAD ? NT * kHeld : 1];
-  __shared__ int ids_[ROWS][NW > 1 ? 2 : 1][LIST];
-  __shared__ float xs_[ROWS][LIST], zs_[STATS ? ROWS : 1][STATS ? LIST : 1];
-  __shared__ Part parts[2][16];
-  __shared__ float ts_[2];
-  const int t = threadIdx.x % NT, r = threadIdx.x / NT, V = a.V, k = a.k;
+  typedef T Pair __attribute__((ext_vector_type(2)));
+  static constexpr int N = kVec<TYPE>;
+  i4 v;  // as stored: 16-bit elements two to a register
+  static __device__ __forceinline__ int place(int i, int V) { return min(i * N, V - N); }
+  static __device__ __forceinline__ int skip(int i, int V) { return max(i * N - (V - N), 0); }
+  __device__ __forceinline__ void load(const T* __restrict__ at) { __builtin_memcpy(&v, at, 16); }
+  __device__ __forceinline__ void store(T* __restrict__ at) const { store16<false>(at, &v); }
+  __device__ __forceinline__ void get(float* e) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kFloat) {
+        e[i] = __int_as_float(v[i]);
+      } else if constexpr (TYPE == kBfloat) {
+        e[2 * i] = __uint_as_float((unsigned)v[i] << 16);
+        e[2 * i + 1] = __uint_as_float((unsigned)v[i] & 0xffff0000u);
+      } else {
+        const Pair p = __builtin_bit_cast(Pair, (int)v[i]);
+        e[2 * i] = (float)p.x;
+        e[2 * i + 1] = (float)p.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float* e) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kFloat)
+        v[i] = __float_as_int(e[i]);
+      else
+        v[i] = __builtin_bit_cast(int, Pair{(T)e[2 * i], (T)e[2 * i + 1]});
+    }
+  }
+};
+
+// The sum of a lane's E exponentials, vectors NT lanes apart, but for those that
+// it skips.
+template <int TYPE, int NT, int E>
+__device__ __forceinline__ float sum_of(const float (&e)[E], int t, int V) {
+  constexpr int VEC = kVec<TYPE>;
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < E / VEC; ++q) {
+    if ((q + 1) * NT * VEC <= V) {  // the same for all lanes
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s += e[q * VEC + i];
+    } else {
+      const int skip = Vec<TYPE>::skip(q * NT + t, V);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s += i < skip ? 0.f : e[q * VEC + i];
+    }
+  }
+  return s;
+}
+
+// An id, at most `most` (64-bit ids may be larger than an int).
+__device__ __forceinline__ int id_at(const void* p, bool wide, int64_t i, int most) {
+  if (!wide) return min(static_cast<const int*>(p)[i], most);
+  const long long id = static_cast<const long long*>(p)[i];
+  return id < 0 ? -1 : id > most ? most : (int)id;
+}
+
+// Workgroups that the card holds at once, with `waves` to a SIMD.
+int64_t resident(int waves, int block) { return 256 * (int64_t)waves * 256 / block; }
+int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// ---------------------------------------------------------------------------
+// Distillation
+
+constexpr int kHeldWidth = 16384;  // rows up to here are held by a workgroup at most
+constexpr int kList = 1024;       // teacher's logits of a row at most
+constexpr int kSeenBits = 32768;  // ids seen, by their low bits
+
+// A row's list, in LDS, the business of LANES lanes.
+template <int LIST>
+struct Listed {
+  int id[LIST];   // -1 where nothing is listed
+  float x[LIST];  // exponents of the teacher's logits
+  float z[LIST];  // the row's own logits there
+};
+
+// One place of the list of row n, as it is stored: nothing is done with the
+// values before they are used, so a row's can be on their way during another's
+// work.  A place behind the list repeats the last.
+struct Place {
+  int lo, hi;
+  unsigned x;
+  __device__ __forceinline__ void load(const DistillArgs& a, int64_t n, int j) {
+    j = min(j, a.k - 1);
+    const int64_t i = n * a.ld_ids + j, l = n * a.ld_teacher + j;
+    if (a.wide) {
+      lo = static_cast<const int*>(a.ids)[2 * i];
+      hi = static_cast<const int*>(a.ids)[2 * i + 1];
+    } else {
+      lo = static_cast<const int*>(a.ids)[i];
+    }
+    if (a.teacher_type == kFloat)
+      x = static_cast<const unsigned*>(a.teacher)[l];
+    else
+      x = static_cast<const unsigned short*>(a.teacher)[l];
+  }
+  // negative: none; at most V: out of range
+  __device__ __forceinline__ int id(const DistillArgs& a) const {
+    if (!a.wide) return min(lo, a.V);
+    return hi < 0 ? -1 : hi > 0 || lo < 0 ? a.V : min(lo, a.V);
+  }
+  __device__ __forceinline__ float logit(const DistillArgs& a) const {
+    if (a.teacher_type == kFloat) return __uint_as_float(x);
+    if (a.teacher_type == kBfloat) return __uint_as_float(x << 16);
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)x);
+  }
+};
+
+// Puts the list of row n into LDS (`first`: the lane's first place of it, which
+// is there already); tm, bad: the largest teacher's logit, whether one has no
+// answer (an id out of range, a NaN or +inf), of this lane's.
+template <int TYPE, int LANES, int LIST>
+__device__ __forceinline__ void read_list(const DistillArgs& a, int64_t n, const typename Elem<TYPE>::T* row, int t,
+                                          Place first, Listed<LIST>& l, float& tm, bool& bad) {
+  tm = -__builtin_inff();
+  bad = false;
+  for (int j = t; j < a.k; j += LANES) {
+    Place p = first;
+    if (j >= LANES) p.load(a, n, j);
+    const int id = p.id(a);
+    const float x = id < 0 ? -__builtin_inff() : p.logit(a);
+    bad |= id >= a.V || !(x < __builtin_inff());
+    const bool listed = x > -__builtin_inff() && id < a.V;
+    l.id[j] = listed ? id : -1;
+    l.x[j] = x;
+    l.z[j] = listed ? Elem<TYPE>::get(row[id]) : 0.f;
+    tm = fmaxf(tm, x);
+  }
+}
+// The teacher's sum of exponentials, and their exponents into the list: 0 where
+// nothing is listed, NaN where there is no answer.
+template <int LANES, int LIST>
+__device__ __forceinline__ float list_sum(const DistillArgs& a, int t, float c, Listed<LIST>& l, float tm, bool bad) {
+  float ts = 0.f;
+  tm = lanes_max<LANES>(tm);
+  if (!(tm > -__builtin_inff())) tm = 0.f;
+  for (int j = t; j < a.k; j += LANES) {
+    const float x = (l.x[j] - tm) * c;
+    l.x[j] = x;
+    ts += exp2_of(x);
+  }
+  if (bad) ts = __builtin_nanf("");
+  return lanes_sum<LANES>(ts);
+}
+
+// The loss of a row whose exponentials, compared with x.m, sum to s.
+template <int LANES, int LIST>
+__device__ __forceinline__ float list_loss(const DistillArgs& a, int t, const Exps& x, const Listed<LIST>& l, float ts,
+                                           float s) {
+  const float lt = log2_of(ts), ls = log2_of(s);
+  float gap = 0.f;
+  for (int j = t; j < a.k; j += LANES) {
+    const float y = l.x[j], w = exp2_of(y);
+    if (l.id[j] >= 0 && w != 0.f) gap += w * ((y - lt) - (x.log2(l.z[j]) - ls));
+  }
+  gap = lanes_sum<LANES>(gap);
+  return ts == 0.f ? 0.f : a.temperature * a.temperature * kLn2 * (gap / ts);
+}
+
+// The gradient at the listed places from `low` to `high`, over what the row's
+// lanes have written there (before a barrier, or in the same wave): each q_id -
+// sum of its p.  `seen` has a bit for each id, by its low bits, all clear: an id
+// listed twice (or two with the same bits) is found by its bit, and then takes
+// the sum over its places, in their order, from the first of them.
+template <int TYPE, int LANES, int LIST, int BITS>
+__device__ __forceinline__ void list_gradient(const DistillArgs& a, int t, const Exps& x, const Listed<LIST>& l, float ts,
+                                              float each, float by, typename Elem<TYPE>::T* out, unsigned* seen,
+                                              int low, int high) {
+  bool twice = false;
+  for (int j = t; j < a.k; j += LANES) {
+    const int id = l.id[j];
+    const unsigned bit = 1u << (id & 31);
+    if (id >= low && id < high) twice |= (atomicOr(&seen[(id & (BITS - 1)) >> 5], bit) & bit) != 0;
+  }
+  twice = lanes_any<LANES>(twice);
+  wave_sync();
+  const float part = by / ts;
+  for (int j = t; j < a.k; j += LANES) {
+    const int id = l.id[j];
+    if (id < low || id >= high) continue;
+    seen[(id & (BITS - 1)) >> 5] = 0;
+    float w = exp2_of(l.x[j]);
+    if (twice) {
+      w = 0.f;
+      bool first = true;
+      for (int i = 0; i < a.k; ++i)
+        if (l.id[i] == id) {
+          first &= i >= j;
+          w += exp2_of(l.x[i]);
+        }
+      if (!first) continue;
+    }
+    out[id] = Elem<TYPE>::put(x.of(l.z[j]) * each - w * part);
+  }
+}
+
+__device__ __forceinline__ float row_weight(const DistillArgs& a, int64_t n) {
+  return (a.weights ? a.weights[n * a.ld_weights] : a.weight) * a.temperature;
+}
+
+// Where the numbers of row n are kept, or, where they are not, where the loss
+// replaces them.
+__device__ __forceinline__ void keep(const DistillArgs& a, int64_t n, float m, float s, float loss) {
+  float* const at = a.stats ? a.stats + 2 * n : a.losses + n;
+  at[0] = m;
+  at[a.stats ? 1 : 0] = s;
+  a.losses[n] = loss;
+}
+
+// Rows of up to E NT elements, in the registers of NT lanes: 16, a wave, or more
+// waves of a workgroup of BLOCK.  The list is the business of the row's first 16
+// or 64 lanes.  STATS: the row's numbers are found here (and the loss, and they
+// are kept); otherwise they are read.  GRAD: the gradient is written.
+// Each group has one row: another's loads would wait for this one's stores.
+// Groups behind the last row do that row again, with the same results.
+template <int TYPE, int NT, int E, int BLOCK, int WAVES, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = kVec<TYPE>, Q = E / VEC, ROWS = BLOCK / NT, NW = NT > 64 ? NT / 64 : 1;
+  constexpr int LANES = NT < 64 ? NT : 64, LIST = NT > 64 ? kList : 64, BITS = NT * E < kSeenBits ? NT * E : kSeenBits;
+  __shared__ Listed<LIST> lists[ROWS];
+  __shared__ unsigned seen_[GRAD ? ROWS : 1][GRAD ? BITS / 32 : 1];
+  __shared__ Part parts[16];
+  __shared__ float ts_[ROWS];
+  const int t = threadIdx.x % NT, r = threadIdx.x / NT, V = a.V;
   const bool lister = t < LANES;
-  float *const mass = mass_[GRAD ? r : 0], *const xs = xs_[r], *const zs = zs_[STATS ? r : 0];
+  Listed<LIST>& l = lists[r];
+  unsigned* const seen = seen_[GRAD ? r : 0];
+  const int64_t n = min((int64_t)blockIdx.x * ROWS + r, a.N - 1);
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  Place first{};
+  if (lister) first.load(a, n, t);
+  Vec<TYPE> raw[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) raw[q].load(row + Vec<TYPE>::place(q * NT + t, V));
   if constexpr (GRAD) {
-    for (int i = t; i < NT * kHeld; i += NT) mass[i] = 0.f;
-    wave_sync();  // a workgroup's: read behind barriers
+    for (int i = t; i < BITS / 32; i += NT) seen[i] = 0;
+    wave_sync();  // a workgroup's: used behind barriers
   }
   const float c = kLog2e / a.temperature;
-  int before = 0, turn = 0;  // length of the list whose places are set
-  for (int64_t n0 = (int64_t)blockIdx.x * ROWS; n0 < a.N; n0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
-    const bool there = n0 + r < a.N;
-    const int64_t n = there ? n0 + r : a.N - 1;  // lanes without a row repeat the last one and write nothing
-    const T* row = static_cast<const T*>(a.z) + n * a.ld;
-    float e[kHeld];
+  float ts = 0.f, tm = 0.f;
+  bool bad = false;
+  if (lister) read_list<TYPE, LANES>(a, n, row, t, first, l, tm, bad);
+  float e[E];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) load_vec<TYPE>(row, (q * NT + t) * VEC, V, e + q * VEC);
-    int *const ids = ids_[r][NW > 1 ? turn : 0], *const old = ids_[r][NW > 1 ? turn ^ 1 : 0];
-    if constexpr (GRAD && NW == 1) {
-      for (int j = t; j < before; j += LANES)
-        if (old[j] >= 0) mass[old[j]] = 0.f;
-      wave_sync();
-    }
-    float ts = 0.f, tm = -__builtin_inff();
+  for (int q = 0; q < Q; ++q) raw[q].get(e + q * VEC);
+  // e: exponentials compared with the largest logit that the wave knows; f: what takes them to the row's
+  Part p;
+  float f = 1.f;
+  if constexpr (STATS) {
+    const Exps x(lanes_max<LANES>(max_of(e)), c);
+    x.all(e);
+    p = Part{x.m, lanes_sum<LANES>(sum_of<TYPE, NT>(e, t, V)), 0.f};
     if (lister) {
-      bool bad = false;
-      for (int j = t; j < k; j += LANES) {
-        const int id = id_at(a.ids, a.wide, n * a.ld_ids + j, V);
-        const float x = id < 0 ? -__builtin_inff() : float_at(a.teacher, a.teacher_type, n * a.ld_teacher + j);
-        bad |= id >= V || !(x < __builtin_inff());
-        const bool listed = x > -__builtin_inff() && id < V;
-        ids[j] = listed ? id : -1;
-        xs[j] = x;
-        if constexpr (STATS) zs[j] = listed ? Elem<TYPE>::get(row[id]) : 0.f;
-        tm = fmaxf(tm, x);
-      }
-      tm = lanes_max<LANES>(tm);
-      if (!(tm > -__builtin_inff())) tm = 0.f;
-      for (int j = t; j < k; j += LANES) {
-        const float x = (xs[j] - tm) * c;
-        xs[j] = x;
-        ts += exp2_of(x);
-      }
-      if (bad) ts = __builtin_nanf("");
-      ts = lanes_sum<LANES>(ts);
-      if (NW > 1 && t == 0) ts_[turn] = ts;
+      ts = list_sum<LANES>(a, t, c, l, tm, bad);
+      if (NW > 1 && t == 0) ts_[r] = ts;
     }
-    // e: exponentials from the largest logit that the wave knows; f: what takes them to the row's
-    Part p;
-    float f = 1.f;
+    p = block_join<NW>(p, c, parts, r * NW);
+    if constexpr (NW > 1) f = Exps(p.m, c).factor(x.m);
+  } else {
+    p = Part{a.stats[2 * n], a.stats[2 * n + 1], 0.f};
+    Exps(p.m, c).all(e);
+    if (lister) {
+      ts = list_sum<LANES>(a, t, c, l, tm, bad);
+      if (NW > 1 && t == 0) ts_[r] = ts;
+    }
+    if constexpr (NW > 1) __syncthreads();
+  }
+  if constexpr (NW > 1) ts = ts_[r];
+  const Exps x(p.m, c);
+  if constexpr (GRAD) {
+    const float by = row_weight(a, n), each = by / p.s;
+    const bool answer = ts > 0.f;  // otherwise nothing is listed (0), or the row has none (NaN)
+    if (!answer) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = ts;
+    }
+    const float scale = answer ? each * f : 1.f;
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] *= scale;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      raw[q].put(e + q * VEC);
+      raw[q].store(out + Vec<TYPE>::place(q * NT + t, V));
+    }
+    if constexpr (NW > 1)
+      __syncthreads();
+    else
+      wave_sync();
+    if (lister && answer) list_gradient<TYPE, LANES, LIST, BITS>(a, t, x, l, ts, each, by, out, seen, 0, V);
+  }
+  if constexpr (STATS) {
+    if (lister) {
+      const float loss = list_loss<LANES>(a, t, x, l, ts, p.s);
+      if (t == 0) keep(a, n, p.m, p.s, loss);
+    }
+  }
+}
+
+// A thread's part of a row of V elements from G of its vectors, q and on, that
+// are NT lanes apart.
+template <int TYPE, int G, int NT>
+__device__ __forceinline__ void add_vectors(Part& p, const Vec<TYPE>* v, float c, int q, int t, int V) {
+  constexpr int VEC = kVec<TYPE>;
+  float e[G * VEC];
+#pragma unroll
+  for (int i = 0; i < G; ++i) v[i].get(e + i * VEC);
+  const Exps x(fmaxf(max_of(e), p.m), c);
+  x.all(e);
+  if ((q + G) * NT * VEC > V) {  // the same for all lanes
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int skip = Vec<TYPE>::skip((q + i) * NT + t, V);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) e[i * VEC + j] = j < skip ? 0.f : e[i * VEC + j];
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < G * VEC; ++i) s += e[i];
+  p = Part{x.m, p.s * x.factor(p.m) + s, 0.f};
+}
+
+// Longer rows, many: a workgroup to each.  HELD vectors of a thread are kept
+// between the row's numbers and its gradient (16: 131072 16-bit elements, 65536
+// float32); what is behind them is read again.  As the gradient of a vector
+// leaves, the next row's comes in.  HELD is 0 where only one of the two is asked
+// for.
+template <int TYPE, int HELD, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs a) {
+  using T = typename Elem<TYPE>::T;
+  using W = Vec<TYPE>;
+  constexpr int VEC = kVec<TYPE>;
+  __shared__ Listed<kList> l;
+  __shared__ unsigned seen[GRAD ? kSeenBits / 32 : 1];
+  __shared__ Part parts[2][16];
+  __shared__ float ts_[2];
+  int t = threadIdx.x;
+  const int V = a.V, vectors = (V + 1024 * VEC - 1) / (1024 * VEC);  // of a thread
+  const bool lister = t < 64;
+  if constexpr (GRAD) {
+    seen[t] = 0;
+    static_assert(kSeenBits / 32 == 1024, "a word for each thread");
+  }
+  const float c = kLog2e / a.temperature;
+  int64_t n = blockIdx.x;
+  Place first{};  // of the list to come
+  if (lister) first.load(a, n, t);
+  constexpr int STEP = 1024 * VEC;
+  // a thread's vector q from base: one decision for all lanes, so that most places are a constant apart
+  const auto at = [&](auto* base, int q) { return base + ((q + 1) * STEP <= V ? q * STEP + t * VEC : W::place(q * 1024 + t, V)); };
+  W v[HELD ? HELD : 1];
+#pragma unroll
+  for (int q = 0; q < HELD; ++q)
+    if (q < vectors) v[q].load(at(static_cast<const T*>(a.z) + n * a.ld, q));
+  int turn = 0;
+  for (; n < a.N; n += gridDim.x, turn ^= 1) {
+    asm volatile("" : "+v"(t));  // places are found again: not kept for all vectors over all rows
+    const T* row = static_cast<const T*>(a.z) + n * a.ld;
+    const int64_t after = min(n + gridDim.x, a.N - 1);
+    float ts = 0.f;
+    if (lister) {
+      float tm;
+      bool bad;
+      read_list<TYPE, 64>(a, n, row, t, first, l, tm, bad);
+      first.load(a, after, t);
+      ts = list_sum<64>(a, t, c, l, tm, bad);
+      if (t == 0) ts_[turn] = ts;
+    }
+    Part p{-FLT_MAX, 0.f, 0.f};
     if constexpr (STATS) {
-      float m = -FLT_MAX, s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) m = fmaxf(m, e[i]);
-      m = lanes_max<LANES>(m);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        e[i] = exp2_of((e[i] - m) * c);
-        s += e[i];
+      for (int q = 0; q < HELD; ++q) {
+        asm volatile("" : "+v"(v[q].v));  // unpacked here, not when they arrive
+        if (q < vectors) add_vectors<TYPE, 1, 1024>(p, v + q, c, q, t, V);
       }
-      p = block_join<NW>(Part{m, lanes_sum<LANES>(s), 0.f}, c, parts[turn]);
-      f = exp2_of((m - p.m) * c);
+      for (int q = HELD; q < vectors; q += 2) {
+        W w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i].load(row + W::place((q + i) * 1024 + t, V));
+        add_vectors<TYPE, 2, 1024>(p, w, c, q, t, V);
+      }
+      p = block_join<16>(lanes_join<64>(p, c), c, parts[turn], 0);
     } else {
       p = Part{a.stats[2 * n], a.stats[2 * n + 1], 0.f};
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) e[i] = exp2_of((e[i] - p.m) * c);
-      if constexpr (NW > 1) __syncthreads();
+      __syncthreads();
     }
-    if constexpr (NW > 1) ts = ts_[turn];
-    const float by = GRAD ? (a.weights ? a.weights[n * a.ld_weights] : a.weight) * a.temperature : 0.f;
-    if (lister) {
-      if constexpr (STATS) {
-        const float lt = log2_of(ts), ls = log2_of(p.s);
-        float gap = 0.f;
-        for (int j = t; j < k; j += LANES) {
-          const float x = xs[j], w = exp2_of(x);
-          if (ids[j] >= 0 && w != 0.f) gap += w * ((x - lt) - ((zs[j] - p.m) * c - ls));
-        }
-        gap = lanes_sum<LANES>(gap);
-        if (t == 0 && there) {
-          a.losses[n] = ts == 0.f ? 0.f : a.temperature * a.temperature * kLn2 * (gap / ts);
-          if (a.stats) {
-            a.stats[2 * n] = p.m;
-            a.stats[2 * n + 1] = p.s;
-          }
-        }
-      }
-      if constexpr (GRAD) {
-        if constexpr (NW > 1) {
-          for (int j = t; j < before; j += LANES)
-            if (old[j] >= 0) mass[old[j]] = 0.f;
-          wave_sync();
-        }
-        before = k;
-        int* const marks = reinterpret_cast<int*>(mass);
-        for (int j = t; j < k; j += LANES)
-          if (ids[j] >= 0) marks[ids[j]] = j;
-        wave_sync();
-        bool twice = false;
-        for (int j = t; j < k; j += LANES) twice |= ids[j] >= 0 && marks[ids[j]] != j;
-        twice = lanes_any<LANES>(twice);
-        wave_sync();
-        const float part = by / ts;
-        for (int j = t; j < k; j += LANES) {
-          const int id = ids[j];
-          if (id < 0) continue;
-          float w = exp2_of(xs[j]);
-          if (twice) {  // the places of an id share the sum, in the order of the list
-            w = 0.f;
-            for (int i = 0; i < k; ++i)
-              if (ids[i] == id) w += exp2_of(xs[i]);
-          }
-          mass[id] = w * part;
-        }
-        wave_sync();
-      }
-    }
+    ts = ts_[turn];
+    const Exps x(p.m, c);
     if constexpr (GRAD) {
-      if constexpr (NW > 1) __syncthreads();
-      float each = by / p.s * f;
-      if (!(ts > 0.f)) {  // nothing listed, or no answer
-        each = ts;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) e[i] = 0.f;
-      }
+      const T* next = static_cast<const T*>(a.z) + after * a.ld;
+      const float by = row_weight(a, n), each = by / p.s;
+      const bool answer = ts > 0.f;
       T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+      const auto gradient = [&](W& w, int q) {
+        float e[VEC];
+        w.get(e);
+        x.all(e);
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const int d = (q * NT + t) * VEC;
+        for (int i = 0; i < VEC; ++i) e[i] = answer ? e[i] * each : ts;
+        w.put(e);
+        w.store(at(out, q));
+      };
 #pragma unroll
-        for (int i = 0; i < VEC; i += 4) {
-          const f4 w = *reinterpret_cast<const f4*>(mass + d + i);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) e[q * VEC + i + y] = e[q * VEC + i + y] * each - w[y];
+      for (int q = 0; q < HELD; ++q) {
+        asm volatile("" : "+v"(v[q].v));  // unpacked again: the floats of before are not kept
+        if (q < vectors) {
+          gradient(v[q], q);
+          v[q].load(at(next, q));
         }
-        if (there) store_vec<TYPE>(out, d, V, e + q * VEC);
+      }
+      for (int q = HELD; q < vectors; q += 2) {
+        W w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i].load(row + W::place((q + i) * 1024 + t, V));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) gradient(w[i], q + i);
+      }
+      __syncthreads();
+      if (lister && answer) list_gradient<TYPE, 64, kList, kSeenBits>(a, t, x, l, ts, each, by, out, seen, 0, V);
+    }
+    if constexpr (STATS) {
+      if (lister) {
+        const float loss = list_loss<64>(a, t, x, l, ts, p.s);
+        if (t == 0) keep(a, n, p.m, p.s, loss);
       }
     }
   }
 }
 
-template <int TYPE, int NT>
+// Longer rows, few: divided over workgroups of 256, `range` elements to each.
+// First the parts' numbers, then, from all of a row's, the loss (by its first
+// workgroup) and the gradient of each part, which reads its elements again.
+template <int TYPE>
+__global__ void __launch_bounds__(256) k_distill_parts(DistillArgs a, int range, Part* __restrict__ out) {
+  using T = typename Elem<TYPE>::T;
+  using W = Vec<TYPE>;
+  constexpr int VEC = kVec<TYPE>;
+  __shared__ Part parts[16];
+  const int t = threadIdx.x, low = (int)blockIdx.x * range, V = min(range, a.V - low);
+  const float c = kLog2e / a.temperature;
+  const T* row = static_cast<const T*>(a.z) + (int64_t)blockIdx.y * a.ld + low;
+  Part p{-FLT_MAX, 0.f, 0.f};
+  for (int q = 0; q * 256 * VEC < V; q += 4) {
+    W v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].load(row + W::place((q + i) * 256 + t, V));
+    add_vectors<TYPE, 4, 256>(p, v, c, q, t, V);
+  }
+  p = block_join<4>(lanes_join<64>(p, c), c, parts, 0);
+  if (t == 0) out[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = p;
+}
+
+template <int TYPE, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(256) k_distill_finish(DistillArgs a, int range, int splits, const Part* __restrict__ in) {
+  using T = typename Elem<TYPE>::T;
+  using W = Vec<TYPE>;
+  constexpr int VEC = kVec<TYPE>;
+  __shared__ Listed<kList> l;
+  __shared__ unsigned seen[GRAD ? kSeenBits / 32 : 1];
+  __shared__ float ts_;
+  const int t = threadIdx.x, low = (int)blockIdx.x * range, V = min(range, a.V - low);
+  const int64_t n = blockIdx.y;
+  const float c = kLog2e / a.temperature;
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  if constexpr (GRAD) {
+    for (int i = t; i < kSeenBits / 32; i += 256) seen[i] = 0;
+  }
+  float ts = 0.f;
+  if (t < 64) {
+    float tm;
+    bool bad;
+    Place first{};
+    first.load(a, n, t);
+    read_list<TYPE, 64>(a, n, row, t, first, l, tm, bad);
+    ts = list_sum<64>(a, t, c, l, tm, bad);
+    if (t == 0) ts_ = ts;
+  }
+  Part p;
+  if constexpr (STATS) {
+    const int i = t & 63;
+    p = lanes_join<64>(i < splits ? in[n * splits + i] : Part{-FLT_MAX, 0.f, 0.f}, c);
+  } else {
+    p = Part{a.stats[2 * n], a.stats[2 * n + 1], 0.f};
+  }
+  __syncthreads();
+  ts = ts_;
+  const Exps x(p.m, c);
+  if constexpr (GRAD) {
+    const float by = row_weight(a, n), each = by / p.s;
+    const bool answer = ts > 0.f;
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+    for (int q = 0; q * 256 * VEC < V; q += 2) {
+      W v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i].load(row + low + W::place((q + i) * 256 + t, V));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float e[VEC];
+        v[i].get(e);
+        x.all(e);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) e[j] = answer ? e[j] * each : ts;
+        v[i].put(e);
+        v[i].store(out + low + W::place((q + i) * 256 + t, V));
+      }
+    }
+    __syncthreads();
+    if (t < 64 && answer) list_gradient<TYPE, 64, kList, kSeenBits>(a, t, x, l, ts, each, by, out, seen, low, low + V);
+  }
+  if constexpr (STATS) {
+    if (blockIdx.x == 0 && t < 64) {
+      const float loss = list_loss<64>(a, t, x, l, ts, p.s);
+      if (t == 0) keep(a, n, p.m, p.s, loss);
+    }
+  }
+}
+
+// Rows shorter than a vector: a thread to each.
+template <int TYPE>
+__global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = kVec<TYPE>;
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= a.N) return;
+  const float c = kLog2e / a.temperature;
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  float e[VEC], p[VEC] = {}, m = -FLT_MAX, tm = -__builtin_inff(), ts = 0.f, s = 0.f;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    e[i] = i < a.V ? Elem<TYPE>::get(row[i]) : -__builtin_inff();
+    m = fmaxf(m, e[i]);
+  }
+  if (!stats) m = a.stats[2 * n];
+  const Exps x(m, c);
+  // the list is read twice: for its largest logit, for the sums
+  bool bad = false;
+  const auto place = [&](int j, float& y) {
+    Place at;
+    at.load(a, n, j);
+    const int id = at.id(a);
+    y = id < 0 ? -__builtin_inff() : at.logit(a);
+    bad |= id >= a.V || !(y < __builtin_inff());
+    return id >= a.V || !(y > -__builtin_inff()) ? -1 : id;
+  };
+  for (int j = 0; j < a.k; ++j) {
+    float y;
+    place(j, y);
+    tm = fmaxf(tm, y);
+  }
+  if (!(tm > -__builtin_inff())) tm = 0.f;
+  float gap = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    float y;
+    const int id = place(j, y);
+    const float lp = (y - tm) * c, w = exp2_of(lp);
+    ts += w;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i == id) {
+        p[i] += w;
+        if (w != 0.f) gap += w * (lp - x.log2(e[i]));
+      }
+  }
+  if (bad) ts = __builtin_nanf("");
+  x.all(e);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s += e[i];
+  if (stats) {
+    const float loss = a.temperature * a.temperature * kLn2 * (gap / ts + (log2_of(s) - log2_of(ts)));
+    keep(a, n, m, s, ts == 0.f ? 0.f : loss);
+  } else {
+    s = a.stats[2 * n + 1];
+  }
+  if (a.grad) {
+    const float by = row_weight(a, n), each = by / s, part = by / ts;
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < a.V) out[i] = Elem<TYPE>::put(ts > 0.f ? e[i] * each - p[i] * part : ts);
+  }
+}
+
+// Parts of a longer row: enough to fill the card, of at least 8192 elements, at most 64.
+int distill_splits(int64_t N, int V) {
+  if (V <= kHeldWidth || N >= 256) return 1;
+  const int64_t most = fewer((V + 8191) / 8192, 64), want = (1024 + N - 1) / N;
+  return (int)fewer(most, want);
+}
+
+template <int TYPE, int NT, int E, int BLOCK, int WAVES>
 void distill_held(const DistillArgs& a, hipStream_t s) {
-  constexpr int BLOCK = NT < 256 ? 256 : NT, ROWS = BLOCK / NT;
-  const int64_t most = 256 * 2048 / BLOCK, need = (a.N + ROWS - 1) / ROWS;  // workgroups that fit the card at once
-  const dim3 grid((unsigned)(need < most ? need : most)), block(BLOCK);
+  constexpr int ROWS = BLOCK / NT;
+  const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS));
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(BLOCK), 0, s, a); };
   if (!a.grad)
-    hipLaunchKernelGGL((k_distill_held<TYPE, NT, true, false>), grid, block, 0, s, a);
+    launch(k_distill_held<TYPE, NT, E, BLOCK, WAVES, true, false>);
   else if (a.losses)
-    hipLaunchKernelGGL((k_distill_held<TYPE, NT, true, true>), grid, block, 0, s, a);
+    launch(k_distill_held<TYPE, NT, E, BLOCK, WAVES, true, true>);
   else
-    hipLaunchKernelGGL((k_distill_held<TYPE, NT, false, true>), grid, block, 0, s, a);
+    launch(k_distill_held<TYPE, NT, E, BLOCK, WAVES, false, true>);
+}
+
+template <int TYPE>
+hipError_t distill_long(const DistillArgs& a, void* workspace, hipStream_t s) {
+  const int splits = distill_splits(a.N, a.V);
+  if (splits == 1) {
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)fewer(a.N, resident(a.grad && a.losses ? 4 : 8, 1024))), dim3(1024), 0, s, a);
+    };
+    const bool half = a.V <= 8 * 1024 * kVec<TYPE>;
+    if (!a.grad)
+      launch(k_distill_wide<TYPE, 0, true, false>);
+    else if (a.losses)
+      half ? launch(k_distill_wide<TYPE, 8, true, true>) : launch(k_distill_wide<TYPE, 16, true, true>);
+    else
+      launch(k_distill_wide<TYPE, 0, false, true>);
+    return hipGetLastError();
+  }
+  constexpr int STEP = 256 * kVec<TYPE>;
+  const int range = ((a.V + splits - 1) / splits + STEP - 1) / STEP * STEP, parts = (a.V + range - 1) / range;
+  const dim3 all((unsigned)parts, (unsigned)a.N), one(1, (unsigned)a.N), block(256);
+  Part* in = static_cast<Part*>(workspace);
+  if (a.losses) {
+    hipLaunchKernelGGL(k_distill_parts<TYPE>, all, block, 0, s, a, range, in);
+    if (a.grad)
+      hipLaunchKernelGGL((k_distill_finish<TYPE, true, true>), all, block, 0, s, a, range, parts, in);
+    else
+      hipLaunchKernelGGL((k_distill_finish<TYPE, true, false>), one, block, 0, s, a, range, parts, in);
+  } else {
+    hipLaunchKernelGGL((k_distill_finish<TYPE, false, true>), all, block, 0, s, a, range, parts, in);
+  }
+  return hipGetLastError();
 }
 
 template <int TYPE>
 hipError_t distill_as(const DistillArgs& a, void* workspace, hipStream_t s) {
-  if (a.V <= 16 * kHeld && a.k <= 64) {
-    distill_held<TYPE, 16>(a, s);
+  if (a.V < kVec<TYPE>) {
+    hipLaunchKernelGGL(k_distill_tiny<TYPE>, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, a, a.losses != nullptr);
     return hipGetLastError();
   }
-  if (a.V <= 64 * kHeld && a.k <= 64) {
-    distill_held<TYPE, 64>(a, s);
-    return hipGetLastError();
+  const bool few = a.k <= 64;
+  if constexpr (TYPE != kFloat) {
+    if (a.V > 256 && a.V <= 1024 && few && a.N >= 8192) {
+      distill_held<TYPE, 16, 64, 256, 3>(a, s);
+      return hipGetLastError();
+    }
+    if (a.V > 4096 && a.V <= kHeldWidth && a.N >= 1024) {
+      distill_held<TYPE, 512, 32, 512, 4>(a, s);
+      return hipGetLastError();
+    }
   }
-  if (a.V <= 1024 * kHeld) {
-    if (a.V <= 256 * kHeld)
-      distill_held<TYPE, 256>(a, s);
-    else if (a.V <= 512 * kHeld)
-      distill_held<TYPE, 512>(a, s);
-    else
-      distill_held<TYPE, 1024>(a, s);
-    return hipGetLastError();
-  }
-  const dim3 grid((unsigned)(a.N < 65536 ? a.N : 65536)), block(1024);
-  if (!a.grad)
-    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, true, false>), grid, block, 0, s, a);
-  else if (a.losses)
-    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, true, true>), grid, block, 0, s, a);
+  if (a.V <= 256 && few)
+    distill_held<TYPE, 16, 16, 256, 6>(a, s);
+  else if (a.V <= 1024 && few)
+    distill_held<TYPE, 64, 16, 256, 7>(a, s);
+  else if (a.V <= 4096)
+    distill_held<TYPE, 256, 16, 256, 4>(a, s);
+  else if (a.V <= kHeldWidth)
+    distill_held<TYPE, 1024, 16, 1024, 4>(a, s);
   else
-    hipLaunchKernelGGL((k_distill_long<TYPE, 1024, false, true>), grid, block, 0, s, a);
+    return distill_long<TYPE>(a, workspace, s);
   return hipGetLastError();
 }
 
@@ -515,39 +835,33 @@ constexpr int kBins = 16384;  // counters of a workgroup
 
 // Parts of a balance call's workspace and of what it keeps for the backward.
 struct BalanceLayout {
-  int64_t blocks, row_blocks;
-  // floats kept: m[N], 1 / s[N], d[N], c[K], scale
-  __host__ __device__ static int64_t c_at(int64_t N) { return 3 * N; }
+  // floats kept: m[N], 1 / s[N], d[N], then from a multiple of 4 c[K], scale
+  __host__ __device__ static int64_t c_at(int64_t N) { return (3 * N + 3) / 4 * 4; }
 };
 
 }  // namespace
 
-size_t balance_stats(int64_t N, int K) { return (size_t)(3 * N + K + 1); }
+size_t balance_stats(int64_t N, int K) { return (size_t)(BalanceLayout::c_at(N) + K + 1); }
 
 namespace {
 
-// Counting workgroups: one for each 8192 ids, up to 128 and to 32 MB of partial
+// Counting workgroups: one for each 2048 ids, up to 128 and to 32 MB of partial
 // counts.
 int64_t count_blocks(int64_t N, int K, int k) {
-  const int64_t b = (N * k + 8191) / 8192, most = K <= 65536 ? 128 : (1 << 23) / K;
+  const int64_t b = (N * k + 2047) / 2048, most = K <= 65536 ? 128 : (1 << 23) / K;
   return b < 1 ? 1 : b < most ? b : most;
 }
-// Workgroups of the row kernels: as many as the card holds at once, where there
-// are rows for them.
-int64_t row_blocks(int64_t N, int K) {
-  const int lanes = K <= 16 * kHeld ? 16 : K <= 64 * kHeld ? 64 : K <= 256 * kHeld ? 256 : K <= 512 * kHeld ? 512 : 1024;
-  const int64_t rows = lanes < 256 ? 256 / lanes : 1, need = (N + rows - 1) / rows;
-  const int64_t most = 256 * 2048 / (lanes < 256 ? 256 : lanes);
-  return need < most ? need : most;
-}
+
+// Workgroups that sum the rows' d, 4096 to each, up to 64.
+int loss_blocks(int64_t N) { return (int)(N <= 4096 ? 1 : fewer((N + 4095) / 4096, 64)); }
 
 }  // namespace
 
-// partial counts [blocks][K], ids and rows and faults of each block, row sums of
-// each workgroup of the row kernel
+// partial counts [blocks][K], ids and rows and faults of each block, partial
+// sums of d, how many of those are there
 size_t balance_workspace(int64_t N, int K, int k) {
   const int64_t b = count_blocks(N, K, k);
-  return (size_t)(16 * ((b * K * 4 + 15) / 16) + 16 * b + 8 * row_blocks(N, K));
+  return (size_t)(16 * ((b * K * 4 + 15) / 16) + 16 * b + 64 * 8 + 16);
 }
 
 namespace {
@@ -557,9 +871,47 @@ struct Totals {
   unsigned rows, bad;
 };
 
+// 1024 threads count the ids of rows n0 .. n1 - 1 that fall into `width` bins
+// from `first` on; sums: ids in range, rows that have an id, whether one is out
+// of range.
+__device__ __forceinline__ void count_rows(const BalanceArgs& a, int64_t n0, int64_t n1, int first, int width,
+                                           unsigned* bins, unsigned* sums) {
+  unsigned ids = 0, rows = 0;
+  bool bad = false;
+  for (int64_t n = n0 + threadIdx.x; n < n1; n += 1024) {
+    bool any = false;
+    for (int j = 0; j < a.k; j += 4) {
+      int id[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) id[x] = j + x < a.k ? id_at(a.ids, a.wide, n * a.ld_ids + j + x, a.K) : -1;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        any |= id[x] >= 0;
+        bad |= id[x] >= a.K;
+        ids += id[x] >= 0 && id[x] < a.K;
+        if ((unsigned)(id[x] - first) < (unsigned)width) atomicAdd(&bins[id[x] - first], 1u);
+      }
+    }
+    rows += any;
+  }
+  for (int w = 32; w > 0; w >>= 1) {
+    ids += __shfl_xor(ids, w);
+    rows += __shfl_xor(rows, w);
+  }
+  const bool worse = __any(bad);
+  if ((threadIdx.x & 63) == 0) {
+    atomicAdd(&sums[0], ids);
+    atomicAdd(&sums[1], rows);
+    if (worse) atomicOr(&sums[2], 1u);
+  }
+}
+__device__ __forceinline__ float balance_scale(int K, unsigned long long ids, unsigned long long rows, bool bad) {
+  return bad ? __builtin_nanf("") : ids ? (float)((double)K / ((double)ids * (double)rows)) : 0.f;
+}
+
 // Workgroup b counts its share of the rows, bins blockIdx.y * kBins on.
 __global__ void __launch_bounds__(1024) k_balance_count(BalanceArgs a, int64_t share, unsigned* __restrict__ part,
-                                                        Totals* __restrict__ totals) {
+                                                        Totals* __restrict__ totals, unsigned* __restrict__ summed) {
   __shared__ unsigned bins[kBins];
   __shared__ unsigned sums[3];
   const int t = threadIdx.x, first = (int)blockIdx.y * kBins, width = min(kBins, a.K - first);
@@ -567,28 +919,13 @@ __global__ void __launch_bounds__(1024) k_balance_count(BalanceArgs a, int64_t s
   if (t < 3) sums[t] = 0;
   __syncthreads();
   const int64_t n0 = blockIdx.x * share, n1 = n0 + share < a.N ? n0 + share : a.N;
-  unsigned ids = 0, rows = 0, bad = 0;
-  for (int64_t n = n0 + t; n < n1; n += 1024) {
-    bool any = false;
-    for (int j = 0; j < a.k; ++j) {
-      const int id = id_at(a.ids, a.wide, n * a.ld_ids + j, a.K);
-      if (id < 0) continue;
-      any = true;
-      if (id >= a.K) {
-        bad = 1;
-        continue;
-      }
-      ++ids;
-      if ((unsigned)(id - first) < (unsigned)width) atomicAdd(&bins[id - first], 1u);
-    }
-    rows += any;
-  }
-  atomicAdd(&sums[0], ids);
-  atomicAdd(&sums[1], rows);
-  atomicOr(&sums[2], bad);
+  count_rows(a, n0, n1, first, width, bins, sums);
   __syncthreads();
   for (int i = t; i < width; i += 1024) part[(int64_t)blockIdx.x * a.K + first + i] = bins[i];
-  if (blockIdx.y == 0 && t == 0) totals[blockIdx.x] = Totals{sums[0], sums[1], sums[2]};
+  if (blockIdx.y == 0 && t == 0) {
+    totals[blockIdx.x] = Totals{sums[0], sums[1], sums[2]};
+    if (blockIdx.x == 0) *summed = 0;
+  }
 }
 
 // The counts of all blocks together, as integers and as floats, and the scale
@@ -599,254 +936,367 @@ __global__ void __launch_bounds__(256) k_balance_sum(BalanceArgs a, int blocks, 
   float* c = a.stats + BalanceLayout::c_at(a.N);
   if (e < a.K) {
     unsigned long long sum = 0;
+#pragma unroll 16
     for (int b = 0; b < blocks; ++b) sum += part[(int64_t)b * a.K + e];
     a.counts[e] = (int64_t)sum;
     c[e] = (float)sum;
   }
-  if (e == 0) {
+  if (blockIdx.x == 0 && threadIdx.x < 64) {
     unsigned long long ids = 0, rows = 0;
-    unsigned bad = 0;
-    for (int b = 0; b < blocks; ++b) {
-      ids += totals[b].ids;
-      rows += totals[b].rows;
-      bad |= totals[b].bad;
+    bool bad = false;
+    for (int b = threadIdx.x; b < blocks; b += 64) {
+      const Totals x = totals[b];
+      ids += x.ids;
+      rows += x.rows;
+      bad |= x.bad != 0;
     }
-    c[a.K] = bad ? __builtin_nanf("") : ids ? (float)((double)a.K / ((double)ids * (double)rows)) : 0.f;
+    for (int w = 32; w > 0; w >>= 1) {
+      ids += __shfl_xor(ids, w);
+      rows += __shfl_xor(rows, w);
+    }
+    bad = __any(bad);
+    if (threadIdx.x == 0) c[a.K] = balance_scale(a.K, ids, rows, bad);
   }
 }
 
-// Whether row n has an id (the same for all lanes of a wave).
-__device__ __forceinline__ bool counted(const BalanceArgs& a, int64_t n) {
+// Whether row n has an id, from the lanes of a group (the same for all of them).
+template <int LANES>
+__device__ __forceinline__ bool counted(const BalanceArgs& a, int64_t n, int t) {
   bool any = false;
-  for (int j = threadIdx.x & 63; j < a.k; j += 64) any |= id_at(a.ids, a.wide, n * a.ld_ids + j, a.K) >= 0;
-  return __ballot(any) != 0;
+  for (int j = t & (LANES - 1); j < a.k; j += LANES) any |= id_at(a.ids, a.wide, n * a.ld_ids + j, a.K) >= 0;
+  return lanes_any<LANES>(any);
+}
+__device__ __forceinline__ void keep(const BalanceArgs& a, int64_t n, float m, float inv, float d) {
+  a.stats[n] = m;
+  a.stats[a.N + n] = inv;
+  a.stats[2 * a.N + n] = d;
+}
+__device__ __forceinline__ float loss_weight(const BalanceArgs& a, float scale) {
+  return (a.weight_at ? *a.weight_at : a.weight) * scale;
 }
 
-template <int TYPE, int NT, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(NT) k_balance_long(BalanceArgs a, double* __restrict__ sums) {
+// Row n of up to E NT elements (K >= VEC), in the registers of NT lanes: 16, a
+// wave, or more waves of a workgroup; its d.  cs: the counts as floats.
+template <int TYPE, int NT, int E, bool STATS, bool GRAD>
+__device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* cs, float scale, int64_t n, int r, int t,
+                                             Part* parts) {
   using T = typename Elem<TYPE>::T;
+  using W = Vec<TYPE>;
+  constexpr int VEC = kVec<TYPE>, Q = E / VEC, NW = NT > 64 ? NT / 64 : 1, LANES = NT < 64 ? NT : 64;
+  const int K = a.K;
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  W v[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) v[q].load(row + W::place(q * NT + t, K));
+  const float c = kLog2e;
+  float e[E], inv, d, f = 1.f;
+  bool in = false;
+  if constexpr (STATS) in = counted<LANES>(a, n, t);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) v[q].get(e + q * VEC);
+  const auto counts = [&](int q, float (&w)[VEC]) { __builtin_memcpy(w, cs + W::place(q * NT + t, K), sizeof w); };
+  if constexpr (STATS) {
+    const Exps x(lanes_max<LANES>(max_of(e)), c);
+    x.all(e);
+    float s = 0.f, y = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float w[VEC];
+      counts(q, w);
+      if ((q + 1) * NT * VEC <= K) {  // the same for all lanes
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          s += e[q * VEC + i];
+          y += e[q * VEC + i] * w[i];
+        }
+      } else {
+        const int skip = W::skip(q * NT + t, K);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float z = i < skip ? 0.f : e[q * VEC + i];
+          s += z;
+          y += z * w[i];
+        }
+      }
+      if (Q > 4) asm volatile("" ::: "memory");  // or all counts come at once, into registers that are not there
+    }
+    const Part p = block_join<NW>(Part{x.m, lanes_sum<LANES>(s), lanes_sum<LANES>(y)}, c, parts, r * NW);
+    if constexpr (NW > 1) f = Exps(p.m, c).factor(x.m);
+    inv = in ? 1.f / p.s : 0.f;
+    d = in ? p.d * inv : 0.f;
+    if (t == 0) keep(a, n, p.m, inv, d);
+  } else {
+    inv = a.stats[a.N + n];
+    d = a.stats[2 * a.N + n];
+    Exps(a.stats[n], c).all(e);
+  }
+  if constexpr (GRAD) {
+    const float each = loss_weight(a, scale) * inv * f;
+    if (inv == 0.f) {  // not counted
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = 0.f;
+    }
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float w[VEC];
+      counts(q, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[q * VEC + i] *= (w[i] - d) * each;
+      v[q].put(e + q * VEC);
+      v[q].store(out + W::place(q * NT + t, K));
+      if (Q > 4) asm volatile("" ::: "memory");
+    }
+  }
+  return d;
+}
+
+// As k_distill_held.
+template <int TYPE, int NT, int E, int BLOCK, int WAVES, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(BLOCK, WAVES) k_balance_held(BalanceArgs a) {
+  __shared__ Part parts[16];
+  const int t = threadIdx.x % NT, r = threadIdx.x / NT;
+  const float* cs = a.stats + BalanceLayout::c_at(a.N);
+  balance_row<TYPE, NT, E, STATS, GRAD>(a, cs, cs[a.K], min((int64_t)blockIdx.x * (BLOCK / NT) + r, a.N - 1), r, t, parts);
+}
+
+// Longer rows: a workgroup to each, which reads it twice.
+template <int TYPE, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(1024, 8) k_balance_long(BalanceArgs a) {
+  using T = typename Elem<TYPE>::T;
+  using W = Vec<TYPE>;
   constexpr int VEC = kVec<TYPE>;
   __shared__ Part parts[16];
   const int t = threadIdx.x, K = a.K;
-  const int64_t N = a.N;
-  const float* cs = a.stats + BalanceLayout::c_at(N);
-  const float scale = cs[K], c = kLog2e;
-  double total = 0;
-  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
-    const T* row = static_cast<const T*>(a.z) + n * a.ld;
-    float m, inv, d;
-    if constexpr (STATS) {
-      Part p{-FLT_MAX, 0.f, 0.f};
-      const bool in = counted(a, n);
-      if (in) {
-        for (int e = t * VEC; e < K; e += NT * VEC) {
-          float v[VEC];
-          load_vec<TYPE>(row, e, K, v);
-          float m = p.m;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) m = fmaxf(m, v[i]);
-          const float f = exp2_of((p.m - m) * c);
-          float s = p.s * f, w = p.d * f;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float x = exp2_of((v[i] - m) * c);
-            s += x;
-            w += x * (e + i < K ? cs[e + i] : 0.f);
-          }
-          p = Part{m, s, w};
-        }
-        const float m = lanes_max<64>(p.m), f = exp2_of((p.m - m) * c);
-        p = Part{m, lanes_sum<64>(p.s * f), lanes_sum<64>(p.d * f)};
-        __syncthreads();
-        p = block_join<NT / 64>(p, c, parts);
-      }
-      m = p.m;
-      inv = in ? 1.f / p.s : 0.f;
-      d = in ? p.d * inv : 0.f;
-      total += d;
-      if (t == 0) {
-        a.stats[n] = m;
-        a.stats[N + n] = inv;
-        a.stats[2 * N + n] = d;
-      }
-    } else {
-      m = a.stats[n];
-      inv = a.stats[N + n];
-      d = a.stats[2 * N + n];
-    }
-    if constexpr (GRAD) {
-      T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
-      const float each = (a.weight_at ? *a.weight_at : a.weight) * scale * inv;
-      const bool in = inv != 0.f;
-      for (int e = t * VEC; e < K; e += NT * VEC) {
-        float v[VEC] = {};
-        if (in) {
-          load_vec<TYPE>(row, e, K, v);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[i] = exp2_of((v[i] - m) * c) * ((e + i < K ? cs[e + i] : 0.f) - d) * each;
-        }
-        store_vec<TYPE>(out, e, K, v);
-      }
-    }
-  }
-  if (STATS && t == 0) sums[blockIdx.x] = total;
-}
-
-// Rows of up to 16 NT elements, in the registers of NT lanes, with the counts of
-// those elements.
-template <int TYPE, int NT, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_balance_held(BalanceArgs a, double* __restrict__ sums) {
-  using T = typename Elem<TYPE>::T;
-  constexpr int VEC = kVec<TYPE>, Q = kHeld / VEC, ROWS = NT < 256 ? 256 / NT : 1, NW = NT > 64 ? NT / 64 : 1;
-  constexpr int LANES = NT < 64 ? NT : 64;
-  __shared__ Part parts[2][16];
-  __shared__ double totals[ROWS];
-  const int t = threadIdx.x % NT, r = threadIdx.x / NT, K = a.K;
-  const int64_t N = a.N;
-  const float* cs = a.stats + BalanceLayout::c_at(N);
-  const float scale = cs[K], c = kLog2e, by = GRAD ? (a.weight_at ? *a.weight_at : a.weight) * scale : 0.f;
-  float w[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int d = (i / VEC * NT + t) * VEC + i % VEC;
-    w[i] = d < K ? cs[d] : 0.f;
-  }
-  double total = 0;
-  int turn = 0;
-  for (int64_t n0 = (int64_t)blockIdx.x * ROWS; n0 < N; n0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
-    const bool there = n0 + r < N;
-    const int64_t n = there ? n0 + r : N - 1;  // lanes without a row repeat the last one and write nothing
-    const T* row = static_cast<const T*>(a.z) + n * a.ld;
-    float e[kHeld];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) load_vec<TYPE>(row, (q * NT + t) * VEC, K, e + q * VEC);
-    float inv, d, f = 1.f;
-    if constexpr (STATS) {
-      bool in = false;
-      for (int j = t & (LANES - 1); j < a.k; j += LANES) in |= id_at(a.ids, a.wide, n * a.ld_ids + j, K) >= 0;
-      in = lanes_any<LANES>(in);
-      float m = -FLT_MAX, s = 0.f, x = 0.f;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) m = fmaxf(m, e[i]);
-      m = lanes_max<LANES>(m);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        e[i] = exp2_of((e[i] - m) * c);
-        s += e[i];
-        x += e[i] * w[i];
-      }
-      const Part p = block_join<NW>(Part{m, lanes_sum<LANES>(s), lanes_sum<LANES>(x)}, c, parts[turn]);
-      f = exp2_of((m - p.m) * c);
-      inv = in ? 1.f / p.s : 0.f;
-      d = in ? p.d * inv : 0.f;
-      if (there) total += d;
-      if (t == 0 && there) {
-        a.stats[n] = p.m;
-        a.stats[N + n] = inv;
-        a.stats[2 * N + n] = d;
-      }
-    } else {
-      const float m = a.stats[n];
-      inv = a.stats[N + n];
-      d = a.stats[2 * N + n];
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) e[i] = exp2_of((e[i] - m) * c);
-    }
-    if constexpr (GRAD) {
-      const float each = by * inv * f;
-      if (inv == 0.f) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) e[i] = 0.f;
-      }
-      T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) e[i] *= (w[i] - d) * each;
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (there) store_vec<TYPE>(out, (q * NT + t) * VEC, K, e + q * VEC);
-    }
-  }
+  const int64_t n = blockIdx.x;
+  const float* cs = a.stats + BalanceLayout::c_at(a.N);
+  const float c = kLog2e;
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  float m, inv, d;
   if constexpr (STATS) {
-    if (t == 0) totals[r] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < ROWS; ++i) total += totals[i];
-      sums[blockIdx.x] = total;
+    const bool in = counted<64>(a, n, t);
+    Part p{-FLT_MAX, 0.f, 0.f};
+    for (int q = t; (q - t) * VEC < K; q += 1024) {
+      W v;
+      float e[VEC], w[VEC];
+      const int at = W::place(q, K), skip = W::skip(q, K);
+      v.load(row + at);
+      __builtin_memcpy(w, cs + at, sizeof w);
+      v.get(e);
+      const Exps x(fmaxf(max_of(e), p.m), c);
+      const float f = x.factor(p.m);
+      x.all(e);
+      p = Part{x.m, p.s * f, p.d * f};
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float z = i < skip ? 0.f : e[i];
+        p.s += z;
+        p.d += z * w[i];
+      }
+    }
+    p = block_join<16>(lanes_join<64>(p, c), c, parts, 0);
+    m = p.m;
+    inv = in ? 1.f / p.s : 0.f;
+    d = in ? p.d * inv : 0.f;
+    if (t == 0) keep(a, n, m, inv, d);
+  } else {
+    m = a.stats[n];
+    inv = a.stats[a.N + n];
+    d = a.stats[2 * a.N + n];
+  }
+  if constexpr (GRAD) {
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+    const float each = loss_weight(a, cs[K]) * inv;
+    const Exps x(m, c);
+    for (int q = t; (q - t) * VEC < K; q += 1024) {
+      W v;
+      float e[VEC], w[VEC];
+      const int at = W::place(q, K);
+      v.load(row + at);
+      __builtin_memcpy(w, cs + at, sizeof w);
+      v.get(e);
+      x.all(e);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = inv == 0.f ? 0.f : e[i] * ((w[i] - d) * each);
+      v.put(e);
+      v.store(out + at);
     }
   }
 }
 
-__global__ void __launch_bounds__(256) k_balance_loss(BalanceArgs a, int blocks, const double* __restrict__ sums) {
-  __shared__ double at[256];
-  double s = 0;
-  for (int b = threadIdx.x; b < blocks; b += 256) s += sums[b];
-  at[threadIdx.x] = s;
-  __syncthreads();
-  for (int w = 128; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) at[threadIdx.x] += at[threadIdx.x + w];
-    __syncthreads();
+// Rows shorter than a vector: a thread to each.
+template <int TYPE>
+__global__ void __launch_bounds__(256) k_balance_tiny(BalanceArgs a, bool stats) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = kVec<TYPE>;
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= a.N) return;
+  const float* cs = a.stats + BalanceLayout::c_at(a.N);
+  const T* row = static_cast<const T*>(a.z) + n * a.ld;
+  float e[VEC], w[VEC], m = -FLT_MAX, inv, d;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    e[i] = i < a.K ? Elem<TYPE>::get(row[i]) : -__builtin_inff();
+    w[i] = i < a.K ? cs[i] : 0.f;
+    m = fmaxf(m, e[i]);
   }
-  if (threadIdx.x == 0) *a.loss = (float)(at[0] * (double)a.stats[BalanceLayout::c_at(a.N) + a.K]);
+  if (!stats) m = a.stats[n];
+  Exps(m, kLog2e).all(e);
+  if (stats) {
+    bool in = false;
+    for (int j = 0; j < a.k; ++j) in |= id_at(a.ids, a.wide, n * a.ld_ids + j, a.K) >= 0;
+    float s = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      s += e[i];
+      y += e[i] * w[i];
+    }
+    inv = in ? 1.f / s : 0.f;
+    d = in ? y * inv : 0.f;
+    keep(a, n, m, inv, d);
+  } else {
+    inv = a.stats[a.N + n];
+    d = a.stats[2 * a.N + n];
+  }
+  if (a.grad) {
+    T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
+    const float each = loss_weight(a, cs[a.K]) * inv;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < a.K) out[i] = Elem<TYPE>::put(inv == 0.f ? 0.f : e[i] * ((w[i] - d) * each));
+  }
 }
 
-template <int TYPE, int NT, bool HELD>
-void balance_rows(const BalanceArgs& a, int64_t grid, double* sums, hipStream_t s) {
-  const dim3 g((unsigned)grid), b(NT < 256 ? 256 : NT);
-  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, 0, s, a, sums); };
-  if constexpr (HELD) {
-    if (!a.grad)
-      launch(k_balance_held<TYPE, NT, true, false>);
-    else if (a.loss)
-      launch(k_balance_held<TYPE, NT, true, true>);
-    else
-      launch(k_balance_held<TYPE, NT, false, true>);
-  } else {
-    if (!a.grad)
-      launch(k_balance_long<TYPE, NT, true, false>);
-    else if (a.loss)
-      launch(k_balance_long<TYPE, NT, true, true>);
-    else
-      launch(k_balance_long<TYPE, NT, false, true>);
+// A small batch in one workgroup: the counts, the rows, the loss.
+constexpr int kSmallWidth = 1024, kSmallIds = 8192, kSmallSize = 1 << 17;
+
+template <int TYPE, int NT, bool GRAD>
+__global__ void __launch_bounds__(1024) k_balance_small(BalanceArgs a) {
+  constexpr int ROWS = 1024 / NT, WIDTH = NT * 16;
+  __shared__ float cw[WIDTH];
+  __shared__ unsigned bins[WIDTH], sums[3];
+  __shared__ double totals[ROWS];
+  const int t = threadIdx.x % NT, r = threadIdx.x / NT;
+  for (int i = threadIdx.x; i < WIDTH; i += 1024) bins[i] = 0;
+  if (threadIdx.x < 3) sums[threadIdx.x] = 0;
+  __syncthreads();
+  count_rows(a, 0, a.N, 0, a.K, bins, sums);
+  __syncthreads();
+  float* cs = a.stats + BalanceLayout::c_at(a.N);
+  const float scale = balance_scale(a.K, sums[0], sums[1], sums[2] != 0);
+  for (int i = threadIdx.x; i < a.K; i += 1024) {
+    cs[i] = cw[i] = (float)bins[i];
+    a.counts[i] = bins[i];
+  }
+  if (threadIdx.x == 0) cs[a.K] = scale;
+  __syncthreads();
+  double total = 0;
+  for (int64_t n = r; n < a.N; n += ROWS) total += balance_row<TYPE, NT, 16, true, GRAD>(a, cw, scale, n, r, t, nullptr);
+  if (t == 0) totals[r] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < ROWS; ++i) total += totals[i];
+    *a.loss = (float)(total * (double)scale);
   }
 }
-template <int TYPE>
-void balance_rows_for(const BalanceArgs& a, int64_t grid, double* sums, hipStream_t s) {
-  if (a.K <= 16 * kHeld)
-    balance_rows<TYPE, 16, true>(a, grid, sums, s);
-  else if (a.K <= 64 * kHeld)
-    balance_rows<TYPE, 64, true>(a, grid, sums, s);
-  else if (a.K <= 256 * kHeld)
-    balance_rows<TYPE, 256, true>(a, grid, sums, s);
-  else if (a.K <= 512 * kHeld)
-    balance_rows<TYPE, 512, true>(a, grid, sums, s);
-  else if (a.K <= 1024 * kHeld)
-    balance_rows<TYPE, 1024, true>(a, grid, sums, s);
+
+// The loss from the rows' d: a share of them to each workgroup, whose sums the
+// last to arrive adds in their order.
+__global__ void __launch_bounds__(1024) k_balance_loss(BalanceArgs a, int64_t share, double* __restrict__ sums,
+                                                       unsigned* __restrict__ summed) {
+  __shared__ double at[16];
+  const int t = threadIdx.x;
+  const float* d = a.stats + 2 * a.N;
+  const int64_t n0 = blockIdx.x * share, n1 = n0 + share < a.N ? n0 + share : a.N;
+  double s = 0;
+#pragma unroll 4
+  for (int64_t n = n0 + t; n < n1; n += 1024) s += d[n];
+  for (int w = 32; w > 0; w >>= 1) s += __shfl_xor(s, w);
+  if ((t & 63) == 0) at[t >> 6] = s;
+  __syncthreads();
+  if (t != 0) return;
+  s = at[0];
+  for (int w = 1; w < 16; ++w) s += at[w];
+  const double scale = a.stats[BalanceLayout::c_at(a.N) + a.K];
+  if (gridDim.x > 1) {
+    __hip_atomic_store(sums + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__hip_atomic_fetch_add(summed, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 != gridDim.x) return;
+    s = 0;
+    for (unsigned b = 0; b < gridDim.x; ++b) s += __hip_atomic_load(sums + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  *a.loss = (float)(s * scale);
+}
+
+template <int TYPE, int NT, int E, int BLOCK, int WAVES>
+void balance_held(const BalanceArgs& a, hipStream_t s) {
+  constexpr int ROWS = BLOCK / NT;
+  const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS));
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(BLOCK), 0, s, a); };
+  if (!a.grad)
+    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, true, false>);
+  else if (a.loss)
+    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, true, true>);
   else
-    balance_rows<TYPE, 1024, false>(a, grid, sums, s);
+    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, false, true>);
+}
+// As distill_as.
+template <int TYPE>
+void balance_rows(const BalanceArgs& a, hipStream_t s) {
+  if (a.K < kVec<TYPE>) {
+    hipLaunchKernelGGL(k_balance_tiny<TYPE>, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, a, a.loss != nullptr);
+    return;
+  }
+  if constexpr (TYPE != kFloat) {
+    if (a.K > 256 && a.K <= 1024 && a.N >= 8192) return balance_held<TYPE, 16, 64, 256, 3>(a, s);
+    if (a.K > 4096 && a.K <= kHeldWidth && a.N >= 1024) return balance_held<TYPE, 512, 32, 512, 4>(a, s);
+  }
+  if (a.K <= 256) return balance_held<TYPE, 16, 16, 256, 7>(a, s);
+  if (a.K <= 1024) return balance_held<TYPE, 64, 16, 256, 7>(a, s);
+  if (a.K <= 4096) return balance_held<TYPE, 256, 16, 256, 6>(a, s);
+  if (a.K <= kHeldWidth) return balance_held<TYPE, 1024, 16, 1024, 4>(a, s);
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(1024), 0, s, a); };
+  if (!a.grad)
+    launch(k_balance_long<TYPE, true, false>);
+  else if (a.loss)
+    launch(k_balance_long<TYPE, true, true>);
+  else
+    launch(k_balance_long<TYPE, false, true>);
 }
 
 template <int TYPE>
 hipError_t balance_as(const BalanceArgs& a, void* workspace, hipStream_t s) {
-  const int64_t grid = row_blocks(a.N, a.K);
   if (!a.loss) {
-    balance_rows_for<TYPE>(a, grid, nullptr, s);
+    balance_rows<TYPE>(a, s);
+    return hipGetLastError();
+  }
+  if (a.K >= kVec<TYPE> && a.K <= kSmallWidth && a.N * a.k <= kSmallIds && a.N * a.K <= kSmallSize) {
+    const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, s, a); };
+    if (a.K <= 256)
+      a.grad ? launch(k_balance_small<TYPE, 16, true>) : launch(k_balance_small<TYPE, 16, false>);
+    else
+      a.grad ? launch(k_balance_small<TYPE, 64, true>) : launch(k_balance_small<TYPE, 64, false>);
     return hipGetLastError();
   }
   const int64_t blocks = count_blocks(a.N, a.K, a.k), share = (a.N + blocks - 1) / blocks;
   unsigned* part = static_cast<unsigned*>(workspace);
   Totals* totals = reinterpret_cast<Totals*>(static_cast<char*>(workspace) + 16 * ((blocks * a.K * 4 + 15) / 16));
   double* sums = reinterpret_cast<double*>(totals + blocks);
+  unsigned* summed = reinterpret_cast<unsigned*>(sums + 64);
   hipLaunchKernelGGL(k_balance_count, dim3((unsigned)blocks, (unsigned)((a.K + kBins - 1) / kBins)), dim3(1024), 0, s, a,
-                     share, part, totals);
+                     share, part, totals, summed);
   hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)((a.K + 255) / 256)), dim3(256), 0, s, a, (int)blocks, part, totals);
-  if (grid) balance_rows_for<TYPE>(a, grid, sums, s);
-  hipLaunchKernelGGL(k_balance_loss, dim3(1), dim3(256), 0, s, a, (int)grid, sums);
+  if (a.N) balance_rows<TYPE>(a, s);
+  const int last = loss_blocks(a.N);
+  hipLaunchKernelGGL(k_balance_loss, dim3((unsigned)last), dim3(1024), 0, s, a, (a.N + last - 1) / last, sums, summed);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t distill_workspace(int64_t N, int V, int k) { return 0; }
+size_t distill_workspace(int64_t N, int V, int k) {
+  const int splits = distill_splits(N, V);
+  return splits > 1 ? (size_t)N * splits * sizeof(Part) : 0;
+}
 
 hipError_t launch_distill(const DistillArgs& a, void* workspace, hipStream_t s) {
   if (a.type == kFloat) return distill_as<kFloat>(a, workspace, s);
