@@ -90,11 +90,10 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 __device__ __forceinline__ float row_max(float x) {
-  x = fmaxf(x, dpp<0xB1>(x));
-  x = fmaxf(x, dpp<0x4E>(x));
-  x = fmaxf(x, dpp<0x124>(x));
-  x = fmaxf(x, dpp<0x128>(x));
-  return x;
+  x = max3(x, x, dpp<0xB1>(x));
+  x = max3(x, x, dpp<0x4E>(x));
+  x = max3(x, x, dpp<0x124>(x));
+  return max3(x, x, dpp<0x128>(x));
 }
 // The same over the lanes of a group, 16 or a wave.  The swaps put the values of
 // the other row, the other half, beside a lane's own.
@@ -114,9 +113,9 @@ __device__ __forceinline__ float lanes_max(float x) {
   x = row_max(x);
   if constexpr (LANES == 64) {
     const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    x = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), x);
     const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+    x = max3(__uint_as_float(q[0]), __uint_as_float(q[1]), x);
   }
   return x;
 }
@@ -165,7 +164,12 @@ struct Vec {
   static __device__ __forceinline__ int place(int i, int V) { return min(i * N, V - N); }
   static __device__ __forceinline__ int skip(int i, int V) { return max(i * N - (V - N), 0); }
   __device__ __forceinline__ void load(const T* __restrict__ at) { __builtin_memcpy(&v, at, 16); }
-  __device__ __forceinline__ void store(T* __restrict__ at) const { store16<false>(at, &v); }
+  __device__ __forceinline__ void store(T* __restrict__ at, bool stream) const {
+    if (stream)
+      store16<true>(at, &v);
+    else
+      store16<false>(at, &v);
+  }
   __device__ __forceinline__ void get(float* e) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -198,16 +202,12 @@ template <int TYPE, int NT, int E>
 __device__ __forceinline__ float sum_of(const float (&e)[E], int t, int V) {
   constexpr int VEC = kVec<TYPE>;
   float s = 0.f;
+  if (V >= NT * E) {  // one decision for all lanes
 #pragma unroll
-  for (int q = 0; q < E / VEC; ++q) {
-    if ((q + 1) * NT * VEC <= V) {  // the same for all lanes
+    for (int i = 0; i < E; ++i) s += e[i];
+  } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s += e[q * VEC + i];
-    } else {
-      const int skip = Vec<TYPE>::skip(q * NT + t, V);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) s += i < skip ? 0.f : e[q * VEC + i];
-    }
+    for (int i = 0; i < E; ++i) s += i % VEC < Vec<TYPE>::skip(i / VEC * NT + t, V) ? 0.f : e[i];
   }
   return s;
 }
@@ -219,9 +219,20 @@ __device__ __forceinline__ int id_at(const void* p, bool wide, int64_t i, int mo
   return id < 0 ? -1 : id > most ? most : (int)id;
 }
 
+// The number of a thread's group of NT lanes in its workgroup: for a wave or more
+// in a scalar register, and with it a row's address.
+template <int NT>
+__device__ __forceinline__ int group_of() {
+  const int r = threadIdx.x / NT;
+  return NT >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
+}
+
 // Workgroups that the card holds at once, with `waves` to a SIMD.
 int64_t resident(int waves, int block) { return 256 * (int64_t)waves * 256 / block; }
 int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
+// Gradients that leave past the caches: those that the last of them cannot hold
+// (65536 x 1024 float32, loss and gradient by autograd: 148 us against 172).
+bool past_caches(int type, int64_t N, int V) { return N * V * (type == kFloat ? 4 : 2) >= (int64_t)256 << 20; }
 
 // ---------------------------------------------------------------------------
 // Distillation
@@ -386,7 +397,7 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
   __shared__ unsigned seen_[GRAD ? ROWS : 1][GRAD ? BITS / 32 : 1];
   __shared__ Part parts[16];
   __shared__ float ts_[ROWS];
-  const int t = threadIdx.x % NT, r = threadIdx.x / NT, V = a.V;
+  const int t = threadIdx.x % NT, r = group_of<NT>(), V = a.V;
   const bool lister = t < LANES;
   Listed<LIST>& l = lists[r];
   unsigned* const seen = seen_[GRAD ? r : 0];
@@ -446,7 +457,7 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       raw[q].put(e + q * VEC);
-      raw[q].store(out + Vec<TYPE>::place(q * NT + t, V));
+      raw[q].store(out + Vec<TYPE>::place(q * NT + t, V), a.stream);
     }
     if constexpr (NW > 1)
       __syncthreads();
@@ -535,9 +546,12 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
     Part p{-FLT_MAX, 0.f, 0.f};
     if constexpr (STATS) {
 #pragma unroll
-      for (int q = 0; q < HELD; ++q) {
-        asm volatile("" : "+v"(v[q].v));  // unpacked here, not when they arrive
-        if (q < vectors) add_vectors<TYPE, 1, 1024>(p, v + q, c, q, t, V);
+      for (int q = 0; q < HELD; q += 2) {
+        asm volatile("" : "+v"(v[q].v), "+v"(v[q + 1].v));  // unpacked here, not when they arrive
+        if (q + 1 < vectors)
+          add_vectors<TYPE, 2, 1024>(p, v + q, c, q, t, V);
+        else if (q < vectors)
+          add_vectors<TYPE, 1, 1024>(p, v + q, c, q, t, V);
       }
       for (int q = HELD; q < vectors; q += 2) {
         W w[2];
@@ -564,7 +578,7 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
 #pragma unroll
         for (int i = 0; i < VEC; ++i) e[i] = answer ? e[i] * each : ts;
         w.put(e);
-        w.store(at(out, q));
+        w.store(at(out, q), a.stream);
       };
 #pragma unroll
       for (int q = 0; q < HELD; ++q) {
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(256) k_distill_finish(DistillArgs a, int range
 #pragma unroll
         for (int j = 0; j < VEC; ++j) e[j] = answer ? e[j] * each : ts;
         v[i].put(e);
-        v[i].store(out + low + W::place((q + i) * 256 + t, V));
+        v[i].store(out + low + W::place((q + i) * 256 + t, V), a.stream);
       }
     }
     __syncthreads();
@@ -928,34 +942,41 @@ __global__ void __launch_bounds__(1024) k_balance_count(BalanceArgs a, int64_t s
   }
 }
 
-// The counts of all blocks together, as integers and as floats, and the scale
-// K / (ids rows): 0 where nothing is counted, NaN for an id out of range.
-__global__ void __launch_bounds__(256) k_balance_sum(BalanceArgs a, int blocks, const unsigned* __restrict__ part,
-                                                     const Totals* __restrict__ totals) {
-  const int e = (int)blockIdx.x * 256 + threadIdx.x;
+// The counts of all blocks together, as integers and as floats, 64 components to
+// a workgroup, whose waves share the blocks; and the scale K / (ids rows): 0
+// where nothing is counted, NaN for an id out of range.
+__global__ void __launch_bounds__(1024) k_balance_sum(BalanceArgs a, int blocks, const unsigned* __restrict__ part,
+                                                      const Totals* __restrict__ totals) {
+  __shared__ unsigned long long sums[16][64];
+  const int t = threadIdx.x & 63, w = threadIdx.x >> 6, e = (int)blockIdx.x * 64 + t;
   float* c = a.stats + BalanceLayout::c_at(a.N);
+  unsigned long long sum = 0;
   if (e < a.K) {
-    unsigned long long sum = 0;
-#pragma unroll 16
-    for (int b = 0; b < blocks; ++b) sum += part[(int64_t)b * a.K + e];
+#pragma unroll 8
+    for (int b = w; b < blocks; b += 16) sum += part[(int64_t)b * a.K + e];
+  }
+  sums[w][t] = sum;
+  __syncthreads();
+  if (w == 0 && e < a.K) {
+    for (int i = 1; i < 16; ++i) sum += sums[i][t];
     a.counts[e] = (int64_t)sum;
     c[e] = (float)sum;
   }
-  if (blockIdx.x == 0 && threadIdx.x < 64) {
+  if (blockIdx.x == 0 && w == 1) {
     unsigned long long ids = 0, rows = 0;
     bool bad = false;
-    for (int b = threadIdx.x; b < blocks; b += 64) {
+    for (int b = t; b < blocks; b += 64) {
       const Totals x = totals[b];
       ids += x.ids;
       rows += x.rows;
       bad |= x.bad != 0;
     }
-    for (int w = 32; w > 0; w >>= 1) {
-      ids += __shfl_xor(ids, w);
-      rows += __shfl_xor(rows, w);
+    for (int s = 32; s > 0; s >>= 1) {
+      ids += __shfl_xor(ids, s);
+      rows += __shfl_xor(rows, s);
     }
     bad = __any(bad);
-    if (threadIdx.x == 0) c[a.K] = balance_scale(a.K, ids, rows, bad);
+    if (t == 0) c[a.K] = balance_scale(a.K, ids, rows, bad);
   }
 }
 
@@ -975,50 +996,39 @@ __device__ __forceinline__ float loss_weight(const BalanceArgs& a, float scale) 
   return (a.weight_at ? *a.weight_at : a.weight) * scale;
 }
 
-// Row n of up to E NT elements (K >= VEC), in the registers of NT lanes: 16, a
+// Row n of up to 16 NT elements (K >= VEC), in the registers of NT lanes: 16, a
 // wave, or more waves of a workgroup; its d.  cs: the counts as floats.
-template <int TYPE, int NT, int E, bool STATS, bool GRAD>
+template <int TYPE, int NT, bool STATS, bool GRAD>
 __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* cs, float scale, int64_t n, int r, int t,
                                              Part* parts) {
   using T = typename Elem<TYPE>::T;
   using W = Vec<TYPE>;
-  constexpr int VEC = kVec<TYPE>, Q = E / VEC, NW = NT > 64 ? NT / 64 : 1, LANES = NT < 64 ? NT : 64;
+  constexpr int VEC = kVec<TYPE>, E = 16, Q = E / VEC, NW = NT > 64 ? NT / 64 : 1, LANES = NT < 64 ? NT : 64;
   const int K = a.K;
   const T* row = static_cast<const T*>(a.z) + n * a.ld;
   W v[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) v[q].load(row + W::place(q * NT + t, K));
+  float w[E];  // the counts
+#pragma unroll
+  for (int q = 0; q < Q; ++q) __builtin_memcpy(w + q * VEC, cs + W::place(q * NT + t, K), VEC * 4);
   const float c = kLog2e;
   float e[E], inv, d, f = 1.f;
   bool in = false;
   if constexpr (STATS) in = counted<LANES>(a, n, t);
 #pragma unroll
   for (int q = 0; q < Q; ++q) v[q].get(e + q * VEC);
-  const auto counts = [&](int q, float (&w)[VEC]) { __builtin_memcpy(w, cs + W::place(q * NT + t, K), sizeof w); };
   if constexpr (STATS) {
     const Exps x(lanes_max<LANES>(max_of(e)), c);
     x.all(e);
-    float s = 0.f, y = 0.f;
+    const float s = sum_of<TYPE, NT>(e, t, K);
+    float y = 0.f;
+    if (K >= NT * E) {  // one decision for all lanes
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      float w[VEC];
-      counts(q, w);
-      if ((q + 1) * NT * VEC <= K) {  // the same for all lanes
+      for (int i = 0; i < E; ++i) y += e[i] * w[i];
+    } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          s += e[q * VEC + i];
-          y += e[q * VEC + i] * w[i];
-        }
-      } else {
-        const int skip = W::skip(q * NT + t, K);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float z = i < skip ? 0.f : e[q * VEC + i];
-          s += z;
-          y += z * w[i];
-        }
-      }
-      if (Q > 4) asm volatile("" ::: "memory");  // or all counts come at once, into registers that are not there
+      for (int i = 0; i < E; ++i) y += i % VEC < W::skip(i / VEC * NT + t, K) ? 0.f : e[i] * w[i];
     }
     const Part p = block_join<NW>(Part{x.m, lanes_sum<LANES>(s), lanes_sum<LANES>(y)}, c, parts, r * NW);
     if constexpr (NW > 1) f = Exps(p.m, c).factor(x.m);
@@ -1039,25 +1049,22 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* 
     T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      float w[VEC];
-      counts(q, w);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) e[q * VEC + i] *= (w[i] - d) * each;
+      for (int i = 0; i < VEC; ++i) e[q * VEC + i] *= (w[q * VEC + i] - d) * each;
       v[q].put(e + q * VEC);
-      v[q].store(out + W::place(q * NT + t, K));
-      if (Q > 4) asm volatile("" ::: "memory");
+      v[q].store(out + W::place(q * NT + t, K), a.stream);
     }
   }
   return d;
 }
 
 // As k_distill_held.
-template <int TYPE, int NT, int E, int BLOCK, int WAVES, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(BLOCK, WAVES) k_balance_held(BalanceArgs a) {
+template <int TYPE, int NT, int BLOCK, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(BLOCK) k_balance_held(BalanceArgs a) {
   __shared__ Part parts[16];
-  const int t = threadIdx.x % NT, r = threadIdx.x / NT;
+  const int t = threadIdx.x % NT, r = group_of<NT>();
   const float* cs = a.stats + BalanceLayout::c_at(a.N);
-  balance_row<TYPE, NT, E, STATS, GRAD>(a, cs, cs[a.K], min((int64_t)blockIdx.x * (BLOCK / NT) + r, a.N - 1), r, t, parts);
+  balance_row<TYPE, NT, STATS, GRAD>(a, cs, cs[a.K], min((int64_t)blockIdx.x * (BLOCK / NT) + r, a.N - 1), r, t, parts);
 }
 
 // Longer rows: a workgroup to each, which reads it twice.
@@ -1119,7 +1126,7 @@ __global__ void __launch_bounds__(1024, 8) k_balance_long(BalanceArgs a) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) e[i] = inv == 0.f ? 0.f : e[i] * ((w[i] - d) * each);
       v.put(e);
-      v.store(out + at);
+      v.store(out + at, a.stream);
     }
   }
 }
@@ -1176,7 +1183,7 @@ __global__ void __launch_bounds__(1024) k_balance_small(BalanceArgs a) {
   __shared__ float cw[WIDTH];
   __shared__ unsigned bins[WIDTH], sums[3];
   __shared__ double totals[ROWS];
-  const int t = threadIdx.x % NT, r = threadIdx.x / NT;
+  const int t = threadIdx.x % NT, r = group_of<NT>();
   for (int i = threadIdx.x; i < WIDTH; i += 1024) bins[i] = 0;
   if (threadIdx.x < 3) sums[threadIdx.x] = 0;
   __syncthreads();
@@ -1191,7 +1198,7 @@ __global__ void __launch_bounds__(1024) k_balance_small(BalanceArgs a) {
   if (threadIdx.x == 0) cs[a.K] = scale;
   __syncthreads();
   double total = 0;
-  for (int64_t n = r; n < a.N; n += ROWS) total += balance_row<TYPE, NT, 16, true, GRAD>(a, cw, scale, n, r, t, nullptr);
+  for (int64_t n = r; n < a.N; n += ROWS) total += balance_row<TYPE, NT, true, GRAD>(a, cw, scale, n, r, t, nullptr);
   if (t == 0) totals[r] = total;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -1227,33 +1234,28 @@ __global__ void __launch_bounds__(1024) k_balance_loss(BalanceArgs a, int64_t sh
   *a.loss = (float)(s * scale);
 }
 
-template <int TYPE, int NT, int E, int BLOCK, int WAVES>
+template <int TYPE, int NT>
 void balance_held(const BalanceArgs& a, hipStream_t s) {
-  constexpr int ROWS = BLOCK / NT;
+  constexpr int BLOCK = NT < 256 ? 256 : NT, ROWS = BLOCK / NT;
   const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS));
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(BLOCK), 0, s, a); };
   if (!a.grad)
-    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, true, false>);
+    launch(k_balance_held<TYPE, NT, BLOCK, true, false>);
   else if (a.loss)
-    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, true, true>);
+    launch(k_balance_held<TYPE, NT, BLOCK, true, true>);
   else
-    launch(k_balance_held<TYPE, NT, E, BLOCK, WAVES, false, true>);
+    launch(k_balance_held<TYPE, NT, BLOCK, false, true>);
 }
-// As distill_as.
 template <int TYPE>
 void balance_rows(const BalanceArgs& a, hipStream_t s) {
   if (a.K < kVec<TYPE>) {
     hipLaunchKernelGGL(k_balance_tiny<TYPE>, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, a, a.loss != nullptr);
     return;
   }
-  if constexpr (TYPE != kFloat) {
-    if (a.K > 256 && a.K <= 1024 && a.N >= 8192) return balance_held<TYPE, 16, 64, 256, 3>(a, s);
-    if (a.K > 4096 && a.K <= kHeldWidth && a.N >= 1024) return balance_held<TYPE, 512, 32, 512, 4>(a, s);
-  }
-  if (a.K <= 256) return balance_held<TYPE, 16, 16, 256, 7>(a, s);
-  if (a.K <= 1024) return balance_held<TYPE, 64, 16, 256, 7>(a, s);
-  if (a.K <= 4096) return balance_held<TYPE, 256, 16, 256, 6>(a, s);
-  if (a.K <= kHeldWidth) return balance_held<TYPE, 1024, 16, 1024, 4>(a, s);
+  if (a.K <= 256) return balance_held<TYPE, 16>(a, s);
+  if (a.K <= 1024) return balance_held<TYPE, 64>(a, s);
+  if (a.K <= 4096) return balance_held<TYPE, 256>(a, s);
+  if (a.K <= kHeldWidth) return balance_held<TYPE, 1024>(a, s);
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(1024), 0, s, a); };
   if (!a.grad)
     launch(k_balance_long<TYPE, true, false>);
@@ -1284,7 +1286,7 @@ hipError_t balance_as(const BalanceArgs& a, void* workspace, hipStream_t s) {
   unsigned* summed = reinterpret_cast<unsigned*>(sums + 64);
   hipLaunchKernelGGL(k_balance_count, dim3((unsigned)blocks, (unsigned)((a.K + kBins - 1) / kBins)), dim3(1024), 0, s, a,
                      share, part, totals, summed);
-  hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)((a.K + 255) / 256)), dim3(256), 0, s, a, (int)blocks, part, totals);
+  hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)((a.K + 63) / 64)), dim3(1024), 0, s, a, (int)blocks, part, totals);
   if (a.N) balance_rows<TYPE>(a, s);
   const int last = loss_blocks(a.N);
   hipLaunchKernelGGL(k_balance_loss, dim3((unsigned)last), dim3(1024), 0, s, a, (a.N + last - 1) / last, sums, summed);
@@ -1298,13 +1300,17 @@ size_t distill_workspace(int64_t N, int V, int k) {
   return splits > 1 ? (size_t)N * splits * sizeof(Part) : 0;
 }
 
-hipError_t launch_distill(const DistillArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_distill(const DistillArgs& given, void* workspace, hipStream_t s) {
+  DistillArgs a = given;
+  a.stream = past_caches(a.type, a.N, a.V);
   if (a.type == kFloat) return distill_as<kFloat>(a, workspace, s);
   if (a.type == kBfloat) return distill_as<kBfloat>(a, workspace, s);
   return distill_as<kHalf>(a, workspace, s);
 }
 
-hipError_t launch_balance(const BalanceArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_balance(const BalanceArgs& given, void* workspace, hipStream_t s) {
+  BalanceArgs a = given;
+  a.stream = past_caches(a.type, a.N, a.K);
   if (a.type == kFloat) return balance_as<kFloat>(a, workspace, s);
   if (a.type == kBfloat) return balance_as<kBfloat>(a, workspace, s);
   return balance_as<kHalf>(a, workspace, s);

@@ -97,6 +97,7 @@ struct DistillArgs {
   float weight;
   void* grad;
   int64_t ld_grad;
+  bool stream;  // set by the launcher
 };
 size_t distill_workspace(int64_t N, int V, int k);
 hipError_t launch_distill(const DistillArgs& a, void* workspace, hipStream_t s);
@@ -118,6 +119,7 @@ struct BalanceArgs {
   float weight;
   void* grad;
   int64_t ld_grad;
+  bool stream;  // set by the launcher
 };
 size_t balance_stats(int64_t N, int K);
 size_t balance_workspace(int64_t N, int K, int k);
