@@ -213,8 +213,9 @@ __device__ __forceinline__ void lds_dma4(unsigned off, const uint8_t* base, unsi
 
 // Large products: WM x WN waves, each with TM x TN blocks of 32 x 32.  A step
 // is one group (128 bytes of a row); two LDS buffers are filled by LDS DMA, one
-// while the other is read.  Chunk c (16 bytes) of row r sits at slot c ^ (r & 7)
-// of its 128 bytes, so 8 consecutive rows' reads of one chunk touch all banks.
+// while the other is read.  Chunk c (16 bytes) of row r sits at slot
+// c ^ (r / 2 & 7) of its 128 bytes: two rows span the 64 banks, and the reads of
+// one chunk from 16 consecutive rows touch each once.
 // Half h of a step takes chunks 4 h + 2 g and the next for lane half g: any
 // assignment serves as long as both sides share it.  Scale words come by DMA
 // for 4 steps at a time.
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(64 * WM* WN, 2)
   for (int i = 0; i < OPS; ++i) {
     const int r = (w * OPS + i) * 8 + (lane >> 3);
     voff[i] = (r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)lda : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldb) +
-              ((lane & 7) ^ (r & 7)) * 16;
+              ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SOPS; ++i) {
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(64 * WM* WN, 2)
   f16v acc[TM][TN] = {};
   i4 fa[2][2], fb[2][TN][2];  // A: this block's 32 bytes and the next one's; B: this half's and the next one's
   unsigned qa[TM], qb[TN];
-  const int c0 = ((2 * g) ^ (r32 & 7)) * 16, c1 = ((2 * g + 1) ^ (r32 & 7)) * 16;  // chunks of half 0; half 1: ^ 64
+  // chunks of half 0; half 1: ^ 64
+  const int c0 = ((2 * g) ^ ((r32 >> 1) & 7)) * 16, c1 = ((2 * g + 1) ^ ((r32 >> 1) & 7)) * 16;
   auto read_a = [&](int k, int h, int i) {
     const uint8_t* p = lds + (k & 1) * STEP + ((wm * TM + i) * 32 + r32) * 128;
     fa[i & 1][0] = *reinterpret_cast<const i4*>(p + (c0 ^ (64 * h)));
@@ -564,6 +566,120 @@ __global__ void __launch_bounds__(64 * byte_waves(MT))
   }
 }
 
+// One row of A, of at least 8 groups: no matrix instruction, whose lanes would
+// want 64 bytes each of 16 rows of B; a wave reads 1024 bytes of one row at a
+// time (8 groups, 16 bytes to a lane), two rows and four times 8 groups at once
+// (the pattern reaches 6.6 TB/s where the other reaches 5.1).  The waves of a
+// workgroup quantise 8 groups of A each, 8 lanes to a block, while their rows of
+// B are on their way, and share the values, in bfloat16, through LDS.
+constexpr int kOneRows = 2, kOneSteps = 4;  // steps: waves of a workgroup
+
+// The largest of 8 neighbouring lanes, in all of them.
+__device__ __forceinline__ unsigned max8(unsigned m) {
+  m = max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));
+  m = max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));
+  return max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));  // the other half's, mirrored
+}
+
+template <int AT, int CT>
+__global__ void __launch_bounds__(64 * kOneSteps)
+    k_byte_one(const void* __restrict__ A, const uint8_t* __restrict__ as, const uint8_t* __restrict__ B, int64_t ldb,
+               const uint8_t* __restrict__ bs, int64_t ldbs, int N, int D, int G, const float* __restrict__ bias,
+               typename Elem<CT>::T* __restrict__ C) {
+  __shared__ i4 held[kOneSteps][2][64];  // a lane's 16 values of each step
+  const int lane = threadIdx.x & 63, sub = lane >> 3, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  // A's values of groups k .. k + 31, 8 of them each wave's; zeros behind the last
+  const auto hold = [&](int k) {
+    const int g = k + 8 * w + sub, d = g * 128 + (lane & 7) * 16;
+    i4 c = {0, 0, 0, 0};
+    float sc = 1.f;
+    if constexpr (AT == kByte) {
+      if (g < G) {
+        c = *reinterpret_cast<const i4*>(static_cast<const uint8_t*>(A) + d);
+        sc = scale_value(as[g]);
+      }
+    } else {
+      const typename Elem<AT>::T* row = static_cast<const typename Elem<AT>::T*>(A);
+      float v[2][8];
+      load8<AT>(row, d, D, v[0]);
+      load8<AT>(row, d + 8, D, v[1]);
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max_mag(m, v[i >> 3][i & 7]);
+      const unsigned e = byte_scale_of(max8(m));
+      const uint2 lo = byte_codes8(v[0], e), hi = byte_codes8(v[1], e);
+      c = i4{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+      sc = scale_value(e);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) held[w][i][lane] = __builtin_bit_cast(i4, bfloats(c[2 * i], c[2 * i + 1], sc));
+  };
+  const bool whole = G <= 8 * kOneSteps;  // A is held once
+  bool first = true;
+  for (int n0 = (int)blockIdx.x * (kOneSteps * kOneRows); n0 < N; n0 += (int)gridDim.x * (kOneSteps * kOneRows)) {
+    const int n = n0 + w * kOneRows;
+    float acc[kOneRows] = {};
+    for (int k = 0; k < G; k += 8 * kOneSteps) {
+      // 16 bytes of each row and step, the rows' scale words; rows and groups behind the last repeat it
+      i4 b[kOneRows][kOneSteps];
+      unsigned q[kOneRows][2 * kOneSteps];
+#pragma unroll
+      for (int r = 0; r < kOneRows; ++r) {
+        const int64_t at = min(n + r, N - 1);
+#pragma unroll
+        for (int s = 0; s < kOneSteps; ++s)
+          b[r][s] = *reinterpret_cast<const i4*>(B + at * ldb + min(k + 8 * s + sub, G - 1) * 128 + (lane & 7) * 16);
+        const unsigned* words = reinterpret_cast<const unsigned*>(bs + at * ldbs);
+#pragma unroll
+        for (int s = 0; s < 2 * kOneSteps; ++s) q[r][s] = words[min((k >> 2) + s, (G - 1) >> 2)];
+      }
+      if (first || !whole) {
+        if (!first) __syncthreads();
+        hold(k);
+        __syncthreads();
+        first = false;
+      }
+#pragma unroll
+      for (int s = 0; s < kOneSteps; ++s) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned pair = (unsigned)held[s][i >> 2][lane][i & 3];
+          x[2 * i] = __uint_as_float(pair << 16);
+          x[2 * i + 1] = __uint_as_float(pair & 0xffff0000u);
+        }
+#pragma unroll
+        for (int r = 0; r < kOneRows; ++r) {
+          const float sc = scale_value(((sub < 4 ? q[r][2 * s] : q[r][2 * s + 1]) >> (8 * (sub & 3))) & 255u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f2 y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)b[r][s][i], sc, false);
+            const f2 z = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((unsigned)b[r][s][i], sc, true);
+            acc[r] = fmaf(y.x, x[4 * i], acc[r]);
+            acc[r] = fmaf(y.y, x[4 * i + 1], acc[r]);
+            acc[r] = fmaf(z.x, x[4 * i + 2], acc[r]);
+            acc[r] = fmaf(z.y, x[4 * i + 3], acc[r]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kOneRows; ++r) {
+      float x = acc[r];
+      x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0xB1, 0xF, 0xF, true));
+      x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4E, 0xF, 0xF, true));
+      x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xF, 0xF, true));
+      x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF, 0xF, true));
+      const auto u = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+      x = __uint_as_float(u[0]) + __uint_as_float(u[1]);
+      const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+      acc[r] = __uint_as_float(z[0]) + __uint_as_float(z[1]);
+    }
+    const float x = lane == 0 ? acc[0] : acc[1];
+    if (lane < kOneRows && n + lane < N) C[n + lane] = Elem<CT>::put(bias ? x + bias[n + lane] : x);
+  }
+}
+
 // Waves of a workgroup: each takes at least 4 groups.
 static int byte_waves_for(int G, int most) {
   const int w = (G + 3) / 4;
@@ -571,7 +687,9 @@ static int byte_waves_for(int G, int most) {
 }
 // Rows that are not in 8 bits are quantised inside the few-rows kernel where
 // that is one step for each of its threads.
+constexpr int kOneGroups = 8;  // groups that one row of A has at least to be k_byte_one's
 static bool byte_inside(int a_type, int64_t M, int G) {
+  if (M == 1 && G >= kOneGroups) return true;
   return a_type != kByte && M <= 16 && M * 16 * G <= 64 * byte_waves_for(G, byte_waves(1));
 }
 
@@ -593,8 +711,18 @@ static void byte_few_as(const ByteProduct& p, int G, hipStream_t s) {
                      dim3(64 * waves), held, s, p.A, p.lda, p.as, p.ldas, (int)p.M, p.B, p.ldb, p.bs, p.ldbs, (int)p.N,
                      p.D, G, share, p.bias, (typename Elem<CT>::T*)p.C, p.ldc);
 }
+template <int AT, int CT>
+static void byte_one(const ByteProduct& p, int G, hipStream_t s) {
+  constexpr int ROWS = kOneSteps * kOneRows;
+  const int64_t need = (p.N + ROWS - 1) / ROWS;
+  hipLaunchKernelGGL((k_byte_one<AT, CT>), dim3((unsigned)(need < (1 << 20) ? need : (1 << 20))), dim3(64 * kOneSteps), 0, s,
+                     p.A, p.as, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, p.bias, (typename Elem<CT>::T*)p.C);
+}
 template <int AT, int MT, int CT>
 static void byte_few(const ByteProduct& p, int G, hipStream_t s) {
+  if constexpr (MT == 1) {
+    if (p.M == 1 && G >= kOneGroups) return byte_one<AT, CT>(p, G, s);
+  }
   if (p.N <= 16 * 512)
     byte_few_as<AT, MT, 1, CT>(p, G, s);
   else
