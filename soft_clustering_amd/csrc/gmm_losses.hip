@@ -153,8 +153,9 @@ __device__ __forceinline__ Part block_join(Part p, float c, Part* at, int w0) {
 // Vectors of a row are numbered by lanes; vector i holds elements VEC i on.  One
 // that would reach behind the row's end (of V >= VEC elements) lies at its end
 // instead: its first `skip` elements are others' as well (all, where it would
-// lie behind it altogether).  They have no part in sums; in maxima and results
-// they do no harm, as all who have an element find and write the same for it.
+// lie behind it altogether).  They have no part in sums; in maxima they do no
+// harm, and in results none where all who have an element find the same for it:
+// lanes that compare with the same largest logit.
 template <int TYPE>
 struct Vec {
   using T = typename Elem<TYPE>::T;
@@ -169,6 +170,16 @@ struct Vec {
       store16<true>(at, &v);
     else
       store16<false>(at, &v);
+  }
+  // Vector i of a row: its own elements alone.
+  __device__ __forceinline__ void store_own(T* __restrict__ row, int i, int V, bool stream) const {
+    const int none = skip(i, V);
+    if (none == 0) return store(row + i * N, stream);
+    T e[N];
+    __builtin_memcpy(e, &v, 16);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j >= none) row[V - N + j] = e[j];
   }
   __device__ __forceinline__ void get(float* e) const {
 #pragma unroll
@@ -227,6 +238,14 @@ __device__ __forceinline__ int group_of() {
   return NT >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
 }
 
+// The grid of a launch with a workgroup for each row or few rows: over two
+// dimensions, as one holds fewer than 2^32 threads.  A workgroup's number in it.
+constexpr int64_t kGridWidth = 1 << 21;
+dim3 row_grid(int64_t blocks) {
+  return blocks <= kGridWidth ? dim3((unsigned)blocks) : dim3((unsigned)kGridWidth, (unsigned)((blocks + kGridWidth - 1) / kGridWidth));
+}
+__device__ __forceinline__ int64_t block_in_grid() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Workgroups that the card holds at once, with `waves` to a SIMD.
 int64_t resident(int waves, int block) { return 256 * (int64_t)waves * 256 / block; }
 int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -247,6 +266,7 @@ struct Listed {
   int id[LIST];   // -1 where nothing is listed
   float x[LIST];  // exponents of the teacher's logits
   float z[LIST];  // the row's own logits there
+  float w[LIST];  // for the gradient: exponentials of the places of an id together at its first, negative at the others
 };
 
 // One place of the list of row n, as it is stored: nothing is done with the
@@ -335,37 +355,52 @@ __device__ __forceinline__ float list_loss(const DistillArgs& a, int t, const Ex
 // The gradient at the listed places from `low` to `high`, over what the row's
 // lanes have written there (before a barrier, or in the same wave): each q_id -
 // sum of its p.  `seen` has a bit for each id, by its low bits, all clear: an id
-// listed twice (or two with the same bits) is found by its bit, and then takes
-// the sum over its places, in their order, from the first of them.
+// that finds its bit set may be listed twice, and the lanes look together for its
+// places, of which the first takes the sum (2048 rows of 131072 with 1024 listed,
+// some dozen of which share a bit or are listed twice: 721 us; every lane
+// looking through the list for its own: 8952 us).
 template <int TYPE, int LANES, int LIST, int BITS>
-__device__ __forceinline__ void list_gradient(const DistillArgs& a, int t, const Exps& x, const Listed<LIST>& l, float ts,
+__device__ __forceinline__ void list_gradient(const DistillArgs& a, int t, const Exps& x, Listed<LIST>& l, float ts,
                                               float each, float by, typename Elem<TYPE>::T* out, unsigned* seen,
                                               int low, int high) {
-  bool twice = false;
-  for (int j = t; j < a.k; j += LANES) {
+  static_assert(LIST <= 32 * LANES, "a bit for each place of a lane");
+  unsigned again = 0;
+  for (int j = t, q = 0; j < a.k; j += LANES, ++q) {
     const int id = l.id[j];
     const unsigned bit = 1u << (id & 31);
-    if (id >= low && id < high) twice |= (atomicOr(&seen[(id & (BITS - 1)) >> 5], bit) & bit) != 0;
+    l.w[j] = exp2_of(l.x[j]);
+    if (id >= low && id < high && (atomicOr(&seen[(id & (BITS - 1)) >> 5], bit) & bit) != 0) again |= 1u << q;
   }
-  twice = lanes_any<LANES>(twice);
   wave_sync();
+  if (lanes_any<LANES>(again != 0)) {
+    for (int q = 0; q * LANES < a.k; ++q) {
+      u64 those = __ballot((again >> q) & 1);
+      if constexpr (LANES < 64) those = (those >> (threadIdx.x & 48)) & 0xffff;
+      for (; those != 0; those &= those - 1) {
+        const int j = q * LANES + __builtin_ctzll(those), id = l.id[j];
+        if (l.w[j] < 0.f) continue;  // found with another place
+        float sum = 0.f, last = -FLT_MAX;
+        for (int i = t; i < a.k; i += LANES)
+          if (l.id[i] == id) {
+            sum += l.w[i];
+            last = fmaxf(last, (float)-i);
+          }
+        sum = lanes_sum<LANES>(sum);
+        const int first = -(int)lanes_max<LANES>(last);
+        wave_sync();
+        for (int i = t; i < a.k; i += LANES)
+          if (l.id[i] == id) l.w[i] = i == first ? sum : -1.f;
+        wave_sync();
+      }
+    }
+  }
   const float part = by / ts;
   for (int j = t; j < a.k; j += LANES) {
     const int id = l.id[j];
     if (id < low || id >= high) continue;
     seen[(id & (BITS - 1)) >> 5] = 0;
-    float w = exp2_of(l.x[j]);
-    if (twice) {
-      w = 0.f;
-      bool first = true;
-      for (int i = 0; i < a.k; ++i)
-        if (l.id[i] == id) {
-          first &= i >= j;
-          w += exp2_of(l.x[i]);
-        }
-      if (!first) continue;
-    }
-    out[id] = Elem<TYPE>::put(x.of(l.z[j]) * each - w * part);
+    const float w = l.w[j];
+    if (w >= 0.f) out[id] = Elem<TYPE>::put(x.of(l.z[j]) * each - w * part);
   }
 }
 
@@ -401,7 +436,7 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
   const bool lister = t < LANES;
   Listed<LIST>& l = lists[r];
   unsigned* const seen = seen_[GRAD ? r : 0];
-  const int64_t n = min((int64_t)blockIdx.x * ROWS + r, a.N - 1);
+  const int64_t n = min(block_in_grid() * ROWS + r, a.N - 1);
   const T* row = static_cast<const T*>(a.z) + n * a.ld;
   Place first{};
   if (lister) first.load(a, n, t);
@@ -457,7 +492,10 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       raw[q].put(e + q * VEC);
-      raw[q].store(out + Vec<TYPE>::place(q * NT + t, V), a.stream);
+      if (NW > 1 && V < NT * E)  // a row's waves compare with the largest of each
+        raw[q].store_own(out, q * NT + t, V, a.stream);
+      else
+        raw[q].store(out + Vec<TYPE>::place(q * NT + t, V), a.stream);
     }
     if constexpr (NW > 1)
       __syncthreads();
@@ -607,7 +645,9 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
   }
 }
 
-// Longer rows, few: divided over workgroups of 256, `range` elements to each.
+// Longer rows, few: divided over workgroups of 256, `range` elements to each,
+// what is left to the last (at least a vector, so that none reaches into the
+// part before, whose listed places are another workgroup's).
 // First the parts' numbers, then, from all of a row's, the loss (by its first
 // workgroup) and the gradient of each part, which reads its elements again.
 template <int TYPE>
@@ -616,7 +656,8 @@ __global__ void __launch_bounds__(256) k_distill_parts(DistillArgs a, int range,
   using W = Vec<TYPE>;
   constexpr int VEC = kVec<TYPE>;
   __shared__ Part parts[16];
-  const int t = threadIdx.x, low = (int)blockIdx.x * range, V = min(range, a.V - low);
+  const int t = threadIdx.x, low = (int)blockIdx.x * range,
+            V = blockIdx.x + 1 < gridDim.x ? range : a.V - low;
   const float c = kLog2e / a.temperature;
   const T* row = static_cast<const T*>(a.z) + (int64_t)blockIdx.y * a.ld + low;
   Part p{-FLT_MAX, 0.f, 0.f};
@@ -638,7 +679,8 @@ __global__ void __launch_bounds__(256) k_distill_finish(DistillArgs a, int range
   __shared__ Listed<kList> l;
   __shared__ unsigned seen[GRAD ? kSeenBits / 32 : 1];
   __shared__ float ts_;
-  const int t = threadIdx.x, low = (int)blockIdx.x * range, V = min(range, a.V - low);
+  const int t = threadIdx.x, low = (int)blockIdx.x * range,
+            V = blockIdx.x + 1 < gridDim.x ? range : a.V - low;
   const int64_t n = blockIdx.y;
   const float c = kLog2e / a.temperature;
   const T* row = static_cast<const T*>(a.z) + n * a.ld;
@@ -770,7 +812,7 @@ int distill_splits(int64_t N, int V) {
 template <int TYPE, int NT, int E, int BLOCK, int WAVES>
 void distill_held(const DistillArgs& a, hipStream_t s) {
   constexpr int ROWS = BLOCK / NT;
-  const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS));
+  const dim3 grid = row_grid((a.N + ROWS - 1) / ROWS);
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(BLOCK), 0, s, a); };
   if (!a.grad)
     launch(k_distill_held<TYPE, NT, E, BLOCK, WAVES, true, false>);
@@ -797,7 +839,7 @@ hipError_t distill_long(const DistillArgs& a, void* workspace, hipStream_t s) {
     return hipGetLastError();
   }
   constexpr int STEP = 256 * kVec<TYPE>;
-  const int range = ((a.V + splits - 1) / splits + STEP - 1) / STEP * STEP, parts = (a.V + range - 1) / range;
+  const int range = ((a.V + splits - 1) / splits + STEP - 1) / STEP * STEP, parts = (a.V - kVec<TYPE>) / range + 1;
   const dim3 all((unsigned)parts, (unsigned)a.N), one(1, (unsigned)a.N), block(256);
   Part* in = static_cast<Part*>(workspace);
   if (a.losses) {
@@ -1052,7 +1094,10 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* 
 #pragma unroll
       for (int i = 0; i < VEC; ++i) e[q * VEC + i] *= (w[q * VEC + i] - d) * each;
       v[q].put(e + q * VEC);
-      v[q].store(out + W::place(q * NT + t, K), a.stream);
+      if (NW > 1 && K < NT * E)  // as k_distill_held
+        v[q].store_own(out, q * NT + t, K, a.stream);
+      else
+        v[q].store(out + W::place(q * NT + t, K), a.stream);
     }
   }
   return d;
@@ -1064,7 +1109,7 @@ __global__ void __launch_bounds__(BLOCK) k_balance_held(BalanceArgs a) {
   __shared__ Part parts[16];
   const int t = threadIdx.x % NT, r = group_of<NT>();
   const float* cs = a.stats + BalanceLayout::c_at(a.N);
-  balance_row<TYPE, NT, STATS, GRAD>(a, cs, cs[a.K], min((int64_t)blockIdx.x * (BLOCK / NT) + r, a.N - 1), r, t, parts);
+  balance_row<TYPE, NT, STATS, GRAD>(a, cs, cs[a.K], min(block_in_grid() * (BLOCK / NT) + r, a.N - 1), r, t, parts);
 }
 
 // Longer rows: a workgroup to each, which reads it twice.
@@ -1075,7 +1120,7 @@ __global__ void __launch_bounds__(1024, 8) k_balance_long(BalanceArgs a) {
   constexpr int VEC = kVec<TYPE>;
   __shared__ Part parts[16];
   const int t = threadIdx.x, K = a.K;
-  const int64_t n = blockIdx.x;
+  const int64_t n = min(block_in_grid(), a.N - 1);  // behind the last: that row again
   const float* cs = a.stats + BalanceLayout::c_at(a.N);
   const float c = kLog2e;
   const T* row = static_cast<const T*>(a.z) + n * a.ld;
@@ -1237,7 +1282,7 @@ __global__ void __launch_bounds__(1024) k_balance_loss(BalanceArgs a, int64_t sh
 template <int TYPE, int NT>
 void balance_held(const BalanceArgs& a, hipStream_t s) {
   constexpr int BLOCK = NT < 256 ? 256 : NT, ROWS = BLOCK / NT;
-  const dim3 grid((unsigned)((a.N + ROWS - 1) / ROWS));
+  const dim3 grid = row_grid((a.N + ROWS - 1) / ROWS);
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(BLOCK), 0, s, a); };
   if (!a.grad)
     launch(k_balance_held<TYPE, NT, BLOCK, true, false>);
@@ -1256,7 +1301,7 @@ void balance_rows(const BalanceArgs& a, hipStream_t s) {
   if (a.K <= 1024) return balance_held<TYPE, 64>(a, s);
   if (a.K <= 4096) return balance_held<TYPE, 256>(a, s);
   if (a.K <= kHeldWidth) return balance_held<TYPE, 1024>(a, s);
-  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(1024), 0, s, a); };
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, row_grid(a.N), dim3(1024), 0, s, a); };
   if (!a.grad)
     launch(k_balance_long<TYPE, true, false>);
   else if (a.loss)

@@ -61,12 +61,21 @@ __device__ __forceinline__ unsigned max_mag(unsigned m, float x) {
 
 // 8 values of a row from element d on; those past D are zero.  The vector
 // form needs only the alignment of one element (unaligned global access).
-template <int TYPE>
+// STREAM: past the caches, for what they cannot hold.
+template <int TYPE, bool STREAM = false>
 __device__ __forceinline__ void load8(const typename Elem<TYPE>::T* __restrict__ row, int d, int D, float (&v)[8]) {
   using T = typename Elem<TYPE>::T;
   if (d + 8 <= D) {
     T t[8];
-    __builtin_memcpy(t, row + d, sizeof t);
+    if constexpr (STREAM) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof t; i += 16) {
+        const i4 q = __builtin_nontemporal_load(reinterpret_cast<const i4u*>(reinterpret_cast<const char*>(row + d) + i));
+        __builtin_memcpy(reinterpret_cast<char*>(t) + i, &q, 16);
+      }
+    } else {
+      __builtin_memcpy(t, row + d, sizeof t);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = Elem<TYPE>::get(t[i]);
   } else {

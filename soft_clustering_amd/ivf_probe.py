@@ -10,7 +10,7 @@ for m lists per vector (the DCO identity of Section 4.5).  This module is
 that evaluation, written with torch tensor operations on whatever device the
 tensors live on (the GPU in the benchmark); it is not part of the EM path,
 whose work all runs in the HIP library.  compressed_topk scans all rows in 4
-bits with the library's product and ranks a shortlist exactly.
+or 8 bits with the library's products and ranks a shortlist exactly.
 
 Readings (the pages leave them open):
   * probing: squared L2 distance from the query to each mean mu_k, computed
@@ -87,19 +87,21 @@ def exact_topk(Q: torch.Tensor, X: torch.Tensor, k: int = 10, batch: int = 64):
 def scan_bias(X, part: int = 1 << 24) -> torch.Tensor:
     """-|x|^2 / 2 of each row, rounded once to float32 (formed in float64, `part`
     values at a time): the bias of compressed_topk's products, kept beside the
-    4-bit rows.  X: the vectors, or their 4-bit rows (MXRows), whose own norms
-    give scores that order by the distance to the values they stand for."""
-    from .rows import MXRows, mx_dequantize
+    compressed rows.  X: the vectors, or their rows in 4 or 8 bits (MXRows,
+    ByteRows), whose own norms give scores that order by the distance to the
+    values they stand for."""
+    from .rows import ByteRows, MXRows, byte_dequantize, mx_dequantize
 
-    held = isinstance(X, MXRows)
+    held = isinstance(X, (MXRows, ByteRows))
+    dequantize = byte_dequantize if isinstance(X, ByteRows) else mx_dequantize
     if not held and (not isinstance(X, torch.Tensor) or X.dtype != torch.float32 or X.dim() != 2):
-        raise TypeError("X must be MXRows or a 2-D float32 tensor")
+        raise TypeError("X must be MXRows, ByteRows or a 2-D float32 tensor")
     n, dim = (len(X), X.dim) if held else X.shape
     bias = torch.empty(n, dtype=torch.float32, device=X.device)
     step = max(1, part // max(1, dim))
     for s in range(0, n, step):
         if held:
-            x = mx_dequantize(X[s:s + step])
+            x = dequantize(X[s:s + step])
         else:
             x = X[s:s + step].detach()
             _check_integral(x, "X")
@@ -110,15 +112,16 @@ def scan_bias(X, part: int = 1 << 24) -> torch.Tensor:
 def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortlist: int = 200, batch: int = 256,
                     bias: torch.Tensor | None = None):
     """Top-k as exact_topk (of integer-valued vectors, as there), among the
-    `shortlist` rows of X whose 4-bit copies (rows = mx_quantize(X)) score best
-    against the query: q.x - |x|^2 / 2 orders by distance, the product taken
-    from the 4-bit rows with the query rounded to 4 bits on the way, the norms
-    from X.  The shortlist is ranked by exact distances.
+    `shortlist` rows of X whose compressed copies (rows = mx_quantize(X) or
+    byte_quantize(X)) score best against the query: q.x - |x|^2 / 2 orders by
+    distance, the product taken from the compressed rows with the query rounded
+    in the same way, the norms from X.  The shortlist is ranked by exact
+    distances.
 
-    With a bias kept by the caller, a call reads 68 bytes for each 128 stored
-    values (and 4 a row) and the shortlisted rows of X, the only ones then
-    checked for integer values; without it, it forms scan_bias(X) first, from
-    512 bytes for each 128 values.
+    With a bias kept by the caller, a call reads 68 bytes (8 bits: 129 to 132)
+    for each 128 stored values (and 4 a row) and the shortlisted rows of X, the
+    only ones then checked for integer values; without it, it forms
+    scan_bias(X) first, from 512 bytes for each 128 values.
 
     How much of the exact result the shortlist holds goes by the bias and by
     the data: the error of a product is that of the 4-bit values times the
@@ -127,12 +130,16 @@ def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortli
     does a whole-numbered centre subtracted from Q and X, which changes no
     distance.  recall@10 of 500 queries among 10^6 rows of 128 values 0..255
     (shortlists of 200 and 1000): 0.25 and 0.98 with scan_bias(X), 0.49 and
-    1.00 with scan_bias(rows), 0.83 and 1.00 with the rows centred as well."""
-    from .rows import MXRows, mx_product
+    1.00 with scan_bias(rows), 0.83 and 1.00 with the rows centred as well.  8
+    bits lose less: of 10^6 rows of even random values 0..255, shortlists of 20
+    and 50 hold 0.96 and 1.00 with scan_bias(X) (4 bits: 0.20 and 0.30), 0.99 and
+    1.00 with scan_bias(rows) (4 bits: 0.51 and 0.71)."""
+    from .rows import ByteRows, MXRows, byte_product, mx_product
 
     _check_integral(Q, "Q")
-    if not isinstance(rows, MXRows):
-        raise TypeError("rows must be MXRows")
+    if not isinstance(rows, (MXRows, ByteRows)):
+        raise TypeError("rows must be MXRows or ByteRows")
+    product = byte_product if isinstance(rows, ByteRows) else mx_product
     if X.dtype != torch.float32 or X.dim() != 2:
         raise TypeError("X must be a 2-D float32 tensor")
     n, dim = X.shape
@@ -153,7 +160,7 @@ def compressed_topk(Q: torch.Tensor, rows, X: torch.Tensor, k: int = 10, shortli
     out_i, out_d = [], []
     for s in range(0, Q.shape[0], batch):
         q = Q[s:s + batch].detach()
-        cand = torch.topk(mx_product(q, rows, bias=bias), shortlist, dim=1, sorted=False).indices
+        cand = torch.topk(product(q, rows, bias=bias), shortlist, dim=1, sorted=False).indices
         x = X[cand].detach()
         if kept:
             _check_integral(x.flatten(0, 1), "X")

@@ -469,7 +469,9 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temp
     nothing has loss and gradient 0; an id of V or more, or logits without a
     distribution, make a row's loss and gradient NaN."""
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
-        return _Distill.apply(logits, ids, teacher, temperature)
+        if isinstance(teacher, torch.Tensor):
+            _no_gradient(teacher, "teacher")  # checked here: nothing requires gradients inside
+        return _Distill.apply(logits, ids, teacher, float(temperature))
     return _distill(_distill_args(logits, ids, teacher, temperature), logits.device, None)
 
 
@@ -483,6 +485,8 @@ def distill_grad(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     args = _distill_args(logits, ids, teacher, temperature)
     _no_gradient(logits, "logits")
     device = logits.device
+    if isinstance(weights, torch.Tensor):
+        _no_gradient(weights, "weights")
     w_ptr, w = _setting(weights, torch.float32, args[2], device, "weights")
     grad, ld_grad = _matrix(out, args[2], args[3], logits.dtype, device)
     if out is not None:
