@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(64 * WM* WN, 2)
 #pragma unroll
   for (int i = 0; i < OPS; ++i) {
     const int r = (w * OPS + i) * 8 + (lane >> 3);
-    voff[i] = (r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)lda : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldb) +
-              ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    voff[i] = (r < BM ? (unsigned)min(r, M - 1 - m0) * (unsigned)lda
+                      : (unsigned)min(r - BM, N - 1 - n0) * (unsigned)ldb) + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < SOPS; ++i) {
@@ -744,13 +744,16 @@ static void byte_one(const ByteProduct& p, int G, hipStream_t s) {
   constexpr int ROWS = kOneWaves * (8 / STEPS);
   const int64_t need = (p.N + ROWS - 1) / ROWS;
   hipLaunchKernelGGL((k_byte_one<AT, CT, STEPS>), dim3((unsigned)(need < (1 << 20) ? need : (1 << 20))),
-                     dim3(64 * kOneWaves), 0, s, p.A, p.as, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, p.bias, (typename Elem<CT>::T*)p.C);
+                     dim3(64 * kOneWaves), 0, s, p.A, p.as, p.B, p.ldb, p.bs, p.ldbs, (int)p.N, p.D, G, p.bias,
+                     (typename Elem<CT>::T*)p.C);
 }
 template <int AT, int MT, int CT>
 static void byte_few(const ByteProduct& p, int G, hipStream_t s) {
   if constexpr (MT == 1) {
     if (p.M == 1 && G >= kOneGroups)
-      return G <= 8 ? byte_one<AT, CT, 1>(p, G, s) : G <= 16 ? byte_one<AT, CT, 2>(p, G, s) : byte_one<AT, CT, 4>(p, G, s);
+      return G <= 8    ? byte_one<AT, CT, 1>(p, G, s)
+             : G <= 16 ? byte_one<AT, CT, 2>(p, G, s)
+                       : byte_one<AT, CT, 4>(p, G, s);
   }
   // One block of 16 B rows to a wave while that gives at most 512 workgroups (64 x
   // 8000 x 1024: 8.5 us against 11.4, 2 x 4096 x 4096 7.2 against 9.3); beyond, the

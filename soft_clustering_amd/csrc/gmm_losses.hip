@@ -242,7 +242,8 @@ __device__ __forceinline__ int group_of() {
 // dimensions, as one holds fewer than 2^32 threads.  A workgroup's number in it.
 constexpr int64_t kGridWidth = 1 << 21;
 dim3 row_grid(int64_t blocks) {
-  return blocks <= kGridWidth ? dim3((unsigned)blocks) : dim3((unsigned)kGridWidth, (unsigned)((blocks + kGridWidth - 1) / kGridWidth));
+  if (blocks <= kGridWidth) return dim3((unsigned)blocks);
+  return dim3((unsigned)kGridWidth, (unsigned)((blocks + kGridWidth - 1) / kGridWidth));
 }
 __device__ __forceinline__ int64_t block_in_grid() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
@@ -250,7 +251,9 @@ __device__ __forceinline__ int64_t block_in_grid() { return (int64_t)blockIdx.y 
 int64_t resident(int waves, int block) { return 256 * (int64_t)waves * 256 / block; }
 int64_t fewer(int64_t a, int64_t b) { return a < b ? a : b; }
 // Gradients that leave past the caches: those that the last of them cannot hold
-// (65536 x 1024 float32, loss and gradient by autograd: 148 us against 172).
+// (balance of 65536 x 1024 float32, by autograd: 151 us against 175; distillation of
+// 1024 x 131071 float32 in one pass 273 against 288, where rows are so long that
+// the listed places' second writing does not count).
 bool past_caches(int type, int64_t N, int V) { return N * V * (type == kFloat ? 4 : 2) >= (int64_t)256 << 20; }
 
 // ---------------------------------------------------------------------------
@@ -493,9 +496,9 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
     for (int q = 0; q < Q; ++q) {
       raw[q].put(e + q * VEC);
       if (NW > 1 && V < NT * E)  // a row's waves compare with the largest of each
-        raw[q].store_own(out, q * NT + t, V, a.stream);
+        raw[q].store_own(out, q * NT + t, V, false);
       else
-        raw[q].store(out + Vec<TYPE>::place(q * NT + t, V), a.stream);
+        raw[q].store(out + Vec<TYPE>::place(q * NT + t, V), false);
     }
     if constexpr (NW > 1)
       __syncthreads();
@@ -535,7 +538,8 @@ __device__ __forceinline__ void add_vectors(Part& p, const Vec<TYPE>* v, float c
   p = Part{x.m, p.s * x.factor(p.m) + s, 0.f};
 }
 
-// Longer rows, many: a workgroup to each.  HELD vectors of a thread are kept
+// Longer rows, many: a workgroup to each (loss and gradient of 2048 x 131071
+// bfloat16: 253 us, 4.2 TB/s of 1.07 GB; read twice: 327).  HELD vectors of a thread are kept
 // between the row's numbers and its gradient (16: 131072 16-bit elements, 65536
 // float32); what is behind them is read again.  As the gradient of a vector
 // leaves, the next row's comes in.  HELD is 0 where only one of the two is asked
@@ -562,7 +566,9 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
   if (lister) first.load(a, n, t);
   constexpr int STEP = 1024 * VEC;
   // a thread's vector q from base: one decision for all lanes, so that most places are a constant apart
-  const auto at = [&](auto* base, int q) { return base + ((q + 1) * STEP <= V ? q * STEP + t * VEC : W::place(q * 1024 + t, V)); };
+  const auto at = [&](auto* base, int q) {
+    return base + ((q + 1) * STEP <= V ? q * STEP + t * VEC : W::place(q * 1024 + t, V));
+  };
   W v[HELD ? HELD : 1];
 #pragma unroll
   for (int q = 0; q < HELD; ++q)
@@ -672,7 +678,8 @@ __global__ void __launch_bounds__(256) k_distill_parts(DistillArgs a, int range,
 }
 
 template <int TYPE, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(256) k_distill_finish(DistillArgs a, int range, int splits, const Part* __restrict__ in) {
+__global__ void __launch_bounds__(256)
+    k_distill_finish(DistillArgs a, int range, int splits, const Part* __restrict__ in) {
   using T = typename Elem<TYPE>::T;
   using W = Vec<TYPE>;
   constexpr int VEC = kVec<TYPE>;
@@ -802,9 +809,11 @@ __global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats)
   }
 }
 
-// Parts of a longer row: enough to fill the card, of at least 8192 elements, at most 64.
+// Parts of a longer row: enough to fill the card, of at least 8192 elements, at
+// most 64 (loss and gradient, bfloat16: 16 x 131071 in 9 us, whole rows 28; 128 x 131071
+// 25 and 32; 4 x 33000 8.0 and 8.8; 4 x 20000 7.9 and 7.2).
 int distill_splits(int64_t N, int V) {
-  if (V <= kHeldWidth || N >= 256) return 1;
+  if (V <= 2 * kHeldWidth || N >= 256) return 1;
   const int64_t most = fewer((V + 8191) / 8192, 64), want = (1024 + N - 1) / N;
   return (int)fewer(most, want);
 }
@@ -824,10 +833,12 @@ void distill_held(const DistillArgs& a, hipStream_t s) {
 
 template <int TYPE>
 hipError_t distill_long(const DistillArgs& a, void* workspace, hipStream_t s) {
-  const int splits = distill_splits(a.N, a.V);
+  // for the loss alone the second launch costs more (128 x 131071 float32: 16 us, whole rows 14)
+  const int splits = !a.grad && a.N >= 64 ? 1 : distill_splits(a.N, a.V);
   if (splits == 1) {
     const auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)fewer(a.N, resident(a.grad && a.losses ? 4 : 8, 1024))), dim3(1024), 0, s, a);
+      const int64_t grid = fewer(a.N, resident(a.grad && a.losses ? 4 : 8, 1024));
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(1024), 0, s, a);
     };
     const bool half = a.V <= 8 * 1024 * kVec<TYPE>;
     if (!a.grad)
@@ -854,20 +865,24 @@ hipError_t distill_long(const DistillArgs& a, void* workspace, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The least lanes that hold a row with 16 elements each: more of them would share
+// out the same loads among more reductions.  Of many 16-bit rows of up to 512
+// elements 16 lanes hold 32 each (loss and gradient of 65536 x 400: 37 us, by
+// waves 51; of 2000 x 300 5.7 against 4.8; float32 65536 x 512: 70 against 62).
+// Loss and gradient in one pass, of 65536 x 1024 bfloat16: 60 us, 4.5 TB/s (16 lanes
+// with 64 elements each: 69); float32: 105 us, 5.1 TB/s (the gradient past the caches,
+// whose listed places are then written a second time: 132).
 template <int TYPE>
 hipError_t distill_as(const DistillArgs& a, void* workspace, hipStream_t s) {
   if (a.V < kVec<TYPE>) {
-    hipLaunchKernelGGL(k_distill_tiny<TYPE>, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, a, a.losses != nullptr);
+    hipLaunchKernelGGL(k_distill_tiny<TYPE>, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, a,
+                       a.losses != nullptr);
     return hipGetLastError();
   }
-  const bool few = a.k <= 64;
+  const bool few = a.k <= 64;  // the lists of several rows in a workgroup's LDS
   if constexpr (TYPE != kFloat) {
-    if (a.V > 256 && a.V <= 1024 && few && a.N >= 8192) {
-      distill_held<TYPE, 16, 64, 256, 3>(a, s);
-      return hipGetLastError();
-    }
-    if (a.V > 4096 && a.V <= kHeldWidth && a.N >= 1024) {
-      distill_held<TYPE, 512, 32, 512, 4>(a, s);
+    if (a.V > 256 && a.V <= 512 && few && a.N >= 8192) {
+      distill_held<TYPE, 16, 32, 256, 5>(a, s);
       return hipGetLastError();
     }
   }
@@ -1103,7 +1118,8 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* 
   return d;
 }
 
-// As k_distill_held.
+// As k_distill_held.  Loss, counts and gradient of 65536 x 1024 float32: 105 us (of
+// which the rows 92), 5.1 TB/s; of 16384 x 16384 bfloat16: 229 us, 4.7 TB/s.
 template <int TYPE, int NT, int BLOCK, bool STATS, bool GRAD>
 __global__ void __launch_bounds__(BLOCK) k_balance_held(BalanceArgs a) {
   __shared__ Part parts[16];
@@ -1219,8 +1235,11 @@ __global__ void __launch_bounds__(256) k_balance_tiny(BalanceArgs a, bool stats)
   }
 }
 
-// A small batch in one workgroup: the counts, the rows, the loss.
-constexpr int kSmallWidth = 1024, kSmallIds = 8192, kSmallSize = 1 << 17;
+// A small batch in one workgroup: the counts, the rows, the loss; up to 4 rows to
+// each group of lanes.  What bounds it is the rows' latency, 1.5 us each: 256 x 64
+// in 12 us against 10.3 by four kernels, which cost the caller 26 us to launch and
+// this one 16; 2048 x 64 would take 65 us against 12.
+constexpr int kSmallWidth = 1024, kSmallIds = 8192, kSmallRows = 4;
 
 template <int TYPE, int NT, bool GRAD>
 __global__ void __launch_bounds__(1024) k_balance_small(BalanceArgs a) {
@@ -1316,7 +1335,7 @@ hipError_t balance_as(const BalanceArgs& a, void* workspace, hipStream_t s) {
     balance_rows<TYPE>(a, s);
     return hipGetLastError();
   }
-  if (a.K >= kVec<TYPE> && a.K <= kSmallWidth && a.N * a.k <= kSmallIds && a.N * a.K <= kSmallSize) {
+  if (a.K >= kVec<TYPE> && a.K <= kSmallWidth && a.N * a.k <= kSmallIds && a.N <= kSmallRows * (a.K <= 256 ? 64 : 16)) {
     const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, s, a); };
     if (a.K <= 256)
       a.grad ? launch(k_balance_small<TYPE, 16, true>) : launch(k_balance_small<TYPE, 16, false>);
@@ -1347,7 +1366,7 @@ size_t distill_workspace(int64_t N, int V, int k) {
 
 hipError_t launch_distill(const DistillArgs& given, void* workspace, hipStream_t s) {
   DistillArgs a = given;
-  a.stream = past_caches(a.type, a.N, a.V);
+  a.stream = a.V > kHeldWidth && a.losses && past_caches(a.type, a.N, a.V);
   if (a.type == kFloat) return distill_as<kFloat>(a, workspace, s);
   if (a.type == kBfloat) return distill_as<kBfloat>(a, workspace, s);
   return distill_as<kHalf>(a, workspace, s);

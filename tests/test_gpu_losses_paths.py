@@ -6,15 +6,16 @@ import torch
 
 import soft_clustering_amd as sc
 from tests import losses_reference as R
-from tests.test_gpu_losses import DEV, NAMES, TYPES, check_balance, check_distill, close, gen, lists, randn, rounding, taken
+from tests.test_gpu_losses import (DEV, NAMES, TYPES, check_balance, check_distill, close, gen, lists, randn, rounding,
+                                   taken)
 
 pytestmark = pytest.mark.gpu
 
 
-# by 16 lanes (also with 64 elements each: 8192 rows of 16-bit logits), a wave,
-# 4, 8 and 16 waves, held and not, divided
+# by 16 lanes (also with 32 elements each: 8192 rows of 16-bit logits), a wave, 4
+# and 16 waves, held and not, divided
 @pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
-@pytest.mark.parametrize("n,V,k", [(8200, 257, 3), (8193, 1023, 64), (9000, 1024, 1), (8192, 300, 65), (1030, 4097, 9),
+@pytest.mark.parametrize("n,V,k", [(8200, 257, 3), (8192, 512, 64), (8193, 511, 9), (8193, 1023, 64), (9000, 1024, 1), (8192, 300, 65), (1030, 4097, 9),
                                    (1024, 16383, 2), (1025, 8200, 200), (300, 16390, 5), (300, 65537, 20),
                                    (280, 131080, 12), (260, 200001, 4), (256, 65536, 1), (255, 65543, 3)])
 def test_distill_forms(n, V, k, dtype):
@@ -65,7 +66,8 @@ def test_distill_ids_that_share_bits(n, V, k):
     """Ids a power of two apart, some of them listed several times."""
     g = gen(n + V)
     z = randn(g, n, V)
-    ids = (torch.randint(0, 40, (n, k), generator=g, device=DEV) * 32768 + torch.randint(0, 60, (n, k), generator=g, device=DEV)) % V
+    far, near = (torch.randint(0, m, (n, k), generator=g, device=DEV) for m in (40, 60))
+    ids = (far * 32768 + near) % V
     ids[:, k // 2] = -1
     check_distill(z, ids, randn(g, n, k), 1.0, torch.ones(n, device=DEV))
 
