@@ -238,9 +238,11 @@ __device__ __forceinline__ void lds_dma4(unsigned off, const uint8_t* base, unsi
 // bfloat16 values.  Otherwise they are one operand of the 8-bit instruction.
 // 8192 x 8192 x 8192 to bfloat16: 435 us, 2.5 PFLOP/s; the same instructions on
 // such values from registers alone 306 us (they run slower the more bits change:
-// 234 us on zeros).  2048 x 50001 x 1024 to float32: 252 us, of which the
-// products alone are 165 (the bfloat16 instructions' rate on such values) and the
-// 410 MB of results, whose rows are no multiple of a cache line, 170 by themselves.
+// 234 us on zeros).  2048 x 50001 x 1000 to float32: 252 us; without the stores
+// 165 (the instructions alone 124, at their rate on such values: loads, conversions
+// and products of a wave stand in line), with one group instead of 8 127.  The
+// results' 410 MB leave from such tiles in 92 us by themselves; blocks of a compute
+// unit put out of step, and stores without the way through LDS, were no faster.
 template <int WM, int WN, int TM, int TN, bool EXACT, bool STREAM, int CT>
 __global__ void __launch_bounds__(64 * WM* WN, 2)
     k_byte_tile(const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ as, int64_t ldas, int M,
