@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats)
 // most 64 (loss and gradient, bfloat16: 16 x 131071 in 9 us, whole rows 28; 128 x 131071
 // 25 and 32; 4 x 33000 8.0 and 8.8; 4 x 20000 7.9 and 7.2).
 int distill_splits(int64_t N, int V) {
-  if (V <= 2 * kHeldWidth || N >= 256) return 1;
+  if (V <= 2 * kHeldWidth || N < 1 || N >= 256) return 1;
   const int64_t most = fewer((V + 8191) / 8192, 64), want = (1024 + N - 1) / N;
   return (int)fewer(most, want);
 }

@@ -269,3 +269,13 @@ def test_the_row_operators_together(n, K, D, dtype):
     close(step, got, bound, "gradient of the weights")
     after = sc.byte_quantize((means + 0.1 * randn(g, K, D)), out=held)
     assert after is held and not torch.equal(sc.byte_dequantize(held).double(), values)
+
+
+@pytest.mark.parametrize("V", [3, 40000, 2 ** 20])
+def test_no_rows_of_any_width(V):
+    z, ids = torch.empty(0, V, device=DEV), torch.empty(0, 3, dtype=torch.int64, device=DEV)
+    losses, grad = sc.distill_grad(z, ids, torch.empty(0, 3, device=DEV))
+    assert losses.shape == (0,) and grad.shape == (0, V)
+    assert sc.distill(z, ids, torch.empty(0, 3, device=DEV)).shape == (0,)
+    loss, counts, grad = sc.balance_grad(z, ids)
+    assert float(loss) == 0 and counts.shape == (V,) and not bool(counts.any()) and grad.shape == (0, V)

@@ -207,3 +207,13 @@ def test_references_against_autograd():
     got = R.balance(z.detach(), ids, 0.3)
     assert torch.allclose(got[0], loss.detach()) and torch.allclose(got[3], grad)
     assert torch.equal(got[2], counts.long())
+
+
+def test_workspace_of_no_rows():
+    """Of any width, none: also where rows would be divided."""
+    from soft_clustering_amd import rows
+
+    for width in (1, 1000, 16385, 40000, 131072, 2 ** 20):
+        assert rows._lib.gmm_distill_workspace(0, width, 5) == 0
+        assert rows._lib.gmm_balance_stats(0, width) >= width
+        assert rows._lib.gmm_balance_workspace(0, width, 5) > 0
