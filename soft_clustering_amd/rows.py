@@ -106,7 +106,7 @@ def _rows(t, name):
 
 def _no_gradient(t, name):
     """There is no backward: what would need one is refused."""
-    if t.requires_grad and torch.is_grad_enabled():
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires gradients, which this call does not compute (detach it, or use no_grad)")
 
 
@@ -426,6 +426,7 @@ def _distill_args(logits, ids, teacher, temperature):
     if (t_rows, t_k) != (N, k) or teacher.device != device:
         raise ValueError(f"teacher must be {N} x {k} on {device}, got {t_rows} x {t_k} on {teacher.device}")
     _no_gradient(teacher, "teacher")
+    _no_gradient(temperature, "temperature")
     return (logits.data_ptr(), code, N, V, ld, ids_ptr, bits, ld_ids, teacher.data_ptr(), t_code, ld_teacher, k,
             float(temperature))
 
@@ -469,8 +470,8 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temp
     nothing has loss and gradient 0; an id of V or more, or logits without a
     distribution, make a row's loss and gradient NaN."""
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
-        if isinstance(teacher, torch.Tensor):
-            _no_gradient(teacher, "teacher")  # checked here: nothing requires gradients inside
+        _no_gradient(teacher, "teacher")  # checked here: nothing requires gradients inside
+        _no_gradient(temperature, "temperature")
         return _Distill.apply(logits, ids, teacher, float(temperature))
     return _distill(_distill_args(logits, ids, teacher, temperature), logits.device, None)
 
@@ -485,8 +486,7 @@ def distill_grad(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     args = _distill_args(logits, ids, teacher, temperature)
     _no_gradient(logits, "logits")
     device = logits.device
-    if isinstance(weights, torch.Tensor):
-        _no_gradient(weights, "weights")
+    _no_gradient(weights, "weights")
     w_ptr, w = _setting(weights, torch.float32, args[2], device, "weights")
     grad, ld_grad = _matrix(out, args[2], args[3], logits.dtype, device)
     if out is not None:
@@ -545,6 +545,7 @@ def balance_grad(logits: torch.Tensor, ids: torch.Tensor, weight: float = 1.0, o
     weight * loss in the logits (in their type), in one pass over them."""
     _, N, K, _ = _rows(logits, "logits")
     _no_gradient(logits, "logits")
+    _no_gradient(weight, "weight")
     grad, ld_grad = _matrix(out, N, K, logits.dtype, logits.device)
     if out is not None:
         _apart(out, logits)

@@ -157,6 +157,13 @@ def test_gradients_that_are_not_computed_are_refused():
             sc.distill(logits, ids, teacher.clone().requires_grad_())
     with pytest.raises(ValueError, match="weights requires"):
         sc.distill_grad(z, ids, teacher, torch.ones(4, device=DEV, requires_grad=True))
+    warm = torch.tensor(2.0, requires_grad=True)
+    for call in (lambda: sc.distill(z, ids, teacher, warm), lambda: sc.distill(leaf, ids, teacher, warm),
+                 lambda: sc.distill_grad(z, ids, teacher, temperature=warm)):
+        with pytest.raises(ValueError, match="temperature requires"):
+            call()
+    with pytest.raises(ValueError, match="weight requires"):
+        sc.balance_grad(z, ids, warm)
     first, = torch.autograd.grad(sc.distill(leaf, ids, teacher).sum(), leaf, create_graph=True)
     with pytest.raises(RuntimeError):
         first.sum().backward()
