@@ -261,7 +261,9 @@ bool past_caches(int type, int64_t N, int V) { return N * V * (type == kFloat ? 
 
 constexpr int kHeldWidth = 16384;  // rows up to here are held by a workgroup at most
 constexpr int kList = 1024;       // teacher's logits of a row at most
-constexpr int kSeenBits = 32768;  // ids seen, by their low bits
+// ids seen, by their low bits (2048 x 131072 with 1024 listed: 362 us; with 32768 bits, of which 16 ids of a row find
+// another's, 584)
+constexpr int kSeenBits = 131072;
 
 // A row's list, in LDS, the business of LANES lanes.
 template <int LIST>
@@ -306,23 +308,42 @@ struct Place {
 
 // Puts the list of row n into LDS (`first`: the lane's first place of it, which
 // is there already); tm, bad: the largest teacher's logit, whether one has no
-// answer (an id out of range, a NaN or +inf), of this lane's.
-template <int TYPE, int LANES, int LIST>
+// answer (an id out of range, a NaN or +inf), of this lane's.  The loads of AT_ONCE
+// places of a lane go out together (4 for long rows: 2048 x 131072 with 1024 listed 668
+// -> 588 us; for held rows the registers would cost a workgroup on the compute unit).
+template <int TYPE, int LANES, int AT_ONCE, int LIST>
 __device__ __forceinline__ void read_list(const DistillArgs& a, int64_t n, const typename Elem<TYPE>::T* row, int t,
                                           Place first, Listed<LIST>& l, float& tm, bool& bad) {
   tm = -__builtin_inff();
   bad = false;
-  for (int j = t; j < a.k; j += LANES) {
-    Place p = first;
-    if (j >= LANES) p.load(a, n, j);
-    const int id = p.id(a);
-    const float x = id < 0 ? -__builtin_inff() : p.logit(a);
-    bad |= id >= a.V || !(x < __builtin_inff());
-    const bool listed = x > -__builtin_inff() && id < a.V;
-    l.id[j] = listed ? id : -1;
-    l.x[j] = x;
-    l.z[j] = listed ? Elem<TYPE>::get(row[id]) : 0.f;
-    tm = fmaxf(tm, x);
+  for (int j0 = t; j0 < a.k; j0 += AT_ONCE * LANES) {
+    Place p[AT_ONCE];
+    int id[AT_ONCE];
+    float x[AT_ONCE], z[AT_ONCE];
+    p[0] = first;
+    if (j0 >= LANES) p[0].load(a, n, j0);
+#pragma unroll
+    for (int i = 1; i < AT_ONCE; ++i)
+      if (j0 - t + i * LANES < a.k) p[i].load(a, n, j0 + i * LANES);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (i == 0 || j0 - t + i * LANES < a.k) {
+        id[i] = p[i].id(a);
+        x[i] = id[i] < 0 ? -__builtin_inff() : p[i].logit(a);
+        bad |= id[i] >= a.V || !(x[i] < __builtin_inff());
+        if (!(x[i] > -__builtin_inff() && id[i] < a.V)) id[i] = -1;
+        z[i] = Elem<TYPE>::get(row[max(id[i], 0)]);
+      }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int j = j0 + i * LANES;
+      if (j < a.k) {
+        l.id[j] = id[i];
+        l.x[j] = x[i];
+        l.z[j] = id[i] < 0 ? 0.f : z[i];
+        tm = fmaxf(tm, x[i]);
+      }
+    }
   }
 }
 // The teacher's sum of exponentials, and their exponents into the list: 0 where
@@ -360,8 +381,8 @@ __device__ __forceinline__ float list_loss(const DistillArgs& a, int t, const Ex
 // sum of its p.  `seen` has a bit for each id, by its low bits, all clear: an id
 // that finds its bit set may be listed twice, and the lanes look together for its
 // places, of which the first takes the sum (2048 rows of 131072 with 1024 listed,
-// some dozen of which share a bit or are listed twice: 721 us; every lane
-// looking through the list for its own: 8952 us).
+// of which some dozen shared a bit or were listed twice: 721 us, with every lane
+// looking through the list for its own 8952).
 template <int TYPE, int LANES, int LIST, int BITS>
 __device__ __forceinline__ void list_gradient(const DistillArgs& a, int t, const Exps& x, Listed<LIST>& l, float ts,
                                               float each, float by, typename Elem<TYPE>::T* out, unsigned* seen,
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(BLOCK, WAVES) k_distill_held(DistillArgs a) {
   const float c = kLog2e / a.temperature;
   float ts = 0.f, tm = 0.f;
   bool bad = false;
-  if (lister) read_list<TYPE, LANES>(a, n, row, t, first, l, tm, bad);
+  if (lister) read_list<TYPE, LANES, 1>(a, n, row, t, first, l, tm, bad);
   float e[E];
 #pragma unroll
   for (int q = 0; q < Q; ++q) raw[q].get(e + q * VEC);
@@ -557,8 +578,7 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
   const int V = a.V, vectors = (V + 1024 * VEC - 1) / (1024 * VEC);  // of a thread
   const bool lister = t < 64;
   if constexpr (GRAD) {
-    seen[t] = 0;
-    static_assert(kSeenBits / 32 == 1024, "a word for each thread");
+    for (int i = t; i < kSeenBits / 32; i += 1024) seen[i] = 0;
   }
   const float c = kLog2e / a.temperature;
   int64_t n = blockIdx.x;
@@ -582,7 +602,7 @@ __global__ void __launch_bounds__(1024, HELD ? 4 : 8) k_distill_wide(DistillArgs
     if (lister) {
       float tm;
       bool bad;
-      read_list<TYPE, 64>(a, n, row, t, first, l, tm, bad);
+      read_list<TYPE, 64, 4>(a, n, row, t, first, l, tm, bad);
       first.load(a, after, t);
       ts = list_sum<64>(a, t, c, l, tm, bad);
       if (t == 0) ts_[turn] = ts;
@@ -700,7 +720,7 @@ __global__ void __launch_bounds__(256)
     bool bad;
     Place first{};
     first.load(a, n, t);
-    read_list<TYPE, 64>(a, n, row, t, first, l, tm, bad);
+    read_list<TYPE, 64, 4>(a, n, row, t, first, l, tm, bad);
     ts = list_sum<64>(a, t, c, l, tm, bad);
     if (t == 0) ts_ = ts;
   }
