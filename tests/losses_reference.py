@@ -4,11 +4,16 @@ what float32 arithmetic as documented may lose (units of u = 2^-24).
 An exponential is exp2((z - m) c), c = log2(e) / T in float32: the difference,
 the product and c (a rounded constant divided) are off by u, u and 1.5 u of
 themselves, so the exponent X by 3.5 u X, the exponential by 3.5 ln2 u X + 2 u
-of itself (the exponential function: one unit in the last place).  Two or three
+of itself (the exponential function: one unit in the last place).  Formed as
+fma(z, c, -round(m c)) it is off by 1.5 u X for c and u X for its one rounding;
+the rounding of m c is the same for all that is compared with m.  Two or three
 such factors meet where parts of a row are joined; X is then the distance from
 the largest logit all the same.  A sum of V terms in threads and a tree has a
-depth of at most V / 64 + 16 roundings.  The exponential function gives 0 below
-2^-126, so a probability may be off by 2^-126 besides (the sum is at least 1)."""
+depth of at most V / 64 + 16 roundings (64 lanes and more hold V / 64 each, then 6
+to 14 levels; 16 lanes hold up to V / 16 of rows of up to 512, then 4 levels: 20 at
+V = 256, where the first is 20 as well, 36 at 512).  The exponential function
+gives 0 below 2^-126, so a probability may be off by 2^-126 besides (the sum is at
+least 1)."""
 import math
 
 import torch
@@ -17,7 +22,7 @@ U, TINY = 2.0 ** -24, 2.0 ** -126
 
 
 def depth(n):
-    return n / 64 + 16
+    return max(n / 64 + 16, min(n, 512) / 16 + 4)
 
 
 def softmax(x, m=None):
