@@ -81,12 +81,16 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
 }
-// Sum and maximum over a row of 16 lanes, in all of them.
+// Sum and maximum over a row of 16 lanes, in all of them.  The sum is the same
+// in each to the last bit, as what follows from it is written by several lanes:
+// every step adds two halves that exchange places (neighbours, pairs, then quads
+// and halves by their mirror images).  Rotations would not do: by a quad they
+// leave (q0 + q3) + (q2 + q1) in one and (q1 + q0) + (q3 + q2) in the next.
 __device__ __forceinline__ float row_sum(float x) {
-  x += dpp<0xB1>(x);  // neighbours, pairs, quads and halves
+  x += dpp<0xB1>(x);
   x += dpp<0x4E>(x);
-  x += dpp<0x124>(x);
-  x += dpp<0x128>(x);
+  x += dpp<0x141>(x);
+  x += dpp<0x140>(x);
   return x;
 }
 __device__ __forceinline__ float row_max(float x) {
