@@ -15,10 +15,13 @@
 // Exponentials are exp2(z c - m c), c = log2(e) / T, in one fused operation from
 // the rounded m c, with m the largest logit seen by the thread or wave, at least
 // the lowest finite float32: that rounding is the same for all that is compared
-// with m, and drops out.  Where m c is no finite number they are
-// exp2((z - m) c).  A logit of -inf gives 0, a row of nothing but the lowest
-// float its even weights, a row of nothing but -inf a sum of 0 and from there
-// NaN; what is below 2^-126 of the largest counts as 0.  Sums are float32 over
+// with m, and drops out, as long as it is no more than a part of a power of two.
+// So they are exp2((z - m) c) where |m c| is above 2^20 (a mask of -1e10 or the
+// lowest number in a whole stretch, a temperature of 1e-6): its rounding would
+// be the exponent of the largest term, up to 2^103.  The largest term is 1 there
+// and within 2^-5 powers of two of it in the fused form.  A logit of -inf gives
+// 0, a row of one number its even weights, a row of nothing but -inf a sum of 0
+// and from there NaN; what is below 2^-126 of the largest counts as 0.  Sums are float32 over
 // at most 2^20 terms in a fixed tree (a thread's share, its wave, the waves),
 // the sum over rows float64.
 #include "gmm_rows_device.h"
@@ -53,10 +56,11 @@ __device__ __forceinline__ float max_of(const float (&e)[E]) {
 }
 
 // Exponentials that are compared with m.
+constexpr float kFused = 0x1p20f;  // |m c| of the fused form at most: its rounding is 2^-5 at most
 struct Exps {
   float m, c, mc;
   bool wide;
-  __device__ __forceinline__ Exps(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), wide(!(fabsf(mc) <= FLT_MAX)) {}
+  __device__ __forceinline__ Exps(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), wide(!(fabsf(mc) <= kFused)) {}
   __device__ __forceinline__ float log2(float z) const { return wide ? (z - m) * c : fmaf(z, c, -mc); }
   __device__ __forceinline__ float of(float z) const { return exp2_of(log2(z)); }
   template <int E>
@@ -69,11 +73,16 @@ struct Exps {
       for (int i = 0; i < E; ++i) e[i] = exp2_of(fmaf(e[i], c, -mc));
     }
   }
-  // what takes exponentials compared with `from` to these (from <= m)
+  // What takes exponentials compared with `from` to these (from <= m).  Each was
+  // formed from its logit less what `from` was replaced by: its rounded product
+  // with c, or itself.
   __device__ __forceinline__ float factor(float from) const {
 #pragma clang fp contract(off)  // the difference of the two rounded products
     const float fc = from * c;
-    return wide || !(fabsf(fc) <= FLT_MAX) ? exp2_of((from - m) * c) : exp2_of(fc - mc);
+    const bool far = !(fabsf(fc) <= kFused);
+    float x = fc - mc;
+    if (wide || far) x = !far ? fmaf(-m, c, fc) : wide ? (from - m) * c : fmaf(from, c, -mc);
+    return exp2_of(x);
   }
 };
 
@@ -366,18 +375,32 @@ __device__ __forceinline__ float list_sum(const DistillArgs& a, int t, float c, 
   return lanes_sum<LANES>(ts);
 }
 
+// A loss T^2 ln2 sum p (log2 p - log2 q) is summed in units of h^2 powers of two,
+// a power of two itself, so that what it is made of stays in float32's range where
+// the loss does: a listed component may lie 3e38 below the largest logit, at any T.
+struct Gaps {
+  float h, unit;
+  __device__ __forceinline__ explicit Gaps(float c) : h(c >= 0.5f ? 0x1p40f : 0x1p8f), unit(c >= 0.5f ? 0x1p-80f : 0x1p-16f) {}
+  __device__ __forceinline__ float below(const Exps& x, float z) const {
+    const float c = x.c * unit;
+    return x.wide ? fmaf(z, 0.25f, x.m * -0.25f) * (4 * c) : fmaf(z, c, -x.mc * unit);
+  }
+  __device__ __forceinline__ float loss(float gap, float T) const { return T * kLn2 * h * gap * (T * h); }
+};
+
 // The loss of a row whose exponentials, compared with x.m, sum to s.
 template <int LANES, int LIST>
 __device__ __forceinline__ float list_loss(const DistillArgs& a, int t, const Exps& x, const Listed<LIST>& l, float ts,
                                            float s) {
-  const float lt = log2_of(ts), ls = log2_of(s);
+  const Gaps g(x.c);
+  const float lt = log2_of(ts) * g.unit, ls = log2_of(s) * g.unit;
   float gap = 0.f;
   for (int j = t; j < a.k; j += LANES) {
     const float y = l.x[j], w = exp2_of(y);
-    if (l.id[j] >= 0 && w != 0.f) gap += w * ((y - lt) - (x.log2(l.z[j]) - ls));
+    if (l.id[j] >= 0 && w != 0.f) gap += w * ((y * g.unit - lt) - (g.below(x, l.z[j]) - ls));
   }
   gap = lanes_sum<LANES>(gap);
-  return ts == 0.f ? 0.f : a.temperature * a.temperature * kLn2 * (gap / ts);
+  return ts == 0.f ? 0.f : g.loss(gap / ts, a.temperature);
 }
 
 // The gradient at the listed places from `low` to `high`, over what the row's
@@ -801,6 +824,7 @@ __global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats)
     tm = fmaxf(tm, y);
   }
   if (!(tm > -__builtin_inff())) tm = 0.f;
+  const Gaps g(x.c);
   float gap = 0.f;
   for (int j = 0; j < a.k; ++j) {
     float y;
@@ -811,7 +835,7 @@ __global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats)
     for (int i = 0; i < VEC; ++i)
       if (i == id) {
         p[i] += w;
-        if (w != 0.f) gap += w * (lp - x.log2(e[i]));
+        if (w != 0.f) gap += w * (lp * g.unit - g.below(x, e[i]));
       }
   }
   if (bad) ts = __builtin_nanf("");
@@ -819,7 +843,7 @@ __global__ void __launch_bounds__(256) k_distill_tiny(DistillArgs a, bool stats)
 #pragma unroll
   for (int i = 0; i < VEC; ++i) s += e[i];
   if (stats) {
-    const float loss = a.temperature * a.temperature * kLn2 * (gap / ts + (log2_of(s) - log2_of(ts)));
+    const float loss = g.loss(gap / ts + (log2_of(s) - log2_of(ts)) * g.unit, a.temperature);
     keep(a, n, m, s, ts == 0.f ? 0.f : loss);
   } else {
     s = a.stats[2 * n + 1];
