@@ -1147,15 +1147,15 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* 
   }
   if constexpr (GRAD) {
     const float each = loss_weight(a, scale) * inv * f;
-    if (inv == 0.f) {  // not counted
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] *= (w[i] - d) * each;
+    if (inv == 0.f) {  // not counted: whatever its logits and the loss's weight
 #pragma unroll
       for (int i = 0; i < E; ++i) e[i] = 0.f;
     }
     T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) e[q * VEC + i] *= (w[q * VEC + i] - d) * each;
       v[q].put(e + q * VEC);
       if (NW > 1 && K < NT * E)  // as k_distill_held
         v[q].store_own(out, q * NT + t, K, a.stream);
