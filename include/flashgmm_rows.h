@@ -202,10 +202,11 @@ gmm_status gmm_distill_backward(const void *logits, int32_t type, int64_t N, int
  *   counts[e] = c_e,
  *   loss     = K / (C R) sum over those rows of d_n, d_n = sum_e c_e p_ne
  *            = K sum_e (c_e / C) (mean of p_ne), 1 where all is even,
- *   gradient = w K / (C R) p_ne (c_e - d_n), 0 for the other rows.
+ *   gradient = w K / (C R) p_ne (c_e - d_n), 0 for the other rows, whatever
+ *              their logits and w.
  * The counts are constants of the gradient.  Without any id the loss is 0.  An
- * id of K or more makes the loss and the whole gradient NaN (it is in no
- * count); a row that is counted and holds a NaN or +inf, or nothing above -inf,
+ * id of K or more makes the loss and the whole gradient NaN, that of the other
+ * rows as well (it is in no count); a row that is counted and holds a NaN or +inf, or nothing above -inf,
  * makes the loss and its own gradient NaN.
  * gmm_balance writes counts (int64[K]), loss (float[1]), stats
  * (gmm_balance_stats floats, for gmm_balance_backward) and, where grad is not

@@ -1097,6 +1097,9 @@ __device__ __forceinline__ void keep(const BalanceArgs& a, int64_t n, float m, f
   a.stats[a.N + n] = inv;
   a.stats[2 * a.N + n] = d;
 }
+// The gradient of a row that is not counted, whatever its logits and the loss's
+// weight: 0, or NaN where an id is out of range (then the scale is NaN).
+__device__ __forceinline__ float not_counted(float scale) { return 0.f * scale; }
 __device__ __forceinline__ float loss_weight(const BalanceArgs& a, float scale) {
   return (a.weight_at ? *a.weight_at : a.weight) * scale;
 }
@@ -1149,9 +1152,9 @@ __device__ __forceinline__ float balance_row(const BalanceArgs& a, const float* 
     const float each = loss_weight(a, scale) * inv * f;
 #pragma unroll
     for (int i = 0; i < E; ++i) e[i] *= (w[i] - d) * each;
-    if (inv == 0.f) {  // not counted: whatever its logits and the loss's weight
+    if (inv == 0.f) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) e[i] = 0.f;
+      for (int i = 0; i < E; ++i) e[i] = not_counted(scale);
     }
     T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
 #pragma unroll
@@ -1222,7 +1225,7 @@ __global__ void __launch_bounds__(1024, 8) k_balance_long(BalanceArgs a) {
   }
   if constexpr (GRAD) {
     T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
-    const float each = loss_weight(a, cs[K]) * inv;
+    const float each = loss_weight(a, cs[K]) * inv, none = not_counted(cs[K]);
     const Exps x(m, c);
     for (int q = t; (q - t) * VEC < K; q += 1024) {
       W v;
@@ -1233,7 +1236,7 @@ __global__ void __launch_bounds__(1024, 8) k_balance_long(BalanceArgs a) {
       v.get(e);
       x.all(e);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = inv == 0.f ? 0.f : e[i] * ((w[i] - d) * each);
+      for (int i = 0; i < VEC; ++i) e[i] = inv == 0.f ? none : e[i] * ((w[i] - d) * each);
       v.put(e);
       v.store(out + at, a.stream);
     }
@@ -1276,10 +1279,10 @@ __global__ void __launch_bounds__(256) k_balance_tiny(BalanceArgs a, bool stats)
   }
   if (a.grad) {
     T* out = static_cast<T*>(a.grad) + n * a.ld_grad;
-    const float each = loss_weight(a, cs[a.K]) * inv;
+    const float each = loss_weight(a, cs[a.K]) * inv, none = not_counted(cs[a.K]);
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      if (i < a.K) out[i] = Elem<TYPE>::put(inv == 0.f ? 0.f : e[i] * ((w[i] - d) * each));
+      if (i < a.K) out[i] = Elem<TYPE>::put(inv == 0.f ? none : e[i] * ((w[i] - d) * each));
   }
 }
 

@@ -1,5 +1,6 @@
 """The balance's gradient in every form of its kernels: rows that take no component
-have gradient 0, whatever their logits and the loss's weight."""
+have gradient 0, whatever their logits and the loss's weight; an id out of range
+makes the whole gradient NaN, theirs included."""
 import pytest
 import torch
 
@@ -38,3 +39,17 @@ def test_rows_that_take_nothing(n, K, dtype):
     for weight in (INF, NAN):
         for way, grad in gradients(z, ids, weight):
             assert not bool(grad[:5].any()), (way, weight)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("n,K", FORMS)
+def test_an_id_out_of_range(n, K, dtype):
+    g = gen(K + 1)
+    z = (randn(g, n, K) * 2).to(dtype)
+    ids = taken(g, z, 2, True)
+    ids[:5] = -1
+    for bad in (K, 2 ** 31 - 1, 2 ** 40):
+        ids[n - 1, 1] = bad
+        for weight in (8.0, 0.0):
+            for way, grad in gradients(z, ids, weight):
+                assert bool(torch.isnan(grad).all()), (way, bad, weight)
