@@ -8,7 +8,8 @@ current stream of the tensors' device.  Outputs come from torch's allocator;
 the calls synchronise nothing and can be captured into a graph.  distill and
 balance are differentiable in the logits.  Nothing else has a backward: rows,
 products, results and teachers that require gradients are refused while
-gradients are on (a draw's ids are whole numbers and never have one).  A result
+gradients are on (a draw's ids are whole numbers and never have one), and so are
+tensors with a forward-mode tangent, logits included.  A result
 that is given (out) must not share memory with an input.
 """
 from __future__ import annotations
@@ -16,6 +17,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import GMM_OK, GMMError, raw_library
 
@@ -104,8 +106,18 @@ def _rows(t, name):
     return code, N, D, ld
 
 
+def _no_tangent(t, name):
+    """No call has a forward-mode derivative: a result without its tangent would
+    read as a derivative of zero."""
+    if forward_ad._current_level < 0:  # outside of any dual_level there are none (1 us less for a call)
+        return
+    if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a forward-mode tangent, for which there is no derivative here")
+
+
 def _no_gradient(t, name):
     """There is no backward: what would need one is refused."""
+    _no_tangent(t, name)
     if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires gradients, which this call does not compute (detach it, or use no_grad)")
 
@@ -425,6 +437,7 @@ def _distill_args(logits, ids, teacher, temperature):
     t_code, t_rows, t_k, ld_teacher = _rows(teacher, "teacher")
     if (t_rows, t_k) != (N, k) or teacher.device != device:
         raise ValueError(f"teacher must be {N} x {k} on {device}, got {t_rows} x {t_k} on {teacher.device}")
+    _no_tangent(logits, "logits")
     _no_gradient(teacher, "teacher")
     _no_gradient(temperature, "temperature")
     return (logits.data_ptr(), code, N, V, ld, ids_ptr, bits, ld_ids, teacher.data_ptr(), t_code, ld_teacher, k,
@@ -455,6 +468,7 @@ class _Distill(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, weights):
         logits, ids, teacher, stats = ctx.saved_tensors
+        _no_tangent(weights, "the losses' gradient")
         args = _distill_args(logits, ids, teacher, ctx.temperature)
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         _call(logits.device, _lib.gmm_distill_backward, *args, stats.data_ptr(), weights.data_ptr(),
@@ -470,6 +484,7 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temp
     nothing has loss and gradient 0; an id of V or more, or logits without a
     distribution, make a row's loss and gradient NaN."""
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        _no_tangent(logits, "logits")
         _no_gradient(teacher, "teacher")  # checked here: nothing requires gradients inside
         _no_gradient(temperature, "temperature")
         return _Distill.apply(logits, ids, teacher, float(temperature))
@@ -521,6 +536,7 @@ class _Balance(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, weight, _):
         logits, stats = ctx.saved_tensors
+        _no_tangent(weight, "the loss's gradient")
         code, N, K, ld = _rows(logits, "logits")
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         _call(logits.device, _lib.gmm_balance_backward, logits.data_ptr(), code, N, K, ld, stats.data_ptr(),
@@ -535,6 +551,7 @@ def balance(logits: torch.Tensor, ids: torch.Tensor):
     The loss is K sum_e (share of e in the counts) (mean softmax of e over the
     rows that take one), 1 where all is even.  Differentiable in the logits (the
     counts are constants).  An id of K or more makes loss and gradient NaN."""
+    _no_tangent(logits, "logits")
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         return _Balance.apply(logits, ids)
     return _balance(logits, ids)[:2]
