@@ -115,11 +115,12 @@ gmm_status gmm_byte_dequantize(const uint8_t *codes, int64_t ld_codes, const uin
 /* Products of rows: C[m, n] = sum_d A[m, d] B[n, d] + bias[n], B in 8 bits, as
  * gmm_mx_product: a_type GMM_TYPE_BYTE takes A's codes and scales, any other
  * rows of that type, quantised as by gmm_byte_quantize on the way (the results
- * are the same).  Products are summed in float32.  With float32 results each is
- * exact where it lies within float32's range; a value of A or B below 2^-130
- * counts to within 2^-134.  With 16-bit results a product may also lose what
- * lies below 2^-13 of the largest among the 8 products of its place (d / 8):
- * 1.4e-5 of the results of normal operands, before the rounding to 16 bits.
+ * are the same).  Products are summed in float32.  With float32 and float16
+ * results each is exact where it lies within float32's range; a value of A or B
+ * below 2^-130 counts to within 2^-134.  With bfloat16 results a product may also
+ * lose what lies below 2^-13 of the largest among the 8 products of its place
+ * (d / 8): 1.4e-5 of the results of normal operands, more of those that are small
+ * against their products, before the rounding to 16 bits.
  * Where the magnitudes of a result's products sum past float32's range, the
  * result may be infinite or NaN.  A block of scale 255 makes its
  * row's results NaN.  workspace: gmm_byte_product_workspace bytes, otherwise as

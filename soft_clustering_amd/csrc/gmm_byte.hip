@@ -195,11 +195,14 @@ hipError_t launch_byte_dequantize(const uint8_t* codes, int64_t ldc, const uint8
 // the sum (measured: relative error 1.4e-5 of the results of normal operands,
 // 2^-16 of the sum of magnitudes at the worst of 2000; by the rule above below
 // 7 * 2^-13 of the largest of each 8).  So
-//   float32 results take the operands as bfloat16, which holds every value of a
-//   row (4 significant bits, the scale applied in the conversion), on the
-//   bfloat16 instructions, whose sums are float32;
-//   16-bit results, rounded to 2^-9 or 2^-12 anyway, take the 8-bit
-//   instructions where the matrix unit is the bound (k_byte_tile).
+//   float32 and float16 results take the operands as bfloat16, which holds every
+//   value of a row (4 significant bits, the scale applied in the conversion), on
+//   the bfloat16 instructions, whose sums are float32.  (float16 rounds a number of
+//   a term's size by 2^-12 to 2^-11, less than may be cut; of 300 x 300 x 100 normal
+//   values 53 results were off by more than that and the sum's own roundings);
+//   bfloat16 results take the 8-bit instructions where the matrix unit is the bound
+//   (k_byte_tile): what is cut from 8 terms is below 7 * 2^-13 of the largest, which
+//   bfloat16 rounds by 2^-9 at most and the elements' 3 fraction bits by 2^-4.
 
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
@@ -234,7 +237,7 @@ __device__ __forceinline__ void lds_dma4(unsigned off, const uint8_t* base, unsi
 // Half h of a step takes chunks 4 h + 2 g and the next for lane half g: any
 // assignment serves as long as both sides share it.  Scale words come by DMA
 // for 4 steps at a time.
-// EXACT (float32 results): a half's 32 bytes become four operands of 8
+// EXACT (float32 and float16 results): a half's 32 bytes become four operands of 8
 // bfloat16 values.  Otherwise they are one operand of the 8-bit instruction.
 // 8192 x 8192 x 8192 to bfloat16: 435 us, 2.5 PFLOP/s; the same instructions on
 // such values from registers alone 306 us (they run slower the more bits change:
@@ -769,7 +772,7 @@ static void byte_few(const ByteProduct& p, int G, hipStream_t s) {
 template <int WM, int WN, int TM, int TN, int CT>
 static hipError_t byte_tiles(const ByteProduct& p, int G, hipStream_t s) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
-  constexpr bool EXACT = CT == kFloat;
+  constexpr bool EXACT = CT != kBfloat;
   const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
   if (tm * tn > (1 << 23)) return hipErrorInvalidValue;  // a result of over 2^37 elements
   const auto launch = [&](auto kernel) {
@@ -816,9 +819,10 @@ static hipError_t byte_product(const ByteProduct& p, int G, hipStream_t s) {
   }
   // Tiles of 256 read half as much, where they fill the card and A has rows for
   // more than half of them (8192 x 8192 x 8192 bfloat16: 439 us against 570; 100 x
-  // 131072 x 1024: 47 against 39).  Float32 results are bound by the instructions.
+  // 131072 x 1024: 47 against 39).  The others are bound by the instructions, and such
+  // tiles of them would spill registers (8192 x 8192 x 8192 to float16: 975 us).
   const int64_t cus = 256;
-  if constexpr (CT != kFloat) {
+  if constexpr (CT == kBfloat) {
     if (p.M > 128 && ((p.M + 255) / 256) * ((p.N + 255) / 256) >= cus) return byte_tiles<2, 4, 4, 2, CT>(p, G, s);
   }
   return byte_tiles<2, 2, 2, 2, CT>(p, G, s);
