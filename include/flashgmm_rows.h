@@ -117,7 +117,8 @@ gmm_status gmm_byte_dequantize(const uint8_t *codes, int64_t ld_codes, const uin
  * rows of that type, quantised as by gmm_byte_quantize on the way (the results
  * are the same).  Products are summed in float32.  With float32 and float16
  * results each is exact where it lies within float32's range; a value of A or B
- * below 2^-130 counts to within 2^-134.  With bfloat16 results a product may also
+ * below 2^-130 counts to within 2^-134, one of 2^128 or more (the largest float32
+ * numbers are rounded there) as infinite.  With bfloat16 results a product may also
  * lose what lies below 2^-13 of the largest among the 8 products of its place
  * (d / 8): 1.4e-5 of the results of normal operands, more of those that are small
  * against their products, before the rounding to 16 bits.
