@@ -278,7 +278,7 @@ bool past_caches(int type, int64_t N, int V) { return N * V * (type == kFloat ? 
 constexpr int kHeldWidth = 16384;  // rows up to here are held by a workgroup at most
 constexpr int kList = 1024;       // teacher's logits of a row at most
 // ids seen, by their low bits (2048 x 131072 with 1024 listed: 362 us; with 32768 bits, of which 16 ids of a row find
-// another's, 584)
+// another's, 584).  The test of ids that share a bit reads this line.
 constexpr int kSeenBits = 131072;
 
 // A row's list, in LDS, the business of LANES lanes.
