@@ -241,8 +241,8 @@ __device__ __forceinline__ void lds_dma4(unsigned off, const uint8_t* base, unsi
 // bfloat16 values.  Otherwise they are one operand of the 8-bit instruction.
 // 8192 x 8192 x 8192 to bfloat16: 435 us, 2.5 PFLOP/s; the same instructions on
 // such values from registers alone 306 us (they run slower the more bits change:
-// 234 us on zeros).  2048 x 50001 x 1000 to float32: 252 us; without the stores
-// 165 (the instructions alone 124, at their rate on such values: loads, conversions
+// 234 us on zeros).  1024 x 100003 x 768 to float32: 253 us, to float16 191;
+// 2048 x 50001 x 1000 to float32: 275 us; without the stores 165 (the instructions alone 124, at their rate on such values: loads, conversions
 // and products of a wave stand in line), with one group instead of 8 127.  The
 // results' 410 MB leave from such tiles in 92 us by themselves; blocks of a compute
 // unit put out of step, and stores without the way through LDS, were no faster.
